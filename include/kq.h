@@ -88,6 +88,7 @@ const char* kq_version(void);
 /* Reads and clears the device error word of the current device; synchronises the device.
  * Every wait inside a kernel is bounded: if one gives up, the kernel records bit 0 here,
  * skips the rest of its work (its output is then invalid) and returns instead of hanging.
+ * Bit 1: a paged-cache kernel met lengths, slots or page ids outside the bounds it was given.
  * Returns the bits (0 = nothing recorded) or KQ_ERR_CUDA if the word cannot be read. */
 int kq_device_errors(void);
 
@@ -348,6 +349,123 @@ int kq_decode_step_attn(const kq_decode_model* model, const kq_kv_cache* cache, 
  * Other arguments, results and errors as kq_decode_step. */
 #define KQ_DECODE_STATIC_SCRATCH_BYTES (4u << 20)
 int kq_decode_step_static(const kq_decode_model* model, const void* x, float* logits, int M, void* stream);
+
+/* ---- Paged 8-bit KV cache: pages, rotary positions, append, attention ----
+ * A serving step over requests of uneven length. kq_pages_plan gives each new token a slot in
+ * the requests' pages, kq_rope turns q and k by their positions, kq_kv8_append writes k and v
+ * into the slots as 8-bit codes, kq_attention_kv8 attends over the pages. (Kipp README lists a
+ * paged cache and a Q8_0 cache; it gives no layout, and a scale per 32 values there: here one
+ * scale per block of tokens and kv head.) New tokens are packed: request r's new_len[r] tokens
+ * stand at rows cu[r] .. cu[r+1]-1 of q, k, v, pos and slot, cu the exclusive prefix sums of
+ * new_len, at positions ctx_len[r], ctx_len[r] + 1, ... of the request. Lengths, tables and
+ * slots live in device memory and are read there, so a step with other lengths needs no host
+ * work and a captured step can be replayed. Nothing here uses atomics on results: outputs are
+ * the same in every run. */
+
+/* Bits of the pages calls' status word (0 = done). With any bit set nothing was handed out or
+ * taken back: the table, the free list and *n_free stand as they were, every slot is -1. */
+enum kq_pages_status {
+  KQ_PAGES_OUT_OF_PAGES = 1u, /* plan: the free list is too short; release: longer than its array */
+  KQ_PAGES_TABLE_FULL = 2u,   /* a request needs more than max_blocks pages */
+  KQ_PAGES_TOKENS_FULL = 4u,  /* more than T new tokens */
+  KQ_PAGES_BAD_ARG = 8u       /* a negative length, or *n_free outside 0..free_capacity */
+};
+enum { KQ_PAGES_MAX_REQUESTS = 4096 };
+
+/* Block tables and slot map of a step, from the requests' lengths.
+ *   ctx_len, new_len  B ints: cached tokens of request r, and its new ones (0 allowed)
+ *   page_size P       16, 32, 64 or 128
+ *   block_table       B x max_blocks ints: the first ceil(ctx/P) entries of a row hold its pages;
+ *                     the entries up to ceil((ctx+new)/P) are written
+ *   free_pages        free_capacity ints; the first *n_free are the free pages. Pages are taken
+ *                     from the end, for request 0 first
+ *   n_free, n_free_out  one word each, not the same (the next step reads this one's output)
+ *   cu                B+1 ints (output); pos, slot: T ints (output), T the tokens' capacity.
+ *                     slot = page * P + position % P. Rows past the last token get pos 0, slot -1
+ *   status            one word (output)
+ * max_blocks * P <= 2^30. One launch. Errors: KQ_ERR_ARG, KQ_ERR_CUDA. */
+int kq_pages_plan(const int* ctx_len, const int* new_len, int B, int page_size, int* block_table, int max_blocks,
+                  const int* free_pages, int free_capacity, const int* n_free, int* n_free_out, int* cu, int* pos,
+                  int* slot, int T, unsigned int* status, void* stream);
+/* Takes back the pages of the requests with done[r] != 0: the first ceil(len[r]/P) entries of
+ * their rows go onto the end of the free list, in order, and become -1. */
+int kq_pages_release(const int* len, const unsigned char* done, int B, int page_size, int* block_table, int max_blocks,
+                     int* free_pages, int free_capacity, const int* n_free, int* n_free_out, unsigned int* status,
+                     void* stream);
+
+/* Rotary positions of one or more axes, on q and k in one launch. Pair i < rot_dim/2 of a head
+ * turns by angle = pos[axis_i][t] * inv_freq[i]: (a, b) -> (a cos - b sin, b cos + a sin); pair i is
+ * elements (i, i + rot_dim/2), or (2i, 2i+1) with KQ_ROPE_ADJACENT. Elements from rot_dim on are
+ * copied. Angles are formed modulo a turn in 64-bit integers: no position is too large; the
+ * products and sums are fp32, rounded once to y_dtype.
+ *   q, k, q_out, k_out  T rows of n heads of head_dim, token strides in elements (views into a
+ *             fused qkv row are fine). A tensor with n = 0 heads may be NULL. In place: same
+ *             pointer, type and stride. Outputs must not overlap inputs otherwise
+ *   inv_freq  rot_dim/2 fp32 (device); pair_axis: rot_dim/2 bytes (device), the axis of each
+ *             pair, or NULL for axis 0 (an axis >= n_axes does not turn); pos: n_axes rows of T ints
+ *   flags     KQ_ROPE_INVERSE turns by the negative angles: the gradient (and inverse) of the call
+ *             without it
+ * Errors: KQ_ERR_ARG, KQ_ERR_UNSUPPORTED, KQ_ERR_CUDA. */
+enum kq_rope_flags { KQ_ROPE_ADJACENT = 1u, KQ_ROPE_INVERSE = 2u };
+int kq_rope(int x_dtype, int y_dtype, const void* q, long long q_stride, void* q_out, long long q_out_stride, int n_q,
+            const void* k, long long k_stride, void* k_out, long long k_out_stride, int n_k, int T, int head_dim,
+            int rot_dim, const float* inv_freq, const unsigned char* pair_axis, const int* pos, int n_axes,
+            unsigned flags, void* stream);
+
+/* One layer's cache (HOST struct of device pointers). k, v: n_pages x n_kv x (page_size * head_dim)
+ * int8 codes, 16-byte aligned; k_scale, v_scale: n_pages x n_kv fp32. A code c under scale s
+ * stands for (c + 1/2) s. Within a (page, kv head) token o = 16 b + p, dim d is at byte
+ *   k: 16 b head_dim + d/32*512 + (p/4*2 + p%2)*64 + d/4%4*16 + d/16%2*8 + p/2%2*4 + d%4
+ *   v: 16 b head_dim + d/32*512 + d%8*64 + p/4*16 + d/16%2*8 + d/8%2*4 + p%4
+ * (the order in which the attention's matrix operands take them). head_dim 64 or 128;
+ * n_pages * page_size < 2^31. Memory needs no initialisation. */
+typedef struct kq_kv8_cache {
+  void *k, *v;
+  float *k_scale, *v_scale;
+  int n_pages, page_size, n_kv, head_dim;
+} kq_kv8_cache;
+/* Bytes of k (and of v); 0 on invalid sizes. */
+size_t kq_kv8_bytes(int n_pages, int page_size, int n_kv, int head_dim);
+
+/* Quantizes T tokens' k and v (rows of n_kv heads, fp32 or bf16, 16-byte aligned, token strides
+ * in elements, multiples of 8) into their slots; slot -1 skips a token. Per (page, kv head), k and
+ * v apart: s = 2^(floor(log2 max|x|) - 6) over the page's tokens (0 if all are 0, at least 2^-126
+ * otherwise) and code floor(x / s), so a value is off by at most s/2 <= max|x| / 128. A token at
+ * page offset 0 starts its page afresh; tokens at later offsets keep what the page holds, and
+ * where they raise the scale by 2^n every code of the page is shifted right by n, which is what
+ * coding all of its tokens in one call gives: the cache does not depend on how tokens were
+ * grouped into calls. A page with a value that is not finite gets scale NaN (until offset 0 is
+ * written again). Scales do not shrink: overwriting a token (a rejected guess) keeps the page's.
+ * The tokens of one call that go to one page stand next to each other at ascending slots, as
+ * kq_pages_plan gives them; slots beyond the pages are skipped and set bit 1 of
+ * kq_device_errors(). Errors: KQ_ERR_ARG, KQ_ERR_UNSUPPORTED, KQ_ERR_CUDA. */
+int kq_kv8_append(const kq_kv8_cache* cache, int x_dtype, const void* k, long long k_stride, const void* v,
+                  long long v_stride, const int* slot, int T, void* stream);
+
+/* Attention of every request's new tokens over its pages (the new ones' k and v appended
+ * before). The token at position x sees positions 0..x of its request, or with a tree mask (windows
+ * of up to 32 new tokens) the ctx_len cached ones and new token j where bit j of its mask word is
+ * set. Query head hq reads kv head hq / (n_q / n_kv).
+ *   o = sum_p softmax_p(scale q.k_p) v_p over the visible positions (zeros if none).
+ *   q, o       T x (n_q * head_dim), fp32 or bf16 each, 16-byte aligned, token strides in elements
+ *              (multiples of 8). Rows past the last token are neither read nor written
+ *   block_table  B x max_blocks page ids; mask: NULL (causal) or T words (device)
+ *   max_new, max_len, total_len  upper bounds, known to the host, of a request's new tokens, of
+ *              ctx + new, and of the sum of ctx + new over the requests: they size the launches and
+ *              the workspace only. A request beyond them is not computed and sets bit 1 of
+ *              kq_device_errors(), as do page ids outside the cache (those rows come out NaN)
+ * Sums and softmax statistics are fp32; codes enter the tensor cores exactly. With fp32 output q
+ * and the weights are carried in 22 bits; with bf16 output in fp16 (11 bits). A row's bits depend
+ * on its own request, window and bounds-independent split only, never on the other requests.
+ * T <= 2^20, B <= KQ_KV8_MAX_REQUESTS, n_q / n_kv <= 64, max_len <= 2^28.
+ * workspace: kq_attention_kv8_workspace_size() bytes, 256-byte aligned. At most two launches.
+ * Errors: KQ_ERR_ARG, KQ_ERR_UNSUPPORTED, KQ_ERR_WORKSPACE, KQ_ERR_CUDA. */
+enum { KQ_KV8_MAX_REQUESTS = 4096 };
+size_t kq_attention_kv8_workspace_size(int B, long long total_len, int max_new, int n_q, int n_kv, int head_dim);
+int kq_attention_kv8(const kq_kv8_cache* cache, int q_dtype, const void* q, long long q_stride, int o_dtype, void* o,
+                     long long o_stride, int n_q, const int* ctx_len, const int* new_len, int B, int T, int max_new,
+                     int max_len, long long total_len, const int* block_table, int max_blocks, const unsigned int* mask,
+                     float scale, void* workspace, size_t ws_bytes, void* stream);
 
 #ifdef __cplusplus
 }

@@ -97,6 +97,21 @@ def load_library(path: str = LIB_PATH):
     L.kq_head_argmax_workspace_size.restype = SZ
     L.kq_head_argmax.argtypes = [P, P, I, P, I, I, I, P, P, P, P, SZ, ctypes.c_uint, P]
     L.kq_head_argmax.restype = I
+    LL, F, U = ctypes.c_longlong, ctypes.c_float, ctypes.c_uint
+    L.kq_pages_plan.argtypes = [P, P, I, I, P, I, P, I, P, P, P, P, P, I, P, P]
+    L.kq_pages_plan.restype = I
+    L.kq_pages_release.argtypes = [P, P, I, I, P, I, P, I, P, P, P, P]
+    L.kq_pages_release.restype = I
+    L.kq_rope.argtypes = [I, I, P, LL, P, LL, I, P, LL, P, LL, I, I, I, I, P, P, P, I, U, P]
+    L.kq_rope.restype = I
+    L.kq_kv8_bytes.argtypes = [I, I, I, I]
+    L.kq_kv8_bytes.restype = SZ
+    L.kq_kv8_append.argtypes = [P, I, P, LL, P, LL, P, I, P]
+    L.kq_kv8_append.restype = I
+    L.kq_attention_kv8_workspace_size.argtypes = [I, LL, I, I, I, I]
+    L.kq_attention_kv8_workspace_size.restype = SZ
+    L.kq_attention_kv8.argtypes = [P, I, P, LL, I, P, LL, I, P, P, I, I, I, I, LL, P, I, P, F, P, SZ, P]
+    L.kq_attention_kv8.restype = I
     _lib = L
     return L
 
@@ -250,7 +265,8 @@ def head_argmax(w_q8: torch.Tensor, shortlist: torch.Tensor | None, x: torch.Ten
 
 
 def device_errors() -> int:
-    """Read and clear the device error word (bit 0: a bounded in-kernel wait gave up)."""
+    """Read and clear the device error word (bit 0: a bounded in-kernel wait gave up; bit 1: a paged-cache
+    kernel met lengths, slots or page ids out of bounds)."""
     rc = lib().kq_device_errors()
     if rc < 0:
         _check(rc)
@@ -263,6 +279,191 @@ def quantize(fmt, w: torch.Tensor, out: torch.Tensor | None = None, stream=None)
     if out is None:
         out = torch.empty((N, row_bytes(fmt, K)), dtype=torch.uint8, device=w.device)
     _check(lib().kq_quantize(_fmt(fmt), w.data_ptr(), out.data_ptr(), N, K, _stream(stream)))
+    return out
+
+
+# ---- Paged 8-bit KV cache ----
+
+PAGES_OUT_OF_PAGES, PAGES_TABLE_FULL, PAGES_TOKENS_FULL, PAGES_BAD_ARG = 1, 2, 4, 8
+KQ_ROPE_ADJACENT, KQ_ROPE_INVERSE = 1, 2
+_DTYPES = {torch.float32: F32, torch.bfloat16: BF16}
+
+
+def _dtype(t) -> int:
+    try:
+        return _DTYPES[t]
+    except KeyError:
+        raise TypeError("tensors must be torch.bfloat16 or torch.float32") from None
+
+
+def _i32(name: str, t: torch.Tensor, *shape) -> int:
+    """The address of a contiguous int32 tensor of at least the given shape's size."""
+    n = 1
+    for d in shape:
+        n *= d
+    if t.dtype != torch.int32 or not t.is_contiguous() or t.numel() < n:
+        raise ValueError(f"{name} must be a contiguous int32 tensor of at least {n} elements")
+    return t.data_ptr()
+
+
+def _heads(name: str, t: torch.Tensor, heads: int | None = None, dim: int | None = None) -> int:
+    """The token stride of a (T, heads, dim) tensor whose heads stand next to each other."""
+    if t.dim() != 3 or (t.stride(2) != 1 and t.shape[2] > 1) or (t.stride(1) != t.shape[2] and t.shape[1] > 1):
+        raise ValueError(f"{name} must be (tokens, heads, head_dim) with contiguous heads")
+    if (heads is not None and t.shape[1] != heads) or (dim is not None and t.shape[2] != dim):
+        raise ValueError(f"{name} must have {heads} heads of {dim}")
+    return t.stride(0) if t.shape[0] > 1 else t.shape[1] * t.shape[2]
+
+
+class PagesPlan:
+    """Outputs of pages_plan (device tensors): cu [B+1], pos [T], slot [T], n_free [1], status [1]."""
+    __slots__ = ("cu", "pos", "slot", "n_free", "status")
+
+    def __init__(self, B: int, T: int, device="cuda"):
+        buf = torch.empty(B + 1 + 2 * T + 2, dtype=torch.int32, device=device)
+        self.cu, self.pos, self.slot, self.n_free, self.status = buf.split((B + 1, T, T, 1, 1))
+
+
+def pages_plan(ctx_len: torch.Tensor, new_len: torch.Tensor, block_table: torch.Tensor, free_pages: torch.Tensor,
+               n_free: torch.Tensor, page_size: int, T: int, out: PagesPlan | None = None, stream=None) -> PagesPlan:
+    """Slots of up to T new tokens and the block-table entries they need (kq_pages_plan). block_table
+    (B x max_blocks) is updated; n_free is read, the new count is in the result."""
+    B, width = block_table.shape
+    if out is None:
+        out = PagesPlan(B, T, block_table.device)
+    _check(lib().kq_pages_plan(_i32("ctx_len", ctx_len, B), _i32("new_len", new_len, B), B, page_size,
+                               _i32("block_table", block_table, B, width), width, _i32("free_pages", free_pages, 0),
+                               free_pages.numel(), _i32("n_free", n_free, 1), _i32("out.n_free", out.n_free, 1),
+                               _i32("out.cu", out.cu, B + 1), _i32("out.pos", out.pos, T), _i32("out.slot", out.slot, T),
+                               T, _i32("out.status", out.status, 1), _stream(stream)))
+    return out
+
+
+def pages_release(length: torch.Tensor, done: torch.Tensor, block_table: torch.Tensor, free_pages: torch.Tensor,
+                  n_free: torch.Tensor, n_free_out: torch.Tensor, page_size: int, status: torch.Tensor | None = None,
+                  stream=None) -> torch.Tensor:
+    """Give back the pages of the requests with done[r] (bool or uint8) set (kq_pages_release); returns status."""
+    B, width = block_table.shape
+    if done.dtype not in (torch.bool, torch.uint8) or not done.is_contiguous() or done.numel() < B:
+        raise ValueError("done must be a contiguous bool or uint8 tensor with one element per request")
+    if status is None:
+        status = torch.empty(1, dtype=torch.int32, device=block_table.device)
+    _check(lib().kq_pages_release(_i32("length", length, B), done.data_ptr(), B, page_size,
+                                  _i32("block_table", block_table, B, width), width, _i32("free_pages", free_pages, 0),
+                                  free_pages.numel(), _i32("n_free", n_free, 1), _i32("n_free_out", n_free_out, 1),
+                                  _i32("status", status, 1), _stream(stream)))
+    return status
+
+
+def rope(q: torch.Tensor | None, k: torch.Tensor | None, pos: torch.Tensor, inv_freq: torch.Tensor,
+         pair_axis: torch.Tensor | None = None, adjacent: bool = False, inverse: bool = False, out_dtype=None,
+         q_out: torch.Tensor | None = None, k_out: torch.Tensor | None = None, stream=None):
+    """Rotary positions on q and k (T, heads, head_dim; either may be None), through kq_rope. pos: int32 [T]
+    or [axes, T]; inv_freq: fp32, one per pair (rot_dim = 2 * its length); pair_axis: uint8, one per pair.
+    inverse=True is the gradient of the call without it. Returns (q_out, k_out)."""
+    ref = q if q is not None else k
+    if ref is None:
+        raise ValueError("one of q and k is needed")
+    T, D = ref.shape[0], ref.shape[2]
+    axes = pos.shape[0] if pos.dim() == 2 else 1
+    pairs = inv_freq.numel()
+    if pairs and (inv_freq.dtype != torch.float32 or not inv_freq.is_contiguous()):
+        raise ValueError("inv_freq must be contiguous fp32")
+    if pair_axis is not None and (pair_axis.dtype != torch.uint8 or not pair_axis.is_contiguous() or pair_axis.numel() != pairs):
+        raise ValueError("pair_axis must be contiguous uint8, one per pair")
+    args, outs, y_dtype = [], [], None
+    for name, x, y in (("q", q, q_out), ("k", k, k_out)):
+        if x is None:
+            args.append((None, 0, None, 0, 0))
+            outs.append(None)
+            continue
+        if x.dtype != ref.dtype or x.shape[0] != T or x.shape[2] != D:
+            raise ValueError("q and k must agree in type, tokens and head_dim")
+        if y is None:
+            y = torch.empty(x.shape, dtype=out_dtype or x.dtype, device=x.device)
+        elif y.shape != x.shape or (out_dtype is not None and y.dtype != out_dtype):
+            raise ValueError(f"{name}_out must have {name}'s shape and out_dtype")
+        if y_dtype is not None and y.dtype != y_dtype:
+            raise ValueError("q_out and k_out must have one type")
+        y_dtype = y.dtype
+        args.append((x.data_ptr(), _heads(name, x), y.data_ptr(), _heads(name + "_out", y), x.shape[1]))
+        outs.append(y)
+    flags = (KQ_ROPE_ADJACENT if adjacent else 0) | (KQ_ROPE_INVERSE if inverse else 0)
+    _check(lib().kq_rope(_dtype(ref.dtype), _dtype(y_dtype), *args[0], *args[1], T, D, 2 * pairs,
+                         inv_freq.data_ptr(), pair_axis.data_ptr() if pair_axis is not None else None,
+                         _i32("pos", pos, axes, T), axes, flags, _stream(stream)))
+    return outs[0], outs[1]
+
+
+class KV8CacheC(ctypes.Structure):
+    """Mirror of kq_kv8_cache (include/kq.h)."""
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("k_scale", ctypes.c_void_p),
+                ("v_scale", ctypes.c_void_p), ("n_pages", ctypes.c_int), ("page_size", ctypes.c_int),
+                ("n_kv", ctypes.c_int), ("head_dim", ctypes.c_int)]
+
+
+class KV8Cache:
+    """One layer's paged 8-bit KV cache: int8 codes k, v (n_pages x n_kv x page_size*head_dim) and fp32
+    scales k_scale, v_scale (n_pages x n_kv); layout in include/kq.h."""
+
+    def __init__(self, n_pages: int, page_size: int, n_kv: int, head_dim: int, device="cuda", k=None, v=None,
+                 k_scale=None, v_scale=None):
+        n = lib().kq_kv8_bytes(n_pages, page_size, n_kv, head_dim)
+        if n == 0 and n_pages != 0:
+            raise KQError(KQ_ERR_ARG, "bad sizes of a paged 8-bit cache")
+        shape = (n_pages, n_kv, page_size * head_dim)
+        self.k, self.v = (t if t is not None else torch.empty(shape, dtype=torch.int8, device=device) for t in (k, v))
+        self.k_scale, self.v_scale = (t if t is not None else torch.zeros(shape[:2], dtype=torch.float32, device=device)
+                                      for t in (k_scale, v_scale))
+        for t, dt, want in ((self.k, torch.int8, n), (self.v, torch.int8, n), (self.k_scale, torch.float32, n_pages * n_kv),
+                            (self.v_scale, torch.float32, n_pages * n_kv)):
+            if t.dtype != dt or not t.is_contiguous() or t.numel() != want:
+                raise ValueError("codes must be contiguous int8 and scales contiguous fp32 of the cache's sizes")
+        self.n_pages, self.page_size, self.n_kv, self.head_dim = n_pages, page_size, n_kv, head_dim
+        self.c = KV8CacheC(self.k.data_ptr(), self.v.data_ptr(), self.k_scale.data_ptr(), self.v_scale.data_ptr(),
+                           n_pages, page_size, n_kv, head_dim)
+        self._ref = ctypes.addressof(self.c)
+
+
+def kv8_append(cache: KV8Cache, k: torch.Tensor, v: torch.Tensor, slot: torch.Tensor, stream=None) -> None:
+    """Quantize k and v (T, n_kv, head_dim) into their slots (int32 [T], -1 skips) through kq_kv8_append."""
+    if k.dtype != v.dtype or k.shape[0] != v.shape[0]:
+        raise ValueError("k and v must agree in type and tokens")
+    T = k.shape[0]
+    _check(lib().kq_kv8_append(cache._ref, _dtype(k.dtype), k.data_ptr(), _heads("k", k, cache.n_kv, cache.head_dim),
+                               v.data_ptr(), _heads("v", v, cache.n_kv, cache.head_dim), _i32("slot", slot, T), T,
+                               _stream(stream)))
+
+
+def attention_kv8_workspace_size(B: int, total_len: int, max_new: int, n_q: int, n_kv: int, head_dim: int) -> int:
+    return lib().kq_attention_kv8_workspace_size(B, total_len, max_new, n_q, n_kv, head_dim)
+
+
+def attention_kv8(q: torch.Tensor, cache: KV8Cache, block_table: torch.Tensor, ctx_len: torch.Tensor,
+                  new_len: torch.Tensor, max_new: int, max_len: int, total_len: int | None = None,
+                  scale: float | None = None, mask: torch.Tensor | None = None, out: torch.Tensor | None = None,
+                  out_dtype=None, workspace: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """Attention of the packed new tokens' q (T, n_q, head_dim) over the requests' pages (kq_attention_kv8).
+    max_new, max_len, total_len (default B * max_len): bounds of new_len, of ctx_len + new_len and of its sum.
+    scale: default 1/sqrt(head_dim); mask: int32 [T] tree masks or None (causal). Returns (T, n_q, head_dim)."""
+    T, n_q, D = q.shape
+    B, width = block_table.shape
+    if total_len is None:
+        total_len = B * max_len
+    if out is None:
+        out = torch.empty((T, n_q, D), dtype=out_dtype or q.dtype, device=q.device)
+    elif out.shape != q.shape or (out_dtype is not None and out.dtype != out_dtype):
+        raise ValueError("out must have q's shape and out_dtype")
+    need = attention_kv8_workspace_size(B, total_len, max_new, n_q, cache.n_kv, D)
+    if workspace is None:
+        workspace = torch.empty(max(need, 256), dtype=torch.uint8, device=q.device)
+    _check(lib().kq_attention_kv8(cache._ref, _dtype(q.dtype), q.data_ptr(), _heads("q", q, None, cache.head_dim),
+                                  _dtype(out.dtype), out.data_ptr(), _heads("out", out, n_q, D), n_q,
+                                  _i32("ctx_len", ctx_len, B), _i32("new_len", new_len, B), B, T, max_new, max_len,
+                                  total_len, _i32("block_table", block_table, B, width), width,
+                                  _i32("mask", mask, T) if mask is not None else None,
+                                  D ** -0.5 if scale is None else scale, workspace.data_ptr(),
+                                  workspace.numel() * workspace.element_size(), _stream(stream)))
     return out
 
 

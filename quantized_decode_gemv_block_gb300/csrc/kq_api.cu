@@ -22,6 +22,16 @@ int ok() {
   return KQ_OK;
 }
 
+// Runs f, which may throw only for want of host memory; nothing passes the C boundary.
+template <typename F>
+int guarded(F f) {
+  try {
+    return f();
+  } catch (...) {
+    return KQ_ERR_CUDA;
+  }
+}
+
 bool fmt_known(int fmt) {
   return fmt == KQ_Q8_0 || fmt == KQ_Q4_K || fmt == KQ_AFFINE4_G32 || fmt == KQ_Q5_K || fmt == KQ_Q6_K;
 }
@@ -139,7 +149,9 @@ int kq_device_errors(void) {
   if (v == 0xFFFFFFFFu) return fail(KQ_ERR_CUDA, err);
   const unsigned int vt = kq::take_tc_errors();
   if (vt == 0xFFFFFFFFu) return fail(KQ_ERR_CUDA, "reading the prefill error word");
-  v |= vt;
+  const unsigned int vk = kq::take_kv8_errors(), va = kq::take_kv8_append_errors();
+  if (vk == 0xFFFFFFFFu || va == 0xFFFFFFFFu) return fail(KQ_ERR_CUDA, "reading the paged cache's error words");
+  v |= vt | vk | va;
   ok();
   return static_cast<int>(v & 0x7FFFFFFFu);
 }
@@ -499,6 +511,198 @@ int kq_decode_step_static(const kq_decode_model* model, const void* x, float* lo
                       static_cast<cudaStream_t>(stream), &err) != 0)
     return fail(KQ_ERR_CUDA, err);
   return ok();
+}
+
+// ---- Paged KV cache and rotary positions ----
+
+static bool dtype_known(int t) { return t == KQ_F32 || t == KQ_BF16; }
+static bool page_size_ok(int p) { return p == 16 || p == 32 || p == 64 || p == 128; }
+
+// Checks shared by plan and release.
+static int pages_check(int B, int page_size, int max_blocks, int free_capacity, const void* ctx, const void* table,
+                       const void* free_pages, const void* n_free, const void* n_free_out, const void* status) {
+  if (B < 0 || B > KQ_PAGES_MAX_REQUESTS) return fail(KQ_ERR_ARG, "B must be in 0.." + std::to_string(KQ_PAGES_MAX_REQUESTS));
+  if (!page_size_ok(page_size)) return fail(KQ_ERR_ARG, "page_size must be 16, 32, 64 or 128");
+  if (max_blocks < 0 || (long long)max_blocks * page_size > 0x40000000LL)
+    return fail(KQ_ERR_ARG, "max_blocks * page_size must be in 0..2^30");
+  if (free_capacity < 0) return fail(KQ_ERR_ARG, "free_capacity must be >= 0");
+  if (!n_free || !n_free_out || !status) return fail(KQ_ERR_ARG, "n_free, n_free_out or status is NULL");
+  if (n_free == n_free_out) return fail(KQ_ERR_ARG, "n_free and n_free_out must be two words");
+  if (B > 0 && (!ctx || (max_blocks > 0 && !table) || (free_capacity > 0 && !free_pages)))
+    return fail(KQ_ERR_ARG, "a length, table or free-list pointer is NULL");
+  if (!aligned(ctx, 4) || !aligned(table, 4) || !aligned(free_pages, 4) || !aligned(n_free, 4) || !aligned(n_free_out, 4) ||
+      !aligned(status, 4))
+    return fail(KQ_ERR_ARG, "arrays must be 4-byte aligned");
+  return KQ_OK;
+}
+
+int kq_pages_plan(const int* ctx_len, const int* new_len, int B, int page_size, int* block_table, int max_blocks,
+                  const int* free_pages, int free_capacity, const int* n_free, int* n_free_out, int* cu, int* pos,
+                  int* slot, int T, unsigned int* status, void* stream) {
+  return guarded([&] {
+    const int rc = pages_check(B, page_size, max_blocks, free_capacity, ctx_len, block_table, free_pages, n_free,
+                               n_free_out, status);
+    if (rc != KQ_OK) return rc;
+    if (T < 0) return fail(KQ_ERR_ARG, "T must be >= 0");
+    if (!cu || (B > 0 && !new_len) || (T > 0 && (!pos || !slot))) return fail(KQ_ERR_ARG, "new_len, cu, pos or slot is NULL");
+    if (!aligned(new_len, 4) || !aligned(cu, 4) || !aligned(pos, 4) || !aligned(slot, 4))
+      return fail(KQ_ERR_ARG, "arrays must be 4-byte aligned");
+    std::string err;
+    const int sms = sm_count(&err);
+    if (sms < 0) return fail(KQ_ERR_CUDA, err);
+    kq::PagesArgs a = {ctx_len, new_len, B, page_size, block_table, max_blocks, free_pages, free_capacity,
+                       n_free, n_free_out, cu, pos, slot, T, status};
+    if (kq::launch_pages_plan(a, sms, static_cast<cudaStream_t>(stream), &err) != 0) return fail(KQ_ERR_CUDA, err);
+    return ok();
+  });
+}
+
+int kq_pages_release(const int* len, const unsigned char* done, int B, int page_size, int* block_table, int max_blocks,
+                     int* free_pages, int free_capacity, const int* n_free, int* n_free_out, unsigned int* status,
+                     void* stream) {
+  return guarded([&] {
+    const int rc = pages_check(B, page_size, max_blocks, free_capacity, len, block_table, free_pages, n_free, n_free_out,
+                               status);
+    if (rc != KQ_OK) return rc;
+    if (B > 0 && !done) return fail(KQ_ERR_ARG, "done is NULL");
+    std::string err;
+    const int sms = sm_count(&err);
+    if (sms < 0) return fail(KQ_ERR_CUDA, err);
+    kq::PagesArgs a = {len, nullptr, B, page_size, block_table, max_blocks, free_pages, free_capacity,
+                       n_free, n_free_out, nullptr, nullptr, nullptr, 0, status};
+    if (kq::launch_pages_release(a, done, sms, static_cast<cudaStream_t>(stream), &err) != 0) return fail(KQ_ERR_CUDA, err);
+    return ok();
+  });
+}
+
+int kq_rope(int x_dtype, int y_dtype, const void* q, long long q_stride, void* q_out, long long q_out_stride, int n_q,
+            const void* k, long long k_stride, void* k_out, long long k_out_stride, int n_k, int T, int head_dim,
+            int rot_dim, const float* inv_freq, const unsigned char* pair_axis, const int* pos, int n_axes,
+            unsigned flags, void* stream) {
+  return guarded([&] {
+    if (!dtype_known(x_dtype) || !dtype_known(y_dtype)) return fail(KQ_ERR_UNSUPPORTED, "x_dtype and y_dtype must be KQ_F32 or KQ_BF16");
+    if (flags & ~(unsigned)(KQ_ROPE_ADJACENT | KQ_ROPE_INVERSE)) return fail(KQ_ERR_ARG, "unknown flag bits " + std::to_string(flags));
+    if (T < 0 || n_q < 0 || n_k < 0 || n_q > 65536 || n_k > 65536) return fail(KQ_ERR_ARG, "T, n_q or n_k out of range");
+    if (head_dim < 1 || head_dim > 4096 || rot_dim < 0 || rot_dim > head_dim || rot_dim % 2)
+      return fail(KQ_ERR_ARG, "head_dim must be in 1..4096 and rot_dim an even number up to it");
+    if (n_axes < 1 || n_axes > 255) return fail(KQ_ERR_ARG, "n_axes must be in 1..255");
+    const long long qw = (long long)n_q * head_dim, kw = (long long)n_k * head_dim;
+    if (q_stride < qw || q_out_stride < qw || k_stride < kw || k_out_stride < kw)
+      return fail(KQ_ERR_ARG, "a token stride is shorter than the token's heads");
+    if (T == 0 || n_q + n_k == 0) return ok();
+    if ((n_q && (!q || !q_out)) || (n_k && (!k || !k_out))) return fail(KQ_ERR_ARG, "q, q_out, k or k_out is NULL");
+    if (rot_dim && (!inv_freq || !pos)) return fail(KQ_ERR_ARG, "inv_freq or pos is NULL");
+    const uintptr_t xa = x_dtype == KQ_F32 ? 4 : 2, ya = y_dtype == KQ_F32 ? 4 : 2;
+    if ((n_q && (!aligned(q, xa) || !aligned(q_out, ya))) || (n_k && (!aligned(k, xa) || !aligned(k_out, ya))) ||
+        !aligned(inv_freq, 4) || !aligned(pos, 4))
+      return fail(KQ_ERR_ARG, "a pointer is not aligned to its element");
+    const bool qi = n_q && q == q_out, ki = n_k && k == k_out;
+    if ((qi && (x_dtype != y_dtype || q_stride != q_out_stride)) || (ki && (x_dtype != y_dtype || k_stride != k_out_stride)))
+      return fail(KQ_ERR_ARG, "in place needs the same type and stride on both sides");
+    std::string err;
+    const int sms = sm_count(&err);
+    if (sms < 0) return fail(KQ_ERR_CUDA, err);
+    kq::RopeArgs a = {x_dtype, y_dtype, n_q ? q : nullptr, n_k ? k : nullptr, n_q ? q_out : nullptr, n_k ? k_out : nullptr,
+                      n_q ? q_stride : 0, n_k ? k_stride : 0, n_q ? q_out_stride : 0, n_k ? k_out_stride : 0,
+                      n_q, n_k, T, head_dim, rot_dim, inv_freq, pair_axis, pos, n_axes,
+                      (flags & KQ_ROPE_ADJACENT) != 0, (flags & KQ_ROPE_INVERSE) != 0};
+    if (kq::launch_rope(a, sms, static_cast<cudaStream_t>(stream), &err) != 0) return fail(KQ_ERR_CUDA, err);
+    return ok();
+  });
+}
+
+static int kv8_check(const kq_kv8_cache* c, kq::KV8Args* a) {
+  if (!c) return fail(KQ_ERR_ARG, "cache is NULL");
+  if (!page_size_ok(c->page_size)) return fail(KQ_ERR_ARG, "page_size must be 16, 32, 64 or 128");
+  if (c->head_dim != 64 && c->head_dim != 128) return fail(KQ_ERR_ARG, "head_dim must be 64 or 128");
+  if (c->n_kv < 1 || c->n_kv > 4096) return fail(KQ_ERR_ARG, "n_kv must be in 1..4096");
+  if (c->n_pages < 0 || (long long)c->n_pages * c->page_size > 0x7FFFFFFFLL)
+    return fail(KQ_ERR_ARG, "n_pages * page_size must be in 0..2^31-1");
+  if (c->n_pages > 0) {
+    if (!c->k || !c->v || !c->k_scale || !c->v_scale) return fail(KQ_ERR_ARG, "a cache pointer is NULL");
+    if (!aligned(c->k, 16) || !aligned(c->v, 16) || !aligned(c->k_scale, 4) || !aligned(c->v_scale, 4))
+      return fail(KQ_ERR_ARG, "codes must be 16-byte and scales 4-byte aligned");
+  }
+  int l = 4;
+  while ((1 << l) < c->page_size) ++l;
+  *a = {static_cast<int8_t*>(c->k), static_cast<int8_t*>(c->v), c->k_scale, c->v_scale, c->n_pages, l, c->n_kv, c->head_dim};
+  return KQ_OK;
+}
+
+size_t kq_kv8_bytes(int n_pages, int page_size, int n_kv, int head_dim) {
+  if (n_pages < 0 || !page_size_ok(page_size) || n_kv < 1 || n_kv > 4096 || (head_dim != 64 && head_dim != 128) ||
+      (long long)n_pages * page_size > 0x7FFFFFFFLL)
+    return 0;
+  return (size_t)n_pages * n_kv * page_size * head_dim;
+}
+
+int kq_kv8_append(const kq_kv8_cache* cache, int x_dtype, const void* k, long long k_stride, const void* v,
+                  long long v_stride, const int* slot, int T, void* stream) {
+  return guarded([&] {
+    kq::KV8Args c;
+    const int rc = kv8_check(cache, &c);
+    if (rc != KQ_OK) return rc;
+    if (!dtype_known(x_dtype)) return fail(KQ_ERR_UNSUPPORTED, "x_dtype must be KQ_F32 or KQ_BF16");
+    if (T < 0) return fail(KQ_ERR_ARG, "T must be >= 0");
+    const long long w = (long long)c.n_kv * c.D;
+    if (k_stride < w || v_stride < w || k_stride % 8 || v_stride % 8)
+      return fail(KQ_ERR_ARG, "k_stride and v_stride must be multiples of 8 that hold a token's heads");
+    if (T == 0) return ok();
+    if (!k || !v || !slot) return fail(KQ_ERR_ARG, "k, v or slot is NULL");
+    if (!aligned(k, 16) || !aligned(v, 16) || !aligned(slot, 4))
+      return fail(KQ_ERR_ARG, "k and v must be 16-byte and slot 4-byte aligned");
+    std::string err;
+    const int sms = sm_count(&err);
+    if (sms < 0) return fail(KQ_ERR_CUDA, err);
+    if (kq::launch_kv8_append(c, x_dtype, k, k_stride, v, v_stride, slot, T, sms, static_cast<cudaStream_t>(stream), &err) != 0)
+      return fail(KQ_ERR_CUDA, err);
+    return ok();
+  });
+}
+
+static bool attention_kv8_sizes_ok(int B, long long total_len, int max_new, int n_q, int n_kv, int head_dim) {
+  return B >= 0 && B <= KQ_KV8_MAX_REQUESTS && total_len >= 0 && total_len <= 0x7FFFFFFFLL && max_new >= 0 && n_kv >= 1 &&
+         n_q >= n_kv && n_q % n_kv == 0 && n_q / n_kv <= 64 && n_kv <= 4096 && (head_dim == 64 || head_dim == 128);
+}
+
+size_t kq_attention_kv8_workspace_size(int B, long long total_len, int max_new, int n_q, int n_kv, int head_dim) {
+  if (!attention_kv8_sizes_ok(B, total_len, max_new, n_q, n_kv, head_dim)) return 0;
+  return kq::attention_kv8_workspace(B, total_len, max_new, n_q, n_kv, head_dim);
+}
+
+int kq_attention_kv8(const kq_kv8_cache* cache, int q_dtype, const void* q, long long q_stride, int o_dtype, void* o,
+                     long long o_stride, int n_q, const int* ctx_len, const int* new_len, int B, int T, int max_new,
+                     int max_len, long long total_len, const int* block_table, int max_blocks, const unsigned int* mask,
+                     float scale, void* workspace, size_t ws_bytes, void* stream) {
+  return guarded([&] {
+    kq::KV8Args c;
+    const int rc = kv8_check(cache, &c);
+    if (rc != KQ_OK) return rc;
+    if (!dtype_known(q_dtype) || !dtype_known(o_dtype)) return fail(KQ_ERR_UNSUPPORTED, "q_dtype and o_dtype must be KQ_F32 or KQ_BF16");
+    if (!attention_kv8_sizes_ok(B, total_len, max_new, n_q, c.n_kv, c.D))
+      return fail(KQ_ERR_ARG, "B, total_len, max_new or n_q out of range (n_q a multiple of n_kv, up to 64 times it)");
+    if (T < 0 || T > (1 << 20)) return fail(KQ_ERR_ARG, "T must be in 0..2^20");
+    if (max_len < 0 || max_len > (1 << 28)) return fail(KQ_ERR_ARG, "max_len must be in 0..2^28");
+    if (max_blocks < 0) return fail(KQ_ERR_ARG, "max_blocks must be >= 0");
+    if (mask && max_new > 32) return fail(KQ_ERR_ARG, "a tree mask takes windows of up to 32 tokens");
+    const long long wq = (long long)n_q * c.D;
+    if (q_stride < wq || o_stride < wq || q_stride % 8 || o_stride % 8)
+      return fail(KQ_ERR_ARG, "q_stride and o_stride must be multiples of 8 that hold a token's heads");
+    if (T == 0 || B == 0) return ok();
+    if (!q || !o || !ctx_len || !new_len || (max_blocks > 0 && !block_table)) return fail(KQ_ERR_ARG, "q, o, a length array or block_table is NULL");
+    if (!aligned(q, 16) || !aligned(o, 16) || !aligned(ctx_len, 4) || !aligned(new_len, 4) || !aligned(block_table, 4) || !aligned(mask, 4))
+      return fail(KQ_ERR_ARG, "q and o must be 16-byte and the int arrays 4-byte aligned");
+    const size_t need = kq::attention_kv8_workspace(B, total_len, max_new, n_q, c.n_kv, c.D);
+    if (need && (!workspace || ws_bytes < need || !aligned(workspace, 256)))
+      return fail(KQ_ERR_WORKSPACE, "workspace must be >= " + std::to_string(need) + " bytes, 256-byte aligned");
+    std::string err;
+    const int sms = sm_count(&err);
+    if (sms < 0) return fail(KQ_ERR_CUDA, err);
+    kq::AttnKV8Args a = {q_dtype, o_dtype, q, q_stride, o, o_stride, B, T, max_new, max_len, total_len, ctx_len, new_len,
+                         block_table, max_blocks, n_q, reinterpret_cast<const uint32_t*>(mask), scale, workspace};
+    if (kq::launch_attention_kv8(c, a, sms, static_cast<cudaStream_t>(stream), &err) != 0) return fail(KQ_ERR_CUDA, err);
+    return ok();
+  });
 }
 
 }  // extern "C"

@@ -112,6 +112,64 @@ int launch_head_select(const void* wq, const void* shortlist, bool x_bf16, const
                        int* token, float* score, unsigned int* scored, void* ws, bool all_rows, int num_sms,
                        cudaStream_t s, std::string* err);
 
+// Paged KV cache (pages.cu, kv8_append.cu, kv8_attention.cu) and rotary positions (rope.cu).
+struct PagesArgs {
+  const int *ctx, *fresh;
+  int B, page_size;
+  int* table;
+  int max_blocks;
+  const int* free_pages;
+  int free_cap;
+  const int* n_free;
+  int* n_free_out;
+  int *cu, *pos, *slot;
+  int T;
+  unsigned* status;
+};
+int launch_pages_plan(const PagesArgs& a, int num_sms, cudaStream_t s, std::string* err);
+int launch_pages_release(const PagesArgs& a, const unsigned char* done, int num_sms, cudaStream_t s, std::string* err);
+
+struct RopeArgs {
+  int x_dtype, y_dtype;
+  const void *x0, *x1;  // q, k: xs elements between tokens, heads D apart
+  void *y0, *y1;
+  long long xs0, xs1, ys0, ys1;
+  int h0, h1, T, D, rot_dim;
+  const float* freq;
+  const unsigned char* axis;
+  const int* pos;
+  int n_axes;
+  bool adjacent, inverse;
+};
+int launch_rope(const RopeArgs& a, int num_sms, cudaStream_t s, std::string* err);
+
+struct KV8Args {
+  int8_t *k, *v;
+  float *k_scale, *v_scale;
+  int n_pages, log2p, n_kv, D;
+};
+int launch_kv8_append(const KV8Args& c, int x_dtype, const void* k, long long ks, const void* v, long long vs,
+                      const int* slot, int T, int num_sms, cudaStream_t s, std::string* err);
+unsigned int take_kv8_append_errors();
+
+struct AttnKV8Args {
+  int q_dtype, o_dtype;
+  const void* q;
+  long long qs;
+  void* o;
+  long long os;
+  int B, T, max_new, max_len;
+  long long total_len;
+  const int *ctx, *fresh, *table;
+  int max_blocks, n_q;
+  const uint32_t* mask;
+  float scale;
+  void* ws;
+};
+size_t attention_kv8_workspace(int B, long long total_len, int max_new, int n_q, int n_kv, int D);
+int launch_attention_kv8(const KV8Args& c, const AttnKV8Args& a, int num_sms, cudaStream_t s, std::string* err);
+unsigned int take_kv8_errors();
+
 // GPU quantizers (fp64 arithmetic).
 int launch_quantize(int fmt, const float* w, void* blocks, int N, int K, cudaStream_t stream,
                     std::string* err);

@@ -1,0 +1,267 @@
+// Block tables and slot maps of a paged KV cache, from the requests' lengths, on the GPU.
+//
+// Request r holds have_r = ceil(ctx_r / P) pages and needs want_r = ceil((ctx_r + new_r) / P).
+// With first_r = sum of (want - have) over the requests before it, its j-th fresh page is the
+// (first_r + j)-th popped from the end of the free list; token t of the packed batch belongs to
+// the request with cu_r <= t < cu_(r+1), stands at ctx_r + t - cu_r and goes to slot
+// table[r][pos / P] * P + pos % P.
+//
+// Bound by latency: a decode step's plan moves a few KB. One launch: every CTA forms both prefix
+// sums over all requests itself (two coalesced reads of 4 bytes per request from L2, a scan in
+// shared memory), then takes its share of the fresh pages and of the tokens, each found by a
+// binary search in shared memory. Sharing one scan between CTAs would need a second launch or a
+// grid barrier, each dearer than the repeated scan. A token whose page is fresh takes its id from
+// the free list, not from the table entry that another CTA may be writing, so no CTA waits for
+// another. No atomics: the result is the same in every run.
+#include <climits>
+#include <cstdint>
+
+#include "kq.h"
+#include "kq_internal.h"
+#include "kq_launch.cuh"
+
+namespace kq {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kWarps = kThreads / 32;
+
+struct PagesParams {
+  const int* ctx;    // plan: cached length; release: held length
+  const int* fresh;  // plan: new tokens; release: null
+  const unsigned char* done;  // release only
+  int B, log2p;
+  int* table;
+  int max_blocks;
+  int* free_pages;
+  int free_cap;
+  const int* n_free;
+  int* n_free_out;
+  int *cu, *pos, *slot;
+  int T;
+  unsigned* status;
+};
+
+// Inclusive sums of (a, b) over the block's threads in thread order; every thread gets its own
+// sums and the totals. All threads call it; `sm` holds 2 * kWarps values.
+__device__ __forceinline__ void block_scan2(long long& a, long long& b, long long& ta, long long& tb, long long* sm) {
+  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long xa = __shfl_up_sync(~0u, a, o), xb = __shfl_up_sync(~0u, b, o);
+    if (lane >= o) {
+      a += xa;
+      b += xb;
+    }
+  }
+  __syncthreads();  // the previous call's readers are done
+  if (lane == 31) {
+    sm[w] = a;
+    sm[kWarps + w] = b;
+  }
+  __syncthreads();
+  long long pa = 0, pb = 0;
+  ta = tb = 0;
+#pragma unroll
+  for (int i = 0; i < kWarps; ++i) {
+    if (i < w) {
+      pa += sm[i];
+      pb += sm[kWarps + i];
+    }
+    ta += sm[i];
+    tb += sm[kWarps + i];
+  }
+  a += pa;
+  b += pb;
+}
+
+// Largest r with s[r] <= x (s ascending, s[0] = 0 <= x): the request of token or page x, with
+// empty requests passed over.
+__device__ __forceinline__ int find_request(const int* s, int B, int x) {
+  int lo = 0, hi = B;  // s[lo] <= x < s[hi]
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (s[mid] <= x) lo = mid;
+    else hi = mid;
+  }
+  return lo;
+}
+
+__global__ void __launch_bounds__(kThreads) pages_plan_kernel(const PagesParams p) {
+  extern __shared__ int sm_cu[];  // B + 1 token prefixes, then B + 1 fresh-page prefixes
+  __shared__ long long sm_scan[2 * kWarps];
+  int* sm_pg = sm_cu + p.B + 1;
+  const int tid = threadIdx.x, P1 = (1 << p.log2p) - 1;
+  grid_dependency_wait();
+  const int nfree = *p.n_free;
+  unsigned bad = nfree < 0 || nfree > p.free_cap ? KQ_PAGES_BAD_ARG : 0u;
+  long long ct = 0, cp = 0;  // totals of the requests before this round of the loop
+  for (int base = 0; base < p.B; base += kThreads) {
+    const int r = base + tid;
+    long long a = 0, b = 0;
+    if (r < p.B) {
+      const int c = p.ctx[r], n = p.fresh[r];
+      if (c < 0 || n < 0) bad |= KQ_PAGES_BAD_ARG;
+      else {
+        const long long want = ((long long)c + n + P1) >> p.log2p;
+        if (want > p.max_blocks) bad |= KQ_PAGES_TABLE_FULL;
+        a = n;
+        b = want - (((long long)c + P1) >> p.log2p);
+      }
+    }
+    long long ta, tb, ia = a, ib = b;
+    block_scan2(ia, ib, ta, tb, sm_scan);
+    if (r < p.B) {  // clamped: a batch that overflows an int is refused below
+      sm_cu[r] = (int)min(ct + ia - a, (long long)INT_MAX);
+      sm_pg[r] = (int)min(cp + ib - b, (long long)INT_MAX);
+    }
+    ct += ta;
+    cp += tb;
+  }
+  if (tid == 0) {
+    sm_cu[p.B] = (int)min(ct, (long long)INT_MAX);
+    sm_pg[p.B] = (int)min(cp, (long long)INT_MAX);
+  }
+  if (ct > p.T) bad |= KQ_PAGES_TOKENS_FULL;
+  if (cp > nfree) bad |= KQ_PAGES_OUT_OF_PAGES;
+  bad = __syncthreads_or((int)bad) ? 0x80000000u | bad : 0u;
+  if (blockIdx.x == 0) {
+    __shared__ unsigned sm_bad;
+    if (tid == 0) sm_bad = 0;
+    __syncthreads();
+    if (bad & 0x7FFFFFFFu) atomicOr(&sm_bad, bad & 0x7FFFFFFFu);
+    __syncthreads();
+    if (tid == 0) {
+      *p.status = sm_bad;
+      *p.n_free_out = bad ? nfree : nfree - (int)cp;
+    }
+    for (int r = tid; r <= p.B; r += kThreads) p.cu[r] = bad ? 0 : sm_cu[r];
+  }
+  const int stride = gridDim.x * kThreads, first = blockIdx.x * kThreads + tid;
+  if (bad) {  // nothing is handed out: every token is skipped by what follows, the table stays
+    for (int t = first; t < p.T; t += stride) {
+      p.pos[t] = 0;
+      p.slot[t] = -1;
+    }
+    return;
+  }
+  const int nt = (int)ct, np = (int)cp;
+  for (int j = first; j < np; j += stride) {
+    const int r = find_request(sm_pg, p.B, j);
+    const int blk = (int)(((long long)p.ctx[r] + P1) >> p.log2p) + j - sm_pg[r];
+    p.table[(long long)r * p.max_blocks + blk] = p.free_pages[nfree - 1 - j];
+  }
+  for (int t = first; t < p.T; t += stride) {
+    int pos = 0, slot = -1;
+    if (t < nt) {
+      const int r = find_request(sm_cu, p.B, t), c = p.ctx[r];
+      pos = c + t - sm_cu[r];
+      const int blk = pos >> p.log2p, held = (int)(((long long)c + P1) >> p.log2p);
+      const int page = blk < held ? p.table[(long long)r * p.max_blocks + blk]
+                                  : p.free_pages[nfree - 1 - (sm_pg[r] + blk - held)];
+      // a negative entry of the caller's table, or one whose slots pass an int, is no slot
+      slot = page < 0 || page > (INT_MAX >> p.log2p) - 1 ? -1 : (page << p.log2p) + (pos & P1);
+    }
+    p.pos[t] = pos;
+    p.slot[t] = slot;
+  }
+}
+
+// The pages of the requests marked done go back on the free list in request order.
+__global__ void __launch_bounds__(kThreads) pages_release_kernel(const PagesParams p) {
+  extern __shared__ int sm_pg[];  // B + 1 prefixes
+  __shared__ long long sm_scan[2 * kWarps];
+  const int tid = threadIdx.x, P1 = (1 << p.log2p) - 1;
+  grid_dependency_wait();
+  const int nfree = *p.n_free;
+  unsigned bad = nfree < 0 || nfree > p.free_cap ? KQ_PAGES_BAD_ARG : 0u;
+  long long cp = 0;
+  for (int base = 0; base < p.B; base += kThreads) {
+    const int r = base + tid;
+    long long b = 0, z = 0, tz, tb;
+    if (r < p.B && p.done[r]) {
+      const int c = p.ctx[r];
+      b = ((long long)c + P1) >> p.log2p;
+      if (c < 0) bad |= KQ_PAGES_BAD_ARG, b = 0;
+      else if (b > p.max_blocks) bad |= KQ_PAGES_TABLE_FULL;
+    }
+    long long ib = b;
+    block_scan2(z, ib, tz, tb, sm_scan);
+    if (r < p.B) sm_pg[r] = (int)min(cp + ib - b, (long long)INT_MAX);
+    cp += tb;
+  }
+  if (tid == 0) sm_pg[p.B] = (int)min(cp, (long long)INT_MAX);
+  if (cp + nfree > p.free_cap) bad |= KQ_PAGES_OUT_OF_PAGES;
+  bad = __syncthreads_or((int)bad) ? 0x80000000u | bad : 0u;
+  if (blockIdx.x == 0) {
+    __shared__ unsigned sm_bad;
+    if (tid == 0) sm_bad = 0;
+    __syncthreads();
+    if (bad & 0x7FFFFFFFu) atomicOr(&sm_bad, bad & 0x7FFFFFFFu);
+    __syncthreads();
+    if (tid == 0) {
+      *p.status = sm_bad;
+      *p.n_free_out = bad ? nfree : nfree + (int)cp;
+    }
+  }
+  if (bad) return;
+  for (int j = blockIdx.x * kThreads + tid; j < (int)cp; j += gridDim.x * kThreads) {
+    const int r = find_request(sm_pg, p.B, j);
+    int* e = p.table + (long long)r * p.max_blocks + (j - sm_pg[r]);
+    p.free_pages[nfree + j] = *e;
+    *e = -1;
+  }
+}
+
+int log2_of(int v) {
+  int l = 0;
+  while ((1 << l) < v) ++l;
+  return l;
+}
+
+}  // namespace
+
+int launch_pages_plan(const PagesArgs& a, int num_sms, cudaStream_t s, std::string* err) {
+  PagesParams p = {};
+  p.ctx = a.ctx;
+  p.fresh = a.fresh;
+  p.B = a.B;
+  p.log2p = log2_of(a.page_size);
+  p.table = a.table;
+  p.max_blocks = a.max_blocks;
+  p.free_pages = const_cast<int*>(a.free_pages);
+  p.free_cap = a.free_cap;
+  p.n_free = a.n_free;
+  p.n_free_out = a.n_free_out;
+  p.cu = a.cu;
+  p.pos = a.pos;
+  p.slot = a.slot;
+  p.T = a.T;
+  p.status = a.status;
+  const size_t smem = (size_t)2 * (a.B + 1) * sizeof(int);
+  // one token per thread up to one CTA per SM; beyond it a CTA's share grows, as each CTA scans all requests
+  const long long want = ((long long)a.T + kThreads - 1) / kThreads;
+  const int grid = (int)(want < 1 ? 1 : want > num_sms ? num_sms : want);
+  return launch_pdl(pages_plan_kernel, dim3(grid), dim3(kThreads), smem, s, p, "pages_plan", err);
+}
+
+int launch_pages_release(const PagesArgs& a, const unsigned char* done, int num_sms, cudaStream_t s, std::string* err) {
+  PagesParams p = {};
+  p.ctx = a.ctx;
+  p.done = done;
+  p.B = a.B;
+  p.log2p = log2_of(a.page_size);
+  p.table = a.table;
+  p.max_blocks = a.max_blocks;
+  p.free_pages = const_cast<int*>(a.free_pages);
+  p.free_cap = a.free_cap;
+  p.n_free = a.n_free;
+  p.n_free_out = a.n_free_out;
+  p.status = a.status;
+  const size_t smem = (size_t)(a.B + 1) * sizeof(int);
+  const long long want = ((long long)a.free_cap + 4 * kThreads - 1) / (4 * kThreads);
+  const int grid = (int)(want < 1 ? 1 : want > num_sms ? num_sms : want);
+  return launch_pdl(pages_release_kernel, dim3(grid), dim3(kThreads), smem, s, p, "pages_release", err);
+}
+
+}  // namespace kq

@@ -1,0 +1,249 @@
+// Rotary positions with one or more position axes (one for text; time, height and width for
+// images and video), on q and k in one launch.
+//
+// Pair i of a head, (a, b), turns by the angle pos[axis_i][t] * freq_i:
+//     a' = a cos - b sin,  b' = b cos + a sin;
+// the inverse rotation (the gradient of the forward one) turns by the negative angle.
+//
+// The angle is formed as a binary fraction of a turn in 64-bit integers, so that positions of any
+// size lose nothing: freq = m 2^e (24-bit m) gives F = m C 2^(e-2), C = round(2^64 * 2/pi), the
+// turn fraction per position in units of 2^-64 (error below one unit for freq <= 1); pos * F
+// modulo 2^64 is the phase, exact but for pos units. Its top 32 bits are cut into the nearest
+// quarter turn and a rest in [-1/8, 1/8] turn, whose sine and cosine come from sincospif.
+//
+// Bound by DRAM: q and k are read and written once; the angles cost about 8 * 70 instructions
+// for eight pairs of a token. A thread takes eight pairs of one token (16-byte accesses for bf16)
+// and turns them in several heads, so the angles are formed once for those heads.
+#include <cuda_bf16.h>
+
+#include <cstdint>
+
+#include "kq.h"
+#include "kq_device.cuh"
+#include "kq_internal.h"
+#include "kq_launch.cuh"
+
+namespace kq {
+namespace {
+
+constexpr int kThreads = 256;
+
+struct RopeParams {
+  const void *x0, *x1;  // q rows, k rows
+  void *y0, *y1;
+  long long xs0, xs1, ys0, ys1;  // elements between tokens
+  int h0, h1;                    // heads
+  int T, D, pairs;
+  const float* freq;
+  const unsigned char* axis;  // null: axis 0
+  const int* pos;             // n_axes rows of T
+  int n_axes;
+  int inverse;
+  int chunks;       // vector chunks of a head: pairs / V turned, then the copied rest
+  int head_groups;  // threads that share a (token, chunk)
+};
+
+// Turn fraction per position of `freq` in units of 2^-64 (two's complement for freq < 0).
+__device__ __forceinline__ unsigned long long turn_per_position(float freq) {
+  const unsigned b = __float_as_uint(freq);
+  const int ex = (b >> 23) & 0xFF;
+  const unsigned long long m = ex ? (b & 0x7FFFFFu) | 0x800000u : b & 0x7FFFFFu;
+  const int sh = (ex ? ex : 1) - 150 - 2;  // freq = m 2^(ex - 150)
+  constexpr unsigned long long C = 0xA2F9836E4E44152Aull;  // round(2^64 * 2 / pi)
+  const unsigned long long lo = m * C, hi = __umul64hi(m, C);
+  unsigned long long f;
+  if (sh >= 64) f = 0;
+  else if (sh >= 0) f = lo << sh;
+  else if (sh > -64) f = (lo >> -sh) | (hi << (64 + sh));
+  else if (sh > -128) f = hi >> (-sh - 64);
+  else f = 0;
+  return b >> 31 ? 0ull - f : f;
+}
+
+__device__ __forceinline__ float2 cos_sin_turn(unsigned long long turn, int pos) {
+  const int ph = (int)((turn * (unsigned long long)(long long)pos) >> 32);
+  const int quarter = (int)((unsigned)ph + 0x20000000u) >> 30;
+  const int rest = (int)((unsigned)ph - ((unsigned)quarter << 30));
+  float s, c;
+  sincospif((float)rest * 4.656612873077393e-10f, &s, &c);  // rest 2^-31 half turns
+  const float cc = quarter & 1 ? s : c, ss = quarter & 1 ? c : s;
+  return make_float2((quarter + 1) & 2 ? -cc : cc, quarter & 2 ? -ss : ss);
+}
+
+template <int V>
+__device__ __forceinline__ void load(float (&v)[V], const float* p) {
+  if (V % 4 == 0) {
+#pragma unroll
+    for (int i = 0; i < V / 4; ++i) {
+      const float4 x = reinterpret_cast<const float4*>(p)[i];
+      v[4 * i] = x.x;
+      v[4 * i + 1] = x.y;
+      v[4 * i + 2] = x.z;
+      v[4 * i + 3] = x.w;
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < V; ++i) v[i] = p[i];
+  }
+}
+template <int V>
+__device__ __forceinline__ void load(float (&v)[V], const uint16_t* p) {
+  if (V % 8 == 0) {
+#pragma unroll
+    for (int i = 0; i < V / 8; ++i) {
+      const uint4 x = reinterpret_cast<const uint4*>(p)[i];
+      const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        v[8 * i + 2 * j] = __uint_as_float(w[j] << 16);
+        v[8 * i + 2 * j + 1] = __uint_as_float(w[j] & 0xFFFF0000u);
+      }
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < V; ++i) v[i] = __uint_as_float((uint32_t)p[i] << 16);
+  }
+}
+template <int V>
+__device__ __forceinline__ void store(float* p, const float (&v)[V]) {
+  if (V % 4 == 0) {
+#pragma unroll
+    for (int i = 0; i < V / 4; ++i)
+      reinterpret_cast<float4*>(p)[i] = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+  } else {
+#pragma unroll
+    for (int i = 0; i < V; ++i) p[i] = v[i];
+  }
+}
+template <int V>
+__device__ __forceinline__ void store(uint16_t* p, const float (&v)[V]) {
+  if (V % 8 == 0) {
+#pragma unroll
+    for (int i = 0; i < V / 8; ++i) {
+      uint32_t w[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        w[j] = (uint32_t)f32_to_bf16_rn(v[8 * i + 2 * j]) | ((uint32_t)f32_to_bf16_rn(v[8 * i + 2 * j + 1]) << 16);
+      reinterpret_cast<uint4*>(p)[i] = make_uint4(w[0], w[1], w[2], w[3]);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < V; ++i) p[i] = f32_to_bf16_rn(v[i]);
+  }
+}
+
+// V pairs per thread: 8 where every row, head and half starts on 16 bytes, else 1.
+template <typename X, typename Y, int V, bool ADJ>
+__global__ void __launch_bounds__(kThreads) rope_kernel(const RopeParams p) {
+  grid_dependency_wait();
+  const long long id = (long long)blockIdx.x * kThreads + threadIdx.x;
+  const long long row = id / p.chunks;
+  const int ch = (int)(id - row * p.chunks);
+  const long long t = row / p.head_groups;
+  const int hg = (int)(row - t * p.head_groups);
+  if (t >= p.T) return;
+  const int turned = p.pairs / V;
+  const int H = p.h0 + p.h1;
+  float c[V], s[V];
+  int d0, d1;
+  if (ch < turned) {
+    const int i0 = ch * V;
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      const int ax = p.axis ? p.axis[i0 + i] : 0;
+      // an axis beyond the positions' rows turns nothing
+      const int pos = ax < p.n_axes ? p.pos[(long long)ax * p.T + t] : 0;
+      const float2 cs = cos_sin_turn(turn_per_position(p.freq[i0 + i]), pos);
+      c[i] = cs.x;
+      s[i] = p.inverse ? -cs.y : cs.y;
+    }
+    d0 = ADJ ? 2 * i0 : i0;
+    d1 = ADJ ? d0 + V : i0 + p.pairs;
+  } else {
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      c[i] = 1.f;
+      s[i] = 0.f;
+    }
+    d0 = 2 * p.pairs + (ch - turned) * 2 * V;
+    d1 = d0 + V;
+  }
+  const bool whole = d1 + V <= p.D;  // the copied rest may be odd: its last chunk is then one value
+  for (int h = hg; h < H; h += p.head_groups) {
+    const bool isq = h < p.h0;
+    const int hh = isq ? h : h - p.h0;
+    const X* x = static_cast<const X*>(isq ? p.x0 : p.x1) + t * (isq ? p.xs0 : p.xs1) + (long long)hh * p.D;
+    Y* y = static_cast<Y*>(isq ? p.y0 : p.y1) + t * (isq ? p.ys0 : p.ys1) + (long long)hh * p.D;
+    float a[V], b[V];
+    load<V>(a, x + d0);
+    if (whole) load<V>(b, x + d1);
+    if (ch < turned) {
+      float ra[V], rb[V];
+      if (ADJ) {  // a, b hold 2V adjacent values
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+          const float u = 2 * i < V ? a[(2 * i) % V] : b[(2 * i) % V], w = 2 * i + 1 < V ? a[(2 * i + 1) % V] : b[(2 * i + 1) % V];
+          const float nu = u * c[i] - w * s[i], nw = w * c[i] + u * s[i];
+          if (2 * i < V) ra[(2 * i) % V] = nu;
+          else rb[(2 * i) % V] = nu;
+          if (2 * i + 1 < V) ra[(2 * i + 1) % V] = nw;
+          else rb[(2 * i + 1) % V] = nw;
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+          ra[i] = a[i] * c[i] - b[i] * s[i];
+          rb[i] = b[i] * c[i] + a[i] * s[i];
+        }
+      }
+      store<V>(y + d0, ra);
+      store<V>(y + d1, rb);
+    } else {
+      store<V>(y + d0, a);
+      if (whole) store<V>(y + d1, b);
+    }
+  }
+}
+
+template <typename X, typename Y>
+int launch_typed(const RopeParams& p, bool vec, bool adj, unsigned grid, cudaStream_t s, std::string* err) {
+  const dim3 g(grid), b(kThreads);
+  if (vec) return adj ? launch_pdl(rope_kernel<X, Y, 8, true>, g, b, 0, s, p, "rope", err)
+                      : launch_pdl(rope_kernel<X, Y, 8, false>, g, b, 0, s, p, "rope", err);
+  return adj ? launch_pdl(rope_kernel<X, Y, 1, true>, g, b, 0, s, p, "rope", err)
+             : launch_pdl(rope_kernel<X, Y, 1, false>, g, b, 0, s, p, "rope", err);
+}
+
+bool on16(const void* p, long long stride, int elem) {
+  return reinterpret_cast<uintptr_t>(p) % 16 == 0 && stride * elem % 16 == 0;
+}
+
+}  // namespace
+
+int launch_rope(const RopeArgs& a, int num_sms, cudaStream_t s, std::string* err) {
+  const int xe = a.x_dtype == KQ_F32 ? 4 : 2, ye = a.y_dtype == KQ_F32 ? 4 : 2;
+  const bool vec = a.D % 16 == 0 && a.rot_dim % 16 == 0 && on16(a.x0, a.xs0, xe) && on16(a.x1, a.xs1, xe) &&
+                   on16(a.y0, a.ys0, ye) && on16(a.y1, a.ys1, ye);
+  const int V = vec ? 8 : 1;
+  RopeParams p = {a.x0, a.x1, a.y0, a.y1, a.xs0, a.xs1, a.ys0, a.ys1, a.h0, a.h1, a.T, a.D, a.rot_dim / 2,
+                  a.freq, a.axis, a.pos, a.n_axes, a.inverse ? 1 : 0, 0, 0};
+  p.chunks = p.pairs / V + (a.D - a.rot_dim + 2 * V - 1) / (2 * V);
+  // heads per thread: up to 8, fewer while the grid would leave SMs without threads
+  const int H = a.h0 + a.h1;
+  int per = 8;
+  while (per > 1 && (long long)a.T * p.chunks * ((H + per - 1) / per) < (long long)num_sms * 2048) per /= 2;
+  p.head_groups = (H + per - 1) / per;
+  const long long total = (long long)a.T * p.head_groups * p.chunks, grid = (total + kThreads - 1) / kThreads;
+  if (grid > 0x7FFFFFFF) {
+    *err = "rope: too many values for one call";
+    return -1;
+  }
+  const unsigned g = (unsigned)grid;
+  if (a.x_dtype == KQ_F32)
+    return a.y_dtype == KQ_F32 ? launch_typed<float, float>(p, vec, a.adjacent, g, s, err)
+                               : launch_typed<float, uint16_t>(p, vec, a.adjacent, g, s, err);
+  return a.y_dtype == KQ_F32 ? launch_typed<uint16_t, float>(p, vec, a.adjacent, g, s, err)
+                             : launch_typed<uint16_t, uint16_t>(p, vec, a.adjacent, g, s, err);
+}
+
+}  // namespace kq
