@@ -44,11 +44,13 @@
 namespace kq {
 namespace {
 
-constexpr int kWarps = 4, kThreads = 32 * kWarps;
-constexpr int kWarpPos = 64, kTile = kWarps * kWarpPos;
-constexpr int kMaxSegments = 128;
+constexpr int kWarps = 4;                          // warps that multiply; one more brings the codes
+constexpr int kMath = 32 * kWarps, kThreads = kMath + 32;
+constexpr int kWarpPos = 32, kStep = kWarps * kWarpPos;  // positions of a step, 32 per warp
+constexpr int kMinSegment = 512, kMaxSegments = 64;      // positions of a segment at least, segments of a request at most
+constexpr int kWindow = 32 * 16 / kStep;                 // steps whose page ids are read at once, a group of 16 tokens per lane
 constexpr int kSplitTokens = 32;  // windows up to this many tokens are cut along the context
-constexpr int kMaxRows = 32;      // query rows of an item
+constexpr float kLowest = -3e38f;  // below every finite score in use: keeps -inf out of differences
 constexpr uint64_t kWaitNs = 2000000000ull;
 constexpr int kCombThreads = 256;
 
@@ -73,16 +75,20 @@ struct AttnKV8Params {
   int slots, row_cap;
 };
 
-__device__ __forceinline__ int segment_tiles(int len) {  // tiles per segment: a power of two
-  const int tiles = (len + kTile - 1) / kTile;
-  int n = 1;
-  while ((tiles + n - 1) / n > kMaxSegments) n <<= 1;
-  return n;
+// log2 of a segment's positions: kMinSegment doubled until kMaxSegments hold the request.
+__device__ __forceinline__ int segment_log2(int len) {
+  constexpr int kBase = kMinSegment * kMaxSegments;
+  static_assert((kBase & (kBase - 1)) == 0, "powers of two");
+  const int over = (len - 1) / kBase;
+  return __ffs(kMinSegment) - 1 + (over > 0 ? 32 - __clz(over) : 0);
 }
 __device__ __forceinline__ int segments(int len) {
-  const int n = segment_tiles(len) * kTile;
-  return (len + n - 1) / n;
+  const int s = segment_log2(len);
+  return (len + (1 << s) - 1) >> s;
 }
+
+// Warps that share a row of the combine: up to 16 segments each, and up to 8 warps.
+__device__ __forceinline__ int combine_warps(int nseg) { return nseg <= 16 ? 1 : nseg <= 32 ? 2 : nseg <= 64 ? 4 : 8; }
 
 // A request whose lengths do not fit the call's bounds takes no part.
 __device__ __forceinline__ bool request_ok(const AttnKV8Params& p, int c, int n) {
@@ -90,10 +96,13 @@ __device__ __forceinline__ bool request_ok(const AttnKV8Params& p, int c, int n)
          ((c + n + (1 << p.log2p) - 1) >> p.log2p) <= p.max_blocks;
 }
 
-// Prefix sums over the requests in shared memory: its first token, work item and partial slot.
-// ITEMS: items of the attention kernel; otherwise tokens of requests that the combine finishes.
+// The requests in shared memory: each one's first token, work item and partial slot, and its cached
+// length. ITEMS: items of the attention kernel; otherwise CTA tasks of the combine.
+struct Request {
+  int tok, item, slot, ctx;
+};
 template <int THREADS, bool ITEMS>
-__device__ __forceinline__ void scan_requests(const AttnKV8Params& p, int row_block, int* tok, int* item, int* slot, int* sm) {
+__device__ __forceinline__ void scan_requests(const AttnKV8Params& p, int row_block, Request* req, int* sm) {
   constexpr int W = THREADS / 32;
   const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
   long long ct = 0;
@@ -101,16 +110,16 @@ __device__ __forceinline__ void scan_requests(const AttnKV8Params& p, int row_bl
   bool bad = false;
   for (int base = 0; base < p.B; base += THREADS) {
     const int r = base + tid;
-    int a = 0, b = 0, c = 0;
+    int a = 0, b = 0, c = 0, ctx = 0;
     if (r < p.B) {
-      const int ctx = p.ctx[r], n = p.fresh[r];
+      const int n = p.fresh[r];
+      ctx = p.ctx[r];
       a = n > 0 ? min(n, p.T + 1) : 0;
       if (request_ok(p, ctx, n)) {
         if (n > 0) {
-          const bool cut = n <= kSplitTokens;
-          const int nseg = cut ? segments(ctx + n) : 1;
-          if (ITEMS) b = (n * p.group + row_block - 1) / row_block * nseg;
-          else b = nseg > 1 ? n : 0;
+          const int nseg = n <= kSplitTokens ? segments(ctx + n) : 1, rows = n * p.group;
+          if (ITEMS) b = (rows + row_block - 1) / row_block * nseg;
+          else b = nseg <= 1 ? 0 : (rows * p.n_kv * combine_warps(nseg) + W - 1) / W;
           c = nseg > 1 ? nseg : 0;
         }
       } else {
@@ -147,29 +156,23 @@ __device__ __forceinline__ void scan_requests(const AttnKV8Params& p, int row_bl
       tb += xb;
       tc += xc;
     }
-    if (r < p.B) {
-      tok[r] = (int)min(ct + pa + a - a0, (long long)INT_MAX);
-      item[r] = ci + pb + b - b0;
-      slot[r] = cs + pc + c - c0;
-    }
+    if (r < p.B) req[r] = {(int)min(ct + pa + a - a0, (long long)INT_MAX), ci + pb + b - b0, cs + pc + c - c0, ctx};
     ct += ta;
     ci += tb;
     cs += tc;
   }
-  if (tid == 0) {
-    tok[p.B] = (int)min(ct, (long long)INT_MAX);
-    item[p.B] = ct > p.T ? 0 : ci;  // more tokens than q has rows: nothing is done
-    slot[p.B] = cs;
-  }
-  if (bad || ct > p.T) atomicOr(&g_kv8_errors, 2u);
+  // more tokens than q has rows, or too many items: nothing is done
+  const bool over = ct > p.T || (long long)ci * p.n_kv > INT_MAX;
+  if (tid == 0) req[p.B] = {(int)min(ct, (long long)INT_MAX), over ? 0 : ci, cs, 0};
+  if (ITEMS && (bad || over)) atomicOr(&g_kv8_errors, 2u);
   __syncthreads();
 }
 
-__device__ __forceinline__ int find_request(const int* s, int B, int x) {  // largest r with s[r] <= x
+__device__ __forceinline__ int find_request(const Request* req, int B, int item) {  // the last r that starts at or before it
   int lo = 0, hi = B;
   while (hi - lo > 1) {
     const int mid = (lo + hi) >> 1;
-    if (s[mid] <= x) lo = mid;
+    if (req[mid].item <= item) lo = mid;
     else hi = mid;
   }
   return lo;
@@ -188,159 +191,276 @@ __device__ __forceinline__ void codes_to_h2(uint32_t w, uint32_t& lo, uint32_t& 
 }
 __device__ __forceinline__ float fast_exp2(float x) {
   float y;
-  asm("ex2.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
 
-// Largest of the eight lanes that hold one query row's scores.
+// Largest, and sum, over the eight lanes that hold one query row.
 __device__ __forceinline__ float max_over_rows(float v) {
 #pragma unroll
   for (int x = 4; x < 32; x <<= 1) v = fmaxf(v, __shfl_xor_sync(~0u, v, x));
   return v;
 }
 
+__device__ __forceinline__ float sum_over_rows(float v) {
+#pragma unroll
+  for (int x = 4; x < 32; x <<= 1) v += __shfl_xor_sync(~0u, v, x);
+  return v;
+}
+
+__device__ __forceinline__ void mbar_arrive(uint64_t* bar) {
+  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_addr(bar)) : "memory");
+}
+// The warps that multiply, without the one that copies.
+__device__ __forceinline__ void math_barrier() { asm volatile("bar.sync 1, %0;" ::"n"(kMath) : "memory"); }
+
+// Shared memory of a CTA: a ring of slots (a step's K or its V), the warps' outputs of an item, for
+// more than 8 query rows the item's query operands of each warp, the requests.
 template <int D, int NT, bool WIDE>
 struct AttnSmem {
-  static constexpr int RB = 8 * NT;
-  static constexpr int kStage = kWarpPos * D;          // bytes of K (and of V) per warp
-  static constexpr int kOut = RB * (D + 4) * 4;        // a warp's output rows, 4 floats of padding
-  static constexpr int kWarpBytes = (2 * kStage > kOut ? 2 * kStage : kOut + 127) / 128 * 128;
-  static constexpr int kQ = NT * D * 16;               // fp16 query operands (hi); the lo parts follow
-  static constexpr size_t bytes(int B) { return (size_t)kWarps * kWarpBytes + (WIDE ? 2 : 1) * kQ + (size_t)3 * (B + 1) * 4; }
+  static constexpr int RB = 8 * NT, PARTS = WIDE ? 2 : 1;
+  static constexpr int kDepth = D == 128 ? 3 : 6;
+  static constexpr int kSlot = kStep * D;
+  static constexpr int kOut = kDepth * kSlot;                     // [warp][RB][D + 4] floats
+  static constexpr int kOutWarp = RB * (D + 4);
+  static constexpr int kQ = kOut + kWarps * kOutWarp * 4;         // [part][NT][D / 32][32 lanes][4 words]
+  static constexpr int kReq = kQ + (NT == 1 ? 0 : PARTS * NT * D * 16);
+  static constexpr size_t bytes(int B) { return kReq + (size_t)(B + 1) * sizeof(Request); }
+};
+
+struct Item {  // (request, kv head, block of query rows, segment)
+  int r, h, row0, rows, seg, nseg, ctx, len, tok0, slot;
+  int step0, step1, end;  // steps of kStep; positions from `end` on are seen by no row
 };
 
 template <int D, int NT, bool WIDE>
-__global__ void __launch_bounds__(kThreads) attn_kv8_kernel(const AttnKV8Params p) {
+__global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : NT == 2 ? 2 : 1) attn_kv8_kernel(const AttnKV8Params p) {
   using S = AttnSmem<D, NT, WIDE>;
-  constexpr int RB = S::RB, C32 = D / 32;
+  constexpr int RB = S::RB, C32 = D / 32, DEPTH = S::kDepth;
+  constexpr bool QREG = NT == 1;  // query operands stay in registers
   extern __shared__ __align__(128) uint8_t smem[];
-  __shared__ __align__(8) uint64_t sm_bar[kWarps][2];
-  __shared__ float sm_hq[RB], sm_rf[RB], sm_m[kWarps][RB], sm_l[kWarps][RB], sm_h[kWarps][RB];
-  __shared__ int sm_lim[RB], sm_scan[3 * kWarps];
+  __shared__ __align__(8) uint64_t sm_full[DEPTH], sm_empty[DEPTH];
+  __shared__ __align__(16) float sm_scale[4][2][kStep / 16];  // [step & 3][k, v][group]
+  __shared__ int sm_scan[3 * (kThreads / 32)];
+  __shared__ __align__(16) float sm_hq[RB], sm_rf[RB];  // read in pairs
+  __shared__ float sm_m[kWarps][RB], sm_l[kWarps][RB], sm_h[kWarps][RB];
+  __shared__ int sm_lim[RB];
   __shared__ uint32_t sm_mask[RB];
-  uint32_t* sm_q = reinterpret_cast<uint32_t*>(smem + kWarps * S::kWarpBytes);  // [hi/lo][NT][C32][32][4]
-  int* sm_tok = reinterpret_cast<int*>(smem + kWarps * S::kWarpBytes + (WIDE ? 2 : 1) * S::kQ);
-  int* sm_item = sm_tok + p.B + 1;
-  int* sm_slot = sm_item + p.B + 1;
+  Request* req = reinterpret_cast<Request*>(smem + S::kReq);
   const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5, g = lane >> 2, t4 = lane & 3;
-  uint8_t* kst = smem + w * S::kWarpBytes;
-  uint8_t* vst = kst + S::kStage;
-  if (lane == 0) {
-    mbar_init(&sm_bar[w][0], 1);
-    mbar_init(&sm_bar[w][1], 1);
+  uint32_t* sm_q = reinterpret_cast<uint32_t*>(smem + S::kQ);
+  if (tid == 0) {
+    for (int k = 0; k < DEPTH; ++k) {
+      mbar_init(&sm_full[k], 1);
+      mbar_init(&sm_empty[k], kWarps);
+    }
     fence_mbar_init();
   }
   grid_dependency_wait();
-  scan_requests<kThreads, true>(p, RB, sm_tok, sm_item, sm_slot, sm_scan);
+  scan_requests<kThreads, true>(p, RB, req, sm_scan);
   grid_launch_dependents();
-  const long long total = (long long)sm_item[p.B] * p.n_kv;
-  const int P = 1 << p.log2p, page_groups = P >= kWarpPos ? 4 : P >> 4;
-  uint32_t phase = 0;
-  bool dead = false;
-  for (long long it = blockIdx.x; it < total; it += gridDim.x) {
-    const int h = (int)(it % p.n_kv), wi = (int)(it / p.n_kv);
-    const int r = find_request(sm_item, p.B, wi);
-    const int ctx = p.ctx[r], n = p.fresh[r], len = ctx + n, rows = n * p.group;
-    const bool cut = n <= kSplitTokens;
-    const int seg_tiles = cut ? segment_tiles(len) : 0, nseg = cut ? segments(len) : 1;
-    const int local = wi - sm_item[r], rb = local / nseg, seg = local - rb * nseg;
-    const int row0 = rb * RB, tok0 = sm_tok[r];
-    // tiles: the segment's, and none past what the block's last token sees
-    const int last_row = min(row0 + RB, rows) - 1;
-    const int end = p.mask ? len : ctx + last_row / p.group + 1;  // exclusive
-    const int tile0 = cut ? seg * seg_tiles : 0;
-    const int tile1 = cut ? min(tile0 + seg_tiles, (end + kTile - 1) / kTile) : (end + kTile - 1) / kTile;
+  const int total = req[p.B].item, P = 1 << p.log2p;
+  // items x kv heads, a CTA's shares gridDim.x apart: (item, head) moves by (d_item, d_head)
+  const int d_item = gridDim.x / p.n_kv, d_head = gridDim.x - d_item * p.n_kv;
+  struct Place {
+    int item, head;
+  };
+  const Place place0 = {(int)blockIdx.x / p.n_kv, (int)blockIdx.x % p.n_kv};
+  auto move = [&](Place& at) {
+    at.item += d_item;
+    at.head += d_head;
+    if (at.head >= p.n_kv) {
+      at.head -= p.n_kv;
+      ++at.item;
+    }
+  };
 
-    // ---- this warp's copies of one tile: K and V of its 64 positions
-    int page = -1;  // lane j < 4: page of group j
-    auto request = [&](int tile) {
-      const int pos = tile * kTile + w * kWarpPos + 16 * lane;
-      page = -1;
-      if (lane < 4 && (pos & -P) < end) {  // also groups past the end of a page that holds positions: its scale is theirs
-        page = p.table[(long long)r * p.max_blocks + (pos >> p.log2p)];
-        if (page < 0 || page >= p.n_pages) {
-          page = -2;
-          atomicOr(&g_kv8_errors, 2u);
+  auto item_of = [&](Place at) {
+    Item x;
+    x.h = at.head;
+    x.r = find_request(req, p.B, at.item);
+    const Request q = req[x.r];
+    x.tok0 = q.tok;
+    x.ctx = q.ctx;
+    x.slot = q.slot;
+    const int n = req[x.r + 1].tok - q.tok;
+    x.len = q.ctx + n;
+    x.rows = n * p.group;
+    const bool cut = n <= kSplitTokens;
+    const int log2 = segment_log2(x.len) - 7;  // of steps
+    static_assert(kStep == 128, "segments are cut into steps of 128");
+    x.nseg = cut ? segments(x.len) : 1;
+    int local = at.item - q.item, rb = 0;
+    if (local >= x.nseg) {
+      rb = local / x.nseg;
+      local -= rb * x.nseg;
+    }
+    x.seg = local;
+    x.row0 = rb * RB;
+    x.end = p.mask || n == 1 ? x.len : x.ctx + (min(x.row0 + RB, x.rows) - 1) / p.group + 1;
+    const int last = (x.end + kStep - 1) / kStep;
+    x.step0 = cut ? x.seg << log2 : 0;
+    x.step1 = cut ? min(x.step0 + (1 << log2), last) : last;
+    return x;
+  };
+
+  bool dead = false;
+  auto wait = [&](uint64_t* bar, uint32_t phase) {
+    if (!dead && !mbar_wait_bounded(bar, phase, kWaitNs)) dead = true;
+  };
+  int slot = 0;
+  uint32_t phase = 0;
+  auto next_slot = [&]() {
+    if (++slot == DEPTH) {
+      slot = 0;
+      phase ^= 1;
+    }
+  };
+
+  // ---- the last warp runs ahead over the CTA's steps, across its items, and fills the ring
+  if (w == kWarps) {
+    const int per = P >> 4, chunks = kStep >> p.log2p;  // groups of a page; pages of a step
+    int steps = 0;
+    for (Place at = place0; at.item < total; move(at)) {
+      const Item x = item_of(at);
+      for (int s0 = x.step0; s0 < x.step1; s0 += kWindow) {
+        // page id and scales of this lane's group of 16 tokens; also of groups past the end of a page
+        // that holds positions: its scale is theirs
+        const int pos = s0 * kStep + 16 * lane;
+        int page = -1;
+        float ks = 0.f, vs = 0.f;
+        if ((pos & -P) < x.end) {
+          page = p.table[(long long)x.r * p.max_blocks + (pos >> p.log2p)];
+          if ((unsigned)page < (unsigned)p.n_pages) {
+            const long long sc = (long long)page * p.n_kv + x.h;
+            ks = p.ks[sc];
+            vs = p.vs[sc];
+          } else {  // no page of this cache: nothing is copied, the rows that see it come out NaN
+            page = -1;
+            ks = vs = __uint_as_float(0x7FC00000u);
+            atomicOr(&g_kv8_errors, 2u);
+          }
+        }
+        const int n = min(kWindow, x.step1 - s0);
+        for (int j = 0; j < n; ++j, ++steps) {
+          const int c = lane < chunks ? lane : 0;  // lane c copies the step's c-th page
+          const int c_page = __shfl_sync(~0u, page, 8 * j + c * per);
+          const int left = x.end - ((s0 + j) * kStep + (c << p.log2p));
+          const unsigned bytes = lane < chunks && c_page >= 0 && left > 0 ? min(per, (left + 15) >> 4) * 16 * D : 0;
+          const unsigned all = __reduce_add_sync(~0u, bytes);
+          const long long off = (((long long)c_page * p.n_kv + x.h) << p.log2p) * D;
+#pragma unroll
+          for (int half = 0; half < 2; ++half) {
+            wait(&sm_empty[slot], phase ^ 1);
+            if (half == 0 && (lane >> 3) == j) {
+              sm_scale[steps & 3][0][lane & 7] = ks;
+              sm_scale[steps & 3][1][lane & 7] = vs;
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive_expect_tx(&sm_full[slot], all);
+            __syncwarp();
+            if (bytes) bulk_g2s(smem + slot * S::kSlot + (c << p.log2p) * D, (half ? p.vc : p.kc) + off, bytes, &sm_full[slot]);
+            next_slot();
+          }
         }
       }
-      const bool live = page >= 0 && pos < end;
-      const unsigned any = __ballot_sync(~0u, live);
-      if (lane == 0) {
-        const uint32_t bytes = __popc(any) * 16 * D;
-        mbar_arrive_expect_tx(&sm_bar[w][0], bytes);
-        mbar_arrive_expect_tx(&sm_bar[w][1], bytes);
-      }
-      __syncwarp();
-      if (live) {
-        const long long off = (((long long)page * p.n_kv + h) << p.log2p) * D + (pos & (P - 1)) * D;
-        bulk_g2s(kst + lane * 16 * D, p.kc + off, 16 * D, &sm_bar[w][0]);
-        bulk_g2s(vst + lane * 16 * D, p.vc + off, 16 * D, &sm_bar[w][1]);
-      }
-    };
-    if (tile0 < tile1) request(tile0);
+    }
+    if (dead && lane == 0) atomicOr(&g_kv8_errors, 1u);
+    return;
+  }
 
-    // ---- query operands: warp w takes rows w, w + 4, ...
-    for (int rr = w; rr < RB; rr += kWarps) {
-      const int row = row0 + rr, i = row / p.group;
-      const bool live = row < rows;
-      float v[4] = {0.f, 0.f, 0.f, 0.f};
-      if (live && 4 * lane < D) {
-        const long long at = (tok0 + i) * p.qs + (long long)(h * p.group + row - i * p.group) * D + 4 * lane;
-        if (p.q_f32) {
-          const float4 x = *reinterpret_cast<const float4*>(static_cast<const float*>(p.q) + at);
-          v[0] = x.x;
-          v[1] = x.y;
-          v[2] = x.z;
-          v[3] = x.w;
-        } else {
-          const uint2 x = *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(p.q) + at);
-          v[0] = __uint_as_float(x.x << 16);
-          v[1] = __uint_as_float(x.x & 0xFFFF0000u);
-          v[2] = __uint_as_float(x.y << 16);
-          v[3] = __uint_as_float(x.y & 0xFFFF0000u);
+  auto free_slot = [&]() {  // its codes are used
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&sm_empty[slot]);
+    next_slot();
+  };
+  int steps = 0;
+  for (Place at = place0; at.item < total; move(at)) {
+    const Item x = item_of(at);
+    const int group = p.group;
+    // ---- query operands: lane (g, t4) holds row g of each block of 8 at dims 16 s + 4 t4 .. + 3; rows
+    // past the last are zeros that see nothing
+    uint2 qh[QREG ? 2 * C32 : 1], ql[QREG && WIDE ? 2 * C32 : 1];
+    float hq[QREG ? 1 : NT][2], rf[QREG ? 1 : NT][2];
+    int lim[QREG ? 1 : NT][2];
+#pragma unroll 1
+    for (int nt = QREG ? 0 : w; nt < NT; nt += QREG ? 1 : kWarps) {  // each warp for itself, or its blocks for all
+      const int row = x.row0 + 8 * nt + g, ti = row / group;
+      const bool live = row < x.rows;
+      float v[2 * C32][4];
+      const long long from = (x.tok0 + ti) * p.qs + (long long)(x.h * group + row - ti * group) * D + 4 * t4;
+      if (p.q_f32) {
+        const float4* src = reinterpret_cast<const float4*>(static_cast<const float*>(p.q) + from);
+#pragma unroll
+        for (int s = 0; s < 2 * C32; ++s) {
+          const float4 q = live ? src[4 * s] : make_float4(0.f, 0.f, 0.f, 0.f);
+          v[s][0] = q.x;
+          v[s][1] = q.y;
+          v[s][2] = q.z;
+          v[s][3] = q.w;
+        }
+      } else {
+        const uint2* src = reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(p.q) + from);
+#pragma unroll
+        for (int s = 0; s < 2 * C32; ++s) {
+          const uint2 q = live ? src[4 * s] : make_uint2(0u, 0u);
+          v[s][0] = __uint_as_float(q.x << 16);
+          v[s][1] = __uint_as_float(q.x & 0xFFFF0000u);
+          v[s][2] = __uint_as_float(q.y << 16);
+          v[s][3] = __uint_as_float(q.y & 0xFFFF0000u);
         }
       }
       unsigned top = 0;
 #pragma unroll
-      for (int e = 0; e < 4; ++e) top = max(top, __float_as_uint(v[e]) & 0x7FFFFFFFu);
-      top = __reduce_max_sync(~0u, top);
+      for (int s = 0; s < 2 * C32; ++s)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) top = max(top, __float_as_uint(v[s][e]) & 0x7FFFFFFFu);
+      top = max(top, __shfl_xor_sync(~0u, top, 1));
+      top = max(top, __shfl_xor_sync(~0u, top, 2));
       // 2^e with the largest |q| 2^e in [2^14, 2^15); 1 for zero rows and for rows that are not finite
       const int ex = (int)(top >> 23);
       const int e2 = top == 0 || ex == 0xFF ? 0 : max(-126, min(126, 14 - (ex - 127)));
-      const float up = __uint_as_float((unsigned)(127 + e2) << 23), down = __uint_as_float((unsigned)(127 - e2) << 23);
+      const float up = __uint_as_float((unsigned)(127 + e2) << 23);
+      const float factor = __uint_as_float((unsigned)(127 - e2) << 23) * p.scale_log2e;
+      // half of each row's sum, as the products below add it up: the codes' + 1/2
+      float half[4] = {0.f, 0.f, 0.f, 0.f};
+      const uint32_t halves[4] = {0x38003800u, 0x38003800u, 0x38003800u, 0x38003800u};
 #pragma unroll
-      for (int e = 0; e < 4; ++e) v[e] *= up;
-      const uint32_t h0 = f2_to_h2(v[0], v[1]), h1 = f2_to_h2(v[2], v[3]);
-      float f[4] = {h_lo_to_f(h0), h_lo_to_f(h0 >> 16), h_lo_to_f(h1), h_lo_to_f(h1 >> 16)};
-      const int c = lane >> 3, s = (lane >> 2) & 1, at = (((rr >> 3) * C32 + c) * 32 + (rr & 7) * 4 + t4) * 4 + 2 * s;
-      if (4 * lane < D) {
-        sm_q[at] = h0;
-        sm_q[at + 1] = h1;
-      }
-      if (WIDE) {
-        const uint32_t l0 = f2_to_h2(v[0] - f[0], v[1] - f[1]), l1 = f2_to_h2(v[2] - f[2], v[3] - f[3]);
-        f[0] += h_lo_to_f(l0);
-        f[1] += h_lo_to_f(l0 >> 16);
-        f[2] += h_lo_to_f(l1);
-        f[3] += h_lo_to_f(l1 >> 16);
-        if (4 * lane < D) {
-          sm_q[S::kQ / 4 + at] = l0;
-          sm_q[S::kQ / 4 + at + 1] = l1;
+      for (int s = 0; s < 2 * C32; ++s) {
+        const float f[4] = {v[s][0] * up, v[s][1] * up, v[s][2] * up, v[s][3] * up};
+        const uint2 hi = make_uint2(f2_to_h2(f[0], f[1]), f2_to_h2(f[2], f[3]));
+        mma_f16_16816(half, halves, hi.x, hi.y, half);
+        if (QREG) qh[QREG ? s : 0] = hi;
+        else *reinterpret_cast<uint2*>(sm_q + ((nt * C32 + (s >> 1)) * 32 + lane) * 4 + 2 * (s & 1)) = hi;
+        if (WIDE) {
+          const uint2 lo = make_uint2(f2_to_h2(f[0] - h_lo_to_f(hi.x), f[1] - h_lo_to_f(hi.x >> 16)),
+                                      f2_to_h2(f[2] - h_lo_to_f(hi.y), f[3] - h_lo_to_f(hi.y >> 16)));
+          mma_f16_16816(half, halves, lo.x, lo.y, half);
+          if (QREG) ql[QREG ? s : 0] = lo;
+          else *reinterpret_cast<uint2*>(sm_q + NT * D * 4 + ((nt * C32 + (s >> 1)) * 32 + lane) * 4 + 2 * (s & 1)) = lo;
         }
       }
-      float sum = (f[0] + f[1]) + (f[2] + f[3]);
+      const int last = live ? x.ctx + ti : -1;
+      if (QREG) {
 #pragma unroll
-      for (int o = 1; o < 32; o <<= 1) sum += __shfl_xor_sync(~0u, sum, o);
-      if (lane == 0) {
-        sm_hq[rr] = 0.5f * sum;
-        sm_rf[rr] = down * p.scale_log2e;
-        sm_lim[rr] = live ? ctx + i : -1;
-        sm_mask[rr] = live && p.mask ? p.mask[tok0 + i] : 0u;
+        for (int k = 0; k < 2; ++k) {
+          hq[0][k] = half[k];
+          rf[0][k] = __shfl_sync(~0u, factor, 8 * t4 + 4 * k);
+          lim[0][k] = __shfl_sync(~0u, last, 8 * t4 + 4 * k);
+        }
+      } else {
+        if (g == 0) *reinterpret_cast<float2*>(sm_hq + 8 * nt + 2 * t4) = make_float2(half[0], half[1]);
+        if (t4 == 0) {
+          sm_rf[8 * nt + g] = factor;
+          sm_lim[8 * nt + g] = last;
+        }
       }
+      if (p.mask && t4 == 0) sm_mask[8 * nt + g] = live ? p.mask[x.tok0 + ti] : 0u;
     }
-    __syncthreads();
+    if (!QREG || p.mask) math_barrier();
 
-    float o[C32][2][NT][4], m[NT][2], l[NT][2], hv[NT][2];
+    // rows 2 t4 and 2 t4 + 1 of each block of 8; l and hv are this lane's share of the row's sums
+    float o[2 * C32][NT][4], m[NT][2], l[NT][2], hv[NT][2];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
@@ -349,244 +469,232 @@ __global__ void __launch_bounds__(kThreads) attn_kv8_kernel(const AttnKV8Params 
         l[nt][k] = hv[nt][k] = 0.f;
       }
 #pragma unroll
-      for (int c = 0; c < C32; ++c)
-#pragma unroll
-        for (int s = 0; s < 2; ++s) o[c][s][nt][0] = o[c][s][nt][1] = o[c][s][nt][2] = o[c][s][nt][3] = 0.f;
+      for (int s = 0; s < 2 * C32; ++s) o[s][nt][0] = o[s][nt][1] = o[s][nt][2] = o[s][nt][3] = 0.f;
     }
-    const int tok_pos = 4 * (g >> 1) + (g & 1);  // token of operand row g in its group; row g + 8 is two further
 
-    for (int tile = tile0; tile < tile1; ++tile) {
-      const int base = tile * kTile + w * kWarpPos;
-      if (base < end) {
-        float ksc = 0.f, vsc = 0.f;
-        if (lane < 4 && page != -1) {
-          const float nan = __uint_as_float(0x7FC00000u);
-          ksc = page >= 0 ? p.ks[(long long)page * p.n_kv + h] : nan;
-          vsc = page >= 0 ? p.vs[(long long)page * p.n_kv + h] : nan;
-        }
-        // ---- scores
-        if (!dead && !mbar_wait_bounded(&sm_bar[w][0], phase, kWaitNs)) dead = true;
-        float sc[4][NT][4];
+    for (int step = x.step0; step < x.step1; ++step, ++steps) {
+      const uint8_t* kst = smem + slot * S::kSlot + w * kWarpPos * D;
+      // ---- scores
+      float sc[2][NT][4];
 #pragma unroll
-        for (int st = 0; st < 4; ++st)
-#pragma unroll
-          for (int nt = 0; nt < NT; ++nt) sc[st][nt][0] = sc[st][nt][1] = sc[st][nt][2] = sc[st][nt][3] = 0.f;
-#pragma unroll
-        for (int c = 0; c < C32; ++c) {
-          uint4 qh[NT], ql[NT];
-#pragma unroll
-          for (int nt = 0; nt < NT; ++nt) {
-            qh[nt] = lds128(sm_q + ((nt * C32 + c) * 32 + lane) * 4);
-            if (WIDE) ql[nt] = lds128(sm_q + S::kQ / 4 + ((nt * C32 + c) * 32 + lane) * 4);
-          }
-#pragma unroll
-          for (int st = 0; st < 4; ++st) {
-            const uint4 x = lds128(kst + st * 16 * D + c * 512 + lane * 16);
-            uint32_t a0[4], a1[4];
-            codes_to_h2(x.x, a0[0], a0[2]);
-            codes_to_h2(x.y, a0[1], a0[3]);
-            codes_to_h2(x.z, a1[0], a1[2]);
-            codes_to_h2(x.w, a1[1], a1[3]);
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-              mma_f16_16816(sc[st][nt], a0, qh[nt].x, qh[nt].y, sc[st][nt]);
-              mma_f16_16816(sc[st][nt], a1, qh[nt].z, qh[nt].w, sc[st][nt]);
-              if (WIDE) {
-                mma_f16_16816(sc[st][nt], a0, ql[nt].x, ql[nt].y, sc[st][nt]);
-                mma_f16_16816(sc[st][nt], a1, ql[nt].z, ql[nt].w, sc[st][nt]);
-              }
-            }
-          }
-        }
-        float kf[4], vf[4];
-#pragma unroll
-        for (int st = 0; st < 4; ++st) {
-          kf[st] = __shfl_sync(~0u, ksc, st);
-          vf[st] = __shfl_sync(~0u, vsc, st);
-        }
-        // ---- weights: rows 2 t4 and 2 t4 + 1 of each block of 8, operand rows g and g + 8 (tokens)
-        uint32_t wb[4][NT][2], wlo[WIDE ? 4 : 1][NT][2];
-        float fv[4][NT][2];
+      for (int st = 0; st < 2; ++st)
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
-          const int rr = nt * 8 + 2 * t4;
-          const float2 hq = lds_f2(sm_hq + rr), rf = lds_f2(sm_rf + rr);
-          const int lim0 = sm_lim[rr], lim1 = sm_lim[rr + 1];
+          const float2 h = QREG ? make_float2(hq[0][0], hq[0][1]) : lds_f2(sm_hq + nt * 8 + 2 * t4);
+          sc[st][nt][0] = sc[st][nt][2] = h.x;
+          sc[st][nt][1] = sc[st][nt][3] = h.y;
+        }
+      wait(&sm_full[slot], phase);
+      const float2 kf2 = lds_f2(&sm_scale[steps & 3][0][2 * w]), vf2 = lds_f2(&sm_scale[steps & 3][1][2 * w]);
+      const float kf[2] = {kf2.x, kf2.y}, vf[2] = {vf2.x, vf2.y};
+#pragma unroll
+      for (int cc = 0; cc < C32; ++cc) {
+        uint32_t a[2][2][4];
+#pragma unroll
+        for (int st = 0; st < 2; ++st) {
+          const uint4 k = lds128(kst + st * 16 * D + cc * 512 + lane * 16);
+          codes_to_h2(k.x, a[st][0][0], a[st][0][2]);
+          codes_to_h2(k.y, a[st][0][1], a[st][0][3]);
+          codes_to_h2(k.z, a[st][1][0], a[st][1][2]);
+          codes_to_h2(k.w, a[st][1][1], a[st][1][3]);
+        }
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          const uint4 q = QREG ? make_uint4(qh[QREG ? 2 * cc : 0].x, qh[QREG ? 2 * cc : 0].y, qh[QREG ? 2 * cc + 1 : 0].x, qh[QREG ? 2 * cc + 1 : 0].y)
+                               : lds128(sm_q + ((nt * C32 + cc) * 32 + lane) * 4);
+#pragma unroll
+          for (int st = 0; st < 2; ++st) {
+            mma_f16_16816(sc[st][nt], a[st][0], q.x, q.y, sc[st][nt]);
+            mma_f16_16816(sc[st][nt], a[st][1], q.z, q.w, sc[st][nt]);
+          }
+          if (WIDE) {
+            const uint4 q2 = QREG ? make_uint4(ql[QREG && WIDE ? 2 * cc : 0].x, ql[QREG && WIDE ? 2 * cc : 0].y,
+                                               ql[QREG && WIDE ? 2 * cc + 1 : 0].x, ql[QREG && WIDE ? 2 * cc + 1 : 0].y)
+                                  : lds128(sm_q + NT * D * 4 + ((nt * C32 + cc) * 32 + lane) * 4);
+#pragma unroll
+            for (int st = 0; st < 2; ++st) {
+              mma_f16_16816(sc[st][nt], a[st][0], q2.x, q2.y, sc[st][nt]);
+              mma_f16_16816(sc[st][nt], a[st][1], q2.z, q2.w, sc[st][nt]);
+            }
+          }
+        }
+      }
+      free_slot();
+      // ---- weights against the page's largest score, up by 2^15 into fp16's range
+      const int pos0 = step * kStep + w * kWarpPos + 4 * (g >> 1) + (g & 1);  // token of operand row g; row g + 8 is two on
+      uint32_t wb[2][NT][2], wl[WIDE ? 2 : 1][NT][2];
+      float fv[2][NT][2];
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        const int rr = nt * 8 + 2 * t4;
+        const float2 rff = QREG ? make_float2(rf[0][0], rf[0][1]) : lds_f2(sm_rf + rr);
+        const int lim0 = QREG ? lim[0][0] : sm_lim[rr], lim1 = QREG ? lim[0][1] : sm_lim[rr + 1];
+        if (p.mask == nullptr) {
+#pragma unroll
+          for (int st = 0; st < 2; ++st) {
+            const int p0 = pos0 + 16 * st, p1 = p0 + 2;
+            const float r0 = rff.x * kf[st], r1 = rff.y * kf[st];
+            float* s = sc[st][nt];
+            s[0] = p0 <= lim0 ? s[0] * r0 : -INFINITY;
+            s[1] = p0 <= lim1 ? s[1] * r1 : -INFINITY;
+            s[2] = p1 <= lim0 ? s[2] * r0 : -INFINITY;
+            s[3] = p1 <= lim1 ? s[3] * r1 : -INFINITY;
+          }
+        } else {
           const uint32_t mk0 = sm_mask[rr], mk1 = sm_mask[rr + 1];
           auto sees = [&](int pos, int lim, uint32_t mk) {
-            if (p.mask == nullptr) return pos <= lim;
-            const int j = pos - ctx;
-            return lim >= 0 && pos < len && (j < 0 || (mk >> (j & 31) & 1u) != 0);
+            const int j = pos - x.ctx;
+            return lim >= 0 && pos < x.len && (j < 0 || (mk >> (j & 31) & 1u) != 0);
           };
-          float gx[4][2];  // largest score of each group, then of each page
 #pragma unroll
-          for (int st = 0; st < 4; ++st) {
-            const int p0 = base + 16 * st + tok_pos, p1 = p0 + 2;
+          for (int st = 0; st < 2; ++st) {
+            const int p0 = pos0 + 16 * st, p1 = p0 + 2;
+            const float r0 = rff.x * kf[st], r1 = rff.y * kf[st];
             float* s = sc[st][nt];
-            s[0] = sees(p0, lim0, mk0) ? (s[0] + hq.x) * (rf.x * kf[st]) : -INFINITY;
-            s[1] = sees(p0, lim1, mk1) ? (s[1] + hq.y) * (rf.y * kf[st]) : -INFINITY;
-            s[2] = sees(p1, lim0, mk0) ? (s[2] + hq.x) * (rf.x * kf[st]) : -INFINITY;
-            s[3] = sees(p1, lim1, mk1) ? (s[3] + hq.y) * (rf.y * kf[st]) : -INFINITY;
-            gx[st][0] = fmaxf(s[0], s[2]);
-            gx[st][1] = fmaxf(s[1], s[3]);
+            s[0] = sees(p0, lim0, mk0) ? s[0] * r0 : -INFINITY;
+            s[1] = sees(p0, lim1, mk1) ? s[1] * r1 : -INFINITY;
+            s[2] = sees(p1, lim0, mk0) ? s[2] * r0 : -INFINITY;
+            s[3] = sees(p1, lim1, mk1) ? s[3] * r1 : -INFINITY;
           }
+        }
+        float al[2];
+        bool moved = false;
 #pragma unroll
-          for (int k = 0; k < 2; ++k) {
-            if (page_groups == 4) {
-              gx[0][k] = gx[1][k] = gx[2][k] = gx[3][k] = max_over_rows(fmaxf(fmaxf(gx[0][k], gx[1][k]), fmaxf(gx[2][k], gx[3][k])));
-            } else if (page_groups == 2) {
-              gx[0][k] = gx[1][k] = max_over_rows(fmaxf(gx[0][k], gx[1][k]));
-              gx[2][k] = gx[3][k] = max_over_rows(fmaxf(gx[2][k], gx[3][k]));
-            } else {
+        for (int k = 0; k < 2; ++k) {
+          float* s0 = sc[0][nt] + k;
+          float* s1 = sc[1][nt] + k;
+          float g0 = fmaxf(s0[0], s0[2]), g1 = fmaxf(s1[0], s1[2]);
+          if (P > 16) {
+            g0 = g1 = max_over_rows(fmaxf(g0, g1));
+          } else {
+            g0 = max_over_rows(g0);
+            g1 = max_over_rows(g1);
+          }
+          // the row's reference follows its largest score only when that is 2^16 weights above it
+          const float top = fmaxf(g0, g1), was = m[nt][k], ref = top > was + 16.f ? top : was;
+          al[k] = ref == was ? 1.f : fast_exp2(was - ref);
+          moved |= ref != was;
+          m[nt][k] = ref;
+          // a group that the row sees nothing of has weights of 0 and takes nothing of its scale, even of a NaN
+          const float c0 = fmaxf(g0, kLowest) - 15.f;
+          const float u0 = fast_exp2(c0 - fmaxf(ref, kLowest));
+          const float f0 = g0 == -INFINITY ? 0.f : u0 * vf[0];
+          s0[0] = fast_exp2(s0[0] - c0);
+          s0[2] = fast_exp2(s0[2] - c0);
+          const float sum0 = s0[0] + s0[2];
+          fv[0][nt][k] = f0;
+          if (P > 16) {
+            s1[0] = fast_exp2(s1[0] - c0);
+            s1[2] = fast_exp2(s1[2] - c0);
+            const float sum = sum0 + (s1[0] + s1[2]);
+            fv[1][nt][k] = f0;
+            l[nt][k] = l[nt][k] * al[k] + sum * u0;
+            hv[nt][k] = hv[nt][k] * al[k] + sum * f0;
+          } else {
+            const float c1 = fmaxf(g1, kLowest) - 15.f;
+            const float u1 = fast_exp2(c1 - fmaxf(ref, kLowest));
+            const float f1 = g1 == -INFINITY ? 0.f : u1 * vf[1];
+            s1[0] = fast_exp2(s1[0] - c1);
+            s1[2] = fast_exp2(s1[2] - c1);
+            const float sum1 = s1[0] + s1[2];
+            fv[1][nt][k] = f1;
+            l[nt][k] = l[nt][k] * al[k] + sum0 * u0 + sum1 * u1;
+            hv[nt][k] = hv[nt][k] * al[k] + sum0 * f0 + sum1 * f1;
+          }
+        }
 #pragma unroll
-              for (int st = 0; st < 4; ++st) gx[st][k] = max_over_rows(gx[st][k]);
+        for (int st = 0; st < 2; ++st) {
+          const float* s = sc[st][nt];
+          const uint32_t e0 = f2_to_h2(s[0], s[1]), e1 = f2_to_h2(s[2], s[3]);
+          wb[st][nt][0] = movmatrix(e0);
+          wb[st][nt][1] = movmatrix(e1);
+          if (WIDE) {
+            wl[WIDE ? st : 0][nt][0] = movmatrix(f2_to_h2(s[0] - h_lo_to_f(e0), s[1] - h_lo_to_f(e0 >> 16)));
+            wl[WIDE ? st : 0][nt][1] = movmatrix(f2_to_h2(s[2] - h_lo_to_f(e1), s[3] - h_lo_to_f(e1 >> 16)));
+          }
+        }
+        if (__any_sync(~0u, moved)) {
+#pragma unroll
+          for (int s = 0; s < 2 * C32; ++s) {
+            o[s][nt][0] *= al[0];
+            o[s][nt][1] *= al[1];
+            o[s][nt][2] *= al[0];
+            o[s][nt][3] *= al[1];
+          }
+        }
+      }
+      // ---- values: a page's products are added up before its scale
+      const uint8_t* vst = smem + slot * S::kSlot + w * kWarpPos * D;
+      wait(&sm_full[slot], phase);
+#pragma unroll
+      for (int cc = 0; cc < C32; ++cc) {
+        float acc[2][NT][4];
+#pragma unroll
+        for (int s = 0; s < 2; ++s)
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) acc[s][nt][0] = acc[s][nt][1] = acc[s][nt][2] = acc[s][nt][3] = 0.f;
+#pragma unroll
+        for (int st = 0; st < 2; ++st) {
+          const uint4 v = lds128(vst + st * 16 * D + cc * 512 + lane * 16);
+          uint32_t a[2][4];
+          codes_to_h2(v.x, a[0][0], a[0][2]);
+          codes_to_h2(v.y, a[0][1], a[0][3]);
+          codes_to_h2(v.z, a[1][0], a[1][2]);
+          codes_to_h2(v.w, a[1][1], a[1][3]);
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int s = 0; s < 2; ++s) {
+              mma_f16_16816(acc[s][nt], a[s], wb[st][nt][0], wb[st][nt][1], acc[s][nt]);
+              if (WIDE) mma_f16_16816(acc[s][nt], a[s], wl[WIDE ? st : 0][nt][0], wl[WIDE ? st : 0][nt][1], acc[s][nt]);
             }
-          }
-          const float mx0 = fmaxf(fmaxf(gx[0][0], gx[1][0]), fmaxf(gx[2][0], gx[3][0]));
-          const float mx1 = fmaxf(fmaxf(gx[0][1], gx[1][1]), fmaxf(gx[2][1], gx[3][1]));
-          const float n0 = fmaxf(m[nt][0], mx0), n1 = fmaxf(m[nt][1], mx1);
-          const float b0 = n0 == -INFINITY ? 0.f : n0, b1 = n1 == -INFINITY ? 0.f : n1;
-          const float al0 = fast_exp2(m[nt][0] - b0), al1 = fast_exp2(m[nt][1] - b1);
-          m[nt][0] = n0;
-          m[nt][1] = n1;
-          if (tile > tile0) {
-            l[nt][0] *= al0;
-            l[nt][1] *= al1;
-            hv[nt][0] *= al0;
-            hv[nt][1] *= al1;
+          if (st == 1 || P == 16) {
 #pragma unroll
-            for (int c = 0; c < C32; ++c)
+            for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
               for (int s = 0; s < 2; ++s) {
-                o[c][s][nt][0] *= al0;
-                o[c][s][nt][1] *= al1;
-                o[c][s][nt][2] *= al0;
-                o[c][s][nt][3] *= al1;
+                float* oo = o[2 * cc + s][nt];
+                float* aa = acc[s][nt];
+                oo[0] += fv[st][nt][0] * aa[0];
+                oo[1] += fv[st][nt][1] * aa[1];
+                oo[2] += fv[st][nt][0] * aa[2];
+                oo[3] += fv[st][nt][1] * aa[3];
+                if (st == 0) aa[0] = aa[1] = aa[2] = aa[3] = 0.f;
               }
           }
-#pragma unroll
-          for (int st = 0; st < 4; ++st) {
-            float* s = sc[st][nt];
-            // weights against the page's largest score, up by 2^15 into fp16's range
-            const float c0 = gx[st][0] == -INFINITY ? 0.f : gx[st][0] - 15.f, c1 = gx[st][1] == -INFINITY ? 0.f : gx[st][1] - 15.f;
-            s[0] = fast_exp2(s[0] - c0);
-            s[1] = fast_exp2(s[1] - c1);
-            s[2] = fast_exp2(s[2] - c0);
-            s[3] = fast_exp2(s[3] - c1);
-            const float up0 = gx[st][0] == -INFINITY ? 0.f : fast_exp2(c0 - b0), up1 = gx[st][1] == -INFINITY ? 0.f : fast_exp2(c1 - b1);
-            float f0 = vf[st] * up0, f1 = vf[st] * up1;
-            if (!(fabsf(vf[st]) <= 3.402823466e38f)) {  // a broken scale reaches the rows that see its page alone
-              const int p0 = base + 16 * st + tok_pos, p1 = p0 + 2;
-              int any = (sees(p0, lim0, mk0) || sees(p1, lim0, mk0) ? 1 : 0) | (sees(p0, lim1, mk1) || sees(p1, lim1, mk1) ? 2 : 0);
-#pragma unroll
-              for (int x = 4; x < 32; x <<= 1) any |= __shfl_xor_sync(~0u, any, x);
-              if (!(any & 1)) f0 = 0.f;
-              if (!(any & 2)) f1 = 0.f;
-            }
-            fv[st][nt][0] = f0;
-            fv[st][nt][1] = f1;
-            const float w0 = s[0] + s[2], w1 = s[1] + s[3];
-            l[nt][0] += w0 * up0;
-            l[nt][1] += w1 * up1;
-            hv[nt][0] += w0 * f0;
-            hv[nt][1] += w1 * f1;
-            const uint32_t e0 = f2_to_h2(s[0], s[1]), e1 = f2_to_h2(s[2], s[3]);
-            wb[st][nt][0] = movmatrix(e0);
-            wb[st][nt][1] = movmatrix(e1);
-            if (WIDE) {
-              wlo[st][nt][0] = movmatrix(f2_to_h2(s[0] - h_lo_to_f(e0), s[1] - h_lo_to_f(e0 >> 16)));
-              wlo[st][nt][1] = movmatrix(f2_to_h2(s[2] - h_lo_to_f(e1), s[3] - h_lo_to_f(e1 >> 16)));
-            }
-          }
         }
-        // ---- values: the groups of one page are added up before its scale
-        if (!dead && !mbar_wait_bounded(&sm_bar[w][1], phase, kWaitNs)) dead = true;
-#pragma unroll
-        for (int c = 0; c < C32; ++c) {
-          float acc[2][NT][4];
-#pragma unroll
-          for (int s = 0; s < 2; ++s)
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt) acc[s][nt][0] = acc[s][nt][1] = acc[s][nt][2] = acc[s][nt][3] = 0.f;
-#pragma unroll
-          for (int st = 0; st < 4; ++st) {
-            const uint4 x = lds128(vst + st * 16 * D + c * 512 + lane * 16);
-            uint32_t a0[4], a1[4];
-            codes_to_h2(x.x, a0[0], a0[2]);
-            codes_to_h2(x.y, a0[1], a0[3]);
-            codes_to_h2(x.z, a1[0], a1[2]);
-            codes_to_h2(x.w, a1[1], a1[3]);
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-              mma_f16_16816(acc[0][nt], a0, wb[st][nt][0], wb[st][nt][1], acc[0][nt]);
-              mma_f16_16816(acc[1][nt], a1, wb[st][nt][0], wb[st][nt][1], acc[1][nt]);
-              if (WIDE) {
-                mma_f16_16816(acc[0][nt], a0, wlo[st][nt][0], wlo[st][nt][1], acc[0][nt]);
-                mma_f16_16816(acc[1][nt], a1, wlo[st][nt][0], wlo[st][nt][1], acc[1][nt]);
-              }
-            }
-            if (((st + 1) & (page_groups - 1)) == 0) {
-#pragma unroll
-              for (int s = 0; s < 2; ++s)
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt) {
-                  o[c][s][nt][0] += fv[st][nt][0] * acc[s][nt][0];
-                  o[c][s][nt][1] += fv[st][nt][1] * acc[s][nt][1];
-                  o[c][s][nt][2] += fv[st][nt][0] * acc[s][nt][2];
-                  o[c][s][nt][3] += fv[st][nt][1] * acc[s][nt][3];
-                  acc[s][nt][0] = acc[s][nt][1] = acc[s][nt][2] = acc[s][nt][3] = 0.f;
-                }
-            }
-          }
-        }
-      } else if (!dead) {  // nothing was copied: the empty phase still completes
-        if (!mbar_wait_bounded(&sm_bar[w][0], phase, kWaitNs) || !mbar_wait_bounded(&sm_bar[w][1], phase, kWaitNs)) dead = true;
       }
-      phase ^= 1;
-      if (tile + 1 < tile1) {
-        __syncwarp();  // every lane has read the staged codes
-        request(tile + 1);
-      }
+      free_slot();
     }
 
     // ---- the four warps' results meet
-    __syncwarp();
-    float* out = reinterpret_cast<float*>(kst);
+    float* out = reinterpret_cast<float*>(smem + S::kOut);
+    float* mine = out + w * S::kOutWarp + g;
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
+    for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
-        float a = l[nt][k], b = hv[nt][k];
-#pragma unroll
-        for (int x = 4; x < 32; x <<= 1) {
-          a += __shfl_xor_sync(~0u, a, x);
-          b += __shfl_xor_sync(~0u, b, x);
-        }
+        const int rr = nt * 8 + 2 * t4 + k;
+        const float den = sum_over_rows(l[nt][k]), half = 0.5f * sum_over_rows(hv[nt][k]);
         if (g == 0) {
-          sm_m[w][nt * 8 + 2 * t4 + k] = m[nt][k];
-          sm_l[w][nt * 8 + 2 * t4 + k] = a;
-          sm_h[w][nt * 8 + 2 * t4 + k] = 0.5f * b;
+          sm_m[w][rr] = m[nt][k];
+          sm_l[w][rr] = den;
+          sm_h[w][rr] = half;
+        }
+#pragma unroll
+        for (int s = 0; s < 2 * C32; ++s) {
+          mine[rr * (D + 4) + 16 * s] = o[s][nt][k];
+          mine[rr * (D + 4) + 16 * s + 8] = o[s][nt][k + 2];
         }
       }
-      float* o0 = out + (nt * 8 + 2 * t4) * (D + 4) + g;
-#pragma unroll
-      for (int c = 0; c < C32; ++c)
-#pragma unroll
-        for (int s = 0; s < 2; ++s) {
-          o0[32 * c + 16 * s] = o[c][s][nt][0];
-          o0[32 * c + 16 * s + D + 4] = o[c][s][nt][1];
-          o0[32 * c + 16 * s + 8] = o[c][s][nt][2];
-          o0[32 * c + 16 * s + 8 + D + 4] = o[c][s][nt][3];
-        }
-    }
-    __syncthreads();
-    const bool partial = nseg > 1;
-    const long long slot = (long long)sm_slot[r] + seg;
-    const bool room = !partial || (slot < p.slots && rows <= p.row_cap);
+    math_barrier();
+    const bool partial = x.nseg > 1;
+    const long long part_slot = (long long)x.slot + x.seg;
+    const bool room = !partial || (part_slot < p.slots && x.rows <= p.row_cap);
     if (!room && tid == 0) atomicOr(&g_kv8_errors, 2u);
-    for (int x = tid; x < RB * (D / 4); x += kThreads) {
-      const int rr = x / (D / 4), d = (x - rr * (D / 4)) * 4, row = row0 + rr;
-      if (row >= rows || !room) continue;
+    const int live_rows = room ? min(RB, x.rows - x.row0) : 0;
+    for (int e = tid; e < live_rows * (D / 4); e += kMath) {
+      const int rr = e / (D / 4), d = (e - rr * (D / 4)) * 4, row = x.row0 + rr;
       float mm = sm_m[0][rr];
 #pragma unroll
       for (int i = 1; i < kWarps; ++i) mm = fmaxf(mm, sm_m[i][rr]);
@@ -595,14 +703,13 @@ __global__ void __launch_bounds__(kThreads) attn_kv8_kernel(const AttnKV8Params 
       float den = 0.f, hs = 0.f;
 #pragma unroll
       for (int i = 0; i < kWarps; ++i) {
-        if (sm_l[i][rr] == 0.f) continue;  // the warp's positions are none of the row's
-        const float f = fast_exp2(sm_m[i][rr] - mb);
-        const float4 v = *reinterpret_cast<const float4*>(smem + i * S::kWarpBytes + (rr * (D + 4) + d) * 4);
+        const float li = sm_l[i][rr], f = li == 0.f ? 0.f : fast_exp2(sm_m[i][rr] - mb);
+        const float4 v = *reinterpret_cast<const float4*>(out + i * S::kOutWarp + rr * (D + 4) + d);
         sum.x += f * v.x;
         sum.y += f * v.y;
         sum.z += f * v.z;
         sum.w += f * v.w;
-        den += f * sm_l[i][rr];
+        den += f * li;
         hs += f * sm_h[i][rr];
       }
       sum.x += hs;
@@ -610,82 +717,111 @@ __global__ void __launch_bounds__(kThreads) attn_kv8_kernel(const AttnKV8Params 
       sum.z += hs;
       sum.w += hs;
       if (partial) {
-        const long long at = (slot * p.n_kv + h) * p.row_cap + row;
-        *reinterpret_cast<float4*>(p.part + at * D + d) = sum;
-        if (d == 0) p.part_ml[at] = make_float2(mm, den);
+        const long long to = (part_slot * p.n_kv + x.h) * p.row_cap + row;
+        *reinterpret_cast<float4*>(p.part + to * D + d) = sum;
+        if (d == 0) p.part_ml[to] = make_float2(mm, den);
       } else {
         const float inv = den == 0.f ? 0.f : 1.f / den;
-        const int i = row / p.group;
-        const long long at = (tok0 + i) * p.os + (long long)(h * p.group + row - i * p.group) * D + d;
-        if (p.o_f32) {
-          *reinterpret_cast<float4*>(static_cast<float*>(p.o) + at) = make_float4(sum.x * inv, sum.y * inv, sum.z * inv, sum.w * inv);
-        } else {
-          *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.o) + at) =
+        const int ti = row / group;
+        const long long to = (x.tok0 + ti) * p.os + (long long)(x.h * group + row - ti * group) * D + d;
+        if (p.o_f32)
+          *reinterpret_cast<float4*>(static_cast<float*>(p.o) + to) = make_float4(sum.x * inv, sum.y * inv, sum.z * inv, sum.w * inv);
+        else
+          *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.o) + to) =
               make_uint2((uint32_t)f32_to_bf16_rn(sum.x * inv) | (uint32_t)f32_to_bf16_rn(sum.y * inv) << 16,
                          (uint32_t)f32_to_bf16_rn(sum.z * inv) | (uint32_t)f32_to_bf16_rn(sum.w * inv) << 16);
-        }
       }
     }
-    fence_proxy_async_smem();  // the next copies overwrite what was read above
-    __syncthreads();
+    math_barrier();
   }
-  if (dead) atomicOr(&g_kv8_errors, 1u);
+  if (dead && lane == 0) atomicOr(&g_kv8_errors, 1u);
 }
 
-// The segments of a request added in order: one CTA per (token, query head), its eight warps each
-// taking every eighth segment, then warp 0 the eight sums.
+// The segments of a request added up: 1 to 8 warps of a CTA per (token, query head), each taking every
+// k-th segment in order, lane j holding the weight of its j-th; then the warps' sums in warp order.
 template <int D>
 __global__ void __launch_bounds__(kCombThreads) attn_kv8_combine_kernel(const AttnKV8Params p) {
   constexpr int W = kCombThreads / 32, E = D / 32;
-  extern __shared__ int sm_req[];
+  extern __shared__ __align__(16) int sm_req[];
   __shared__ int sm_scan[3 * W];
-  __shared__ float sm_o[W][D], sm_mx[W], sm_sum[W];
-  int *sm_tok = sm_req, *sm_item = sm_tok + p.B + 1, *sm_slot = sm_item + p.B + 1;
+  __shared__ float sm_o[W][D], sm_sum[W];
+  Request* req = reinterpret_cast<Request*>(sm_req);
   const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
+  // the lengths were written before the attention kernel passed its own wait, after which alone this
+  // kernel can start
+  scan_requests<kCombThreads, false>(p, 1, req, sm_scan);
   grid_dependency_wait();
-  scan_requests<kCombThreads, false>(p, 1, sm_tok, sm_item, sm_slot, sm_scan);
-  const int n_q = p.n_kv * p.group;
-  const long long total = (long long)sm_item[p.B] * n_q;
-  for (long long it = blockIdx.x; it < total; it += gridDim.x) {
-    const int ti = (int)(it / n_q), hq = (int)(it - (long long)ti * n_q);
-    const int r = find_request(sm_item, p.B, ti), i = ti - sm_item[r];
-    const int n = p.fresh[r], nseg = segments(p.ctx[r] + n), h = hq / p.group, row = i * p.group + hq - h * p.group;
-    if ((long long)sm_slot[r] + nseg > p.slots || n * p.group > p.row_cap) continue;
-    const long long first = ((long long)sm_slot[r] * p.n_kv + h) * p.row_cap + row, step = (long long)p.n_kv * p.row_cap;
-    float mx = -INFINITY;
-    for (int s = lane; s < nseg; s += 32) mx = fmaxf(mx, p.part_ml[first + s * step].x);
-#pragma unroll
-    for (int x = 1; x < 32; x <<= 1) mx = fmaxf(mx, __shfl_xor_sync(~0u, mx, x));
-    const float mb = mx == -INFINITY ? 0.f : mx;
+  const int n_q = p.n_kv * p.group, total = req[p.B].item;
+  for (int it = blockIdx.x; it < total; it += gridDim.x) {
+    const int r = find_request(req, p.B, it), local = it - req[r].item, tok0 = req[r].tok;
+    const int n = req[r + 1].tok - tok0, nseg = segments(req[r].ctx + n);
+    if ((long long)req[r].slot + nseg > p.slots || n * p.group > p.row_cap) continue;
+    const int k = combine_warps(nseg), sub = w & (k - 1);
+    const int task = (local * W + w) / k;  // (token, query head) of the request
+    const bool live = task < n * n_q;
+    const int i = task / n_q, hq = task - i * n_q, h = hq / p.group, row = i * p.group + hq - h * p.group;
+    const long long first = ((long long)req[r].slot * p.n_kv + h) * p.row_cap + row, step = (long long)p.n_kv * p.row_cap;
     float acc[E], den = 0.f;
 #pragma unroll
     for (int e = 0; e < E; ++e) acc[e] = 0.f;
-#pragma unroll 4
-    for (int s = w; s < nseg; s += W) {
-      const float2 ml = p.part_ml[first + s * step];
-      const float* src = p.part + (first + s * step) * D + lane * E;
-      const float f = ml.y == 0.f ? 0.f : fast_exp2(ml.x - mb);
-      den += f * ml.y;
+    if (live) {
+      float mx = -INFINITY;
+      for (int s = lane; s < nseg; s += 32) mx = fmaxf(mx, p.part_ml[first + s * step].x);
 #pragma unroll
-      for (int e = 0; e < E; ++e) acc[e] += f * src[e];
-    }
-#pragma unroll
-    for (int e = 0; e < E; ++e) sm_o[w][lane * E + e] = acc[e];
-    if (lane == 0) sm_sum[w] = den;
-    __syncthreads();
-    if (tid < D) {
-      float v = 0.f, dn = 0.f;
-#pragma unroll
-      for (int k = 0; k < W; ++k) {
-        v += sm_o[k][tid];
-        dn += sm_sum[k];
+      for (int x = 1; x < 32; x <<= 1) mx = fmaxf(mx, __shfl_xor_sync(~0u, mx, x));
+      const float mb = mx == -INFINITY ? 0.f : mx;
+      const int mine = (nseg - sub + k - 1) / k;  // segments sub + j k
+      for (int j0 = 0; j0 < mine; j0 += 32) {
+        float wt = 0.f;
+        if (j0 + lane < mine) {
+          const float2 ml = p.part_ml[first + (sub + (j0 + lane) * k) * step];
+          wt = ml.y == 0.f ? 0.f : fast_exp2(ml.x - mb);
+          den += wt * ml.y;
+        }
+        const int jn = min(32, mine - j0);
+#pragma unroll 8
+        for (int j = 0; j < jn; ++j) {
+          const float f = __shfl_sync(~0u, wt, j);
+          const float* src = p.part + (first + (sub + (j0 + j) * k) * step) * D + lane * E;
+          if (E == 4) {
+            const float4 v = *reinterpret_cast<const float4*>(src);
+            acc[0] += f * v.x;
+            acc[1] += f * v.y;
+            acc[E - 2] += f * v.z;
+            acc[E - 1] += f * v.w;
+          } else {
+            const float2 v = *reinterpret_cast<const float2*>(src);
+            acc[0] += f * v.x;
+            acc[1] += f * v.y;
+          }
+        }
       }
-      const float res = dn == 0.f ? 0.f : v * (1.f / dn);  // as a request of one segment
-      const long long at = (sm_tok[r] + i) * p.os + (long long)hq * D + tid;
-      if (p.o_f32) static_cast<float*>(p.o)[at] = res;
-      else static_cast<uint16_t*>(p.o)[at] = f32_to_bf16_rn(res);
+#pragma unroll
+      for (int x = 1; x < 32; x <<= 1) den += __shfl_xor_sync(~0u, den, x);
     }
-    __syncthreads();
+    if (k > 1) {  // uniform in the CTA
+#pragma unroll
+      for (int e = 0; e < E; ++e) sm_o[w][lane * E + e] = acc[e];
+      if (lane == 0) sm_sum[w] = den;
+      __syncthreads();
+      if (sub == 0) {
+        for (int j = 1; j < k; ++j) {
+          den += sm_sum[w + j];
+#pragma unroll
+          for (int e = 0; e < E; ++e) acc[e] += sm_o[w + j][lane * E + e];
+        }
+      }
+      __syncthreads();
+    }
+    if (live && sub == 0) {
+      const float inv = den == 0.f ? 0.f : 1.f / den;  // as a request of one segment
+      const long long at = (tok0 + i) * p.os + (long long)hq * D + lane * E;
+#pragma unroll
+      for (int e = 0; e < E; ++e) {
+        if (p.o_f32) static_cast<float*>(p.o)[at + e] = acc[e] * inv;
+        else static_cast<uint16_t*>(p.o)[at + e] = f32_to_bf16_rn(acc[e] * inv);
+      }
+    }
   }
 }
 
@@ -713,23 +849,25 @@ int launch_typed(const AttnKV8Params& p, int num_sms, cudaStream_t s, std::strin
     return -1;
   }
   if (launch_pdl(kernel, dim3(num_sms * per_sm), dim3(kThreads), smem, s, p, "attention_kv8", err) != 0) return -1;
-  if (p.max_len <= kTile) return 0;  // no request can have two segments
+  if (p.max_len <= kMinSegment) return 0;  // no request can have two segments
   const long long tasks = (long long)p.T * p.n_kv * p.group;
   const int grid = (int)(tasks < (long long)num_sms * 8 ? tasks : (long long)num_sms * 8);
-  return launch_pdl(attn_kv8_combine_kernel<D>, dim3(grid), dim3(kCombThreads), (size_t)3 * (p.B + 1) * 4, s, p,
+  return launch_pdl(attn_kv8_combine_kernel<D>, dim3(grid), dim3(kCombThreads), (size_t)(p.B + 1) * sizeof(Request), s, p,
                     "attention_kv8 combine", err);
 }
 
 template <int D>
 int launch_dim(const AttnKV8Params& p, int num_sms, cudaStream_t s, std::string* err) {
   const long long rows = (long long)p.max_new * p.group;
-  if (p.o_f32) return rows <= 8 ? launch_typed<D, 1, true>(p, num_sms, s, err) : launch_typed<D, 2, true>(p, num_sms, s, err);
+  if (p.o_f32)
+    return rows <= 8 ? launch_typed<D, 1, true>(p, num_sms, s, err)
+         : rows <= 16 ? launch_typed<D, 2, true>(p, num_sms, s, err) : launch_typed<D, 4, true>(p, num_sms, s, err);
   return rows <= 8 ? launch_typed<D, 1, false>(p, num_sms, s, err)
        : rows <= 16 ? launch_typed<D, 2, false>(p, num_sms, s, err) : launch_typed<D, 4, false>(p, num_sms, s, err);
 }
 
 size_t part_rows(int max_new, int n_q, int n_kv) { return (size_t)(n_q / n_kv) * (max_new < kSplitTokens ? max_new : kSplitTokens); }
-size_t part_slots(int B, long long total_len) { return (size_t)(total_len / kTile) + B; }
+size_t part_slots(int B, long long total_len) { return (size_t)(total_len / kMinSegment) + B; }
 
 }  // namespace
 

@@ -32,9 +32,9 @@ def test_cache_sizes(kq):
     assert L.kq_kv8_bytes(1 << 20, 128, 8, 128) == (1 << 20) * 128 * 8 * 128  # passes 32 bits
     for bad in ((-1, 32, 4, 128), (10, 24, 4, 128), (10, 32, 0, 128), (10, 32, 4, 96), (1 << 27, 16, 1, 64)):
         assert L.kq_kv8_bytes(*bad) == 0
-    # slots of 256 positions plus one per request, query rows of up to 32 tokens, D sums and two statistics
-    assert L.kq_attention_kv8_workspace_size(3, 1000, 1, 16, 4, 128) == (1000 // 256 + 3) * 4 * 4 * 130 * 4
-    assert L.kq_attention_kv8_workspace_size(3, 1000, 500, 16, 4, 128) == (1000 // 256 + 3) * 4 * 4 * 32 * 130 * 4
+    # slots of 512 positions plus one per request, query rows of up to 32 tokens, D sums and two statistics
+    assert L.kq_attention_kv8_workspace_size(3, 1000, 1, 16, 4, 128) == (1000 // 512 + 3) * 4 * 4 * 130 * 4
+    assert L.kq_attention_kv8_workspace_size(3, 1000, 500, 16, 4, 128) == (1000 // 512 + 3) * 4 * 4 * 32 * 130 * 4
     for bad in ((-1, 10, 1, 4, 4, 64), (4097, 10, 1, 4, 4, 64), (1, -1, 1, 4, 4, 64), (1, 10, 1, 6, 4, 64), (1, 10, 1, 4, 4, 80),
                 (1, 10, -1, 4, 4, 64), (1, 10, 1, 130, 2, 64)):
         assert L.kq_attention_kv8_workspace_size(*bad) == 0
