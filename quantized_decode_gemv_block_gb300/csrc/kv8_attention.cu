@@ -76,19 +76,26 @@ struct AttnKV8Params {
 };
 
 // log2 of a segment's positions: kMinSegment doubled until kMaxSegments hold the request.
-__device__ __forceinline__ int segment_log2(int len) {
+__host__ __device__ inline int segment_log2(int len) {
   constexpr int kBase = kMinSegment * kMaxSegments;
   static_assert((kBase & (kBase - 1)) == 0, "powers of two");
+  int log2 = 0;
+  while ((1 << log2) < kMinSegment) ++log2;  // a constant
+#ifdef __CUDA_ARCH__
   const int over = (len - 1) / kBase;
-  return __ffs(kMinSegment) - 1 + (over > 0 ? 32 - __clz(over) : 0);
+  return log2 + (over > 0 ? 32 - __clz(over) : 0);
+#else
+  for (int over = (len - 1) / kBase; over > 0; over >>= 1) ++log2;
+  return log2;
+#endif
 }
-__device__ __forceinline__ int segments(int len) {
+__host__ __device__ inline int segments(int len) {
   const int s = segment_log2(len);
   return (len + (1 << s) - 1) >> s;
 }
 
-// Warps that share a row of the combine: up to 16 segments each, and up to 8 warps.
-__device__ __forceinline__ int combine_warps(int nseg) { return nseg <= 16 ? 1 : nseg <= 32 ? 2 : nseg <= 64 ? 4 : 8; }
+// Warps that share a row of the combine: 8 segments each, and up to 8 warps.
+__host__ __device__ constexpr int combine_warps(int nseg) { return nseg <= 8 ? 1 : nseg <= 16 ? 2 : nseg <= 32 ? 4 : 8; }
 
 // A request whose lengths do not fit the call's bounds takes no part.
 __device__ __forceinline__ bool request_ok(const AttnKV8Params& p, int c, int n) {
@@ -183,11 +190,19 @@ __device__ __forceinline__ uint32_t movmatrix(uint32_t a) {
   asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(a));
   return d;
 }
-// Four int8 codes -> fp16 pairs: 1024 + (c + 128) by a byte permute under 0x64, minus 1152.
-__device__ __forceinline__ void codes_to_h2(uint32_t w, uint32_t& lo, uint32_t& hi) {
-  const uint32_t u = w ^ 0x80808080u;
-  lo = h2_sub(prmt(u, 0x64646464u, 0x4140), 0x64806480u);
-  hi = h2_sub(prmt(u, 0x64646464u, 0x4342), 0x64806480u);
+// Four int8 codes -> the fp16 pairs (0, 2) and (1, 3): c + 128 under the byte 0x64 is 1152 + c - 128 in
+// fp16 (1024 + u), one LOP3 per pair ((w & mask) ^ bits), minus 1152.
+__device__ __forceinline__ void codes_to_h2(uint32_t w, uint32_t& even, uint32_t& odd) {
+  uint32_t e, o;
+  asm("lop3.b32 %0, %1, 0x00FF00FF, 0x64806480, 0x6A;" : "=r"(e) : "r"(w));
+  asm("lop3.b32 %0, %1, 0x00FF00FF, 0x64806480, 0x6A;" : "=r"(o) : "r"(w >> 8));
+  even = h2_sub(e, 0x64806480u);
+  odd = h2_sub(o, 0x64806480u);
+}
+// Tokens (4 t, 4 t + 1) and (4 t + 2, 4 t + 3) of a row -> the pairs that codes_to_h2 makes.
+__device__ __forceinline__ void weight_operand(uint32_t (&b)[2], uint32_t lo, uint32_t hi) {
+  b[0] = prmt(lo, hi, 0x5410);
+  b[1] = prmt(lo, hi, 0x7632);
 }
 __device__ __forceinline__ float fast_exp2(float x) {
   float y;
@@ -230,11 +245,11 @@ struct AttnSmem {
 
 struct Item {  // (request, kv head, block of query rows, segment)
   int r, h, row0, rows, seg, nseg, ctx, len, tok0, slot;
-  int step0, step1, end;  // steps of kStep; positions from `end` on are seen by no row
+  int step0, step1, end, seen;  // steps of kStep; positions from `end` on are seen by no row, those below `seen` by all
 };
 
 template <int D, int NT, bool WIDE>
-__global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : NT == 2 ? 2 : 1) attn_kv8_kernel(const AttnKV8Params p) {
+__global__ void __launch_bounds__(kThreads, D == 64 ? (NT == 1 ? 4 : 3) : NT == 1 ? 3 : NT == 2 ? 2 : 1) attn_kv8_kernel(const AttnKV8Params p) {
   using S = AttnSmem<D, NT, WIDE>;
   constexpr int RB = S::RB, C32 = D / 32, DEPTH = S::kDepth;
   constexpr bool QREG = NT == 1;  // query operands stay in registers
@@ -298,6 +313,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : NT == 2 ? 2 : 1) attn_
     x.seg = local;
     x.row0 = rb * RB;
     x.end = p.mask || n == 1 ? x.len : x.ctx + (min(x.row0 + RB, x.rows) - 1) / p.group + 1;
+    x.seen = x.ctx + (p.mask ? 0 : x.row0 / p.group + 1);
     const int last = (x.end + kStep - 1) / kStep;
     x.step0 = cut ? x.seg << log2 : 0;
     x.step1 = cut ? min(x.step0 + (1 << log2), last) : last;
@@ -428,13 +444,13 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : NT == 2 ? 2 : 1) attn_
 #pragma unroll
       for (int s = 0; s < 2 * C32; ++s) {
         const float f[4] = {v[s][0] * up, v[s][1] * up, v[s][2] * up, v[s][3] * up};
-        const uint2 hi = make_uint2(f2_to_h2(f[0], f[1]), f2_to_h2(f[2], f[3]));
+        const uint2 hi = make_uint2(f2_to_h2(f[0], f[2]), f2_to_h2(f[1], f[3]));
         mma_f16_16816(half, halves, hi.x, hi.y, half);
         if (QREG) qh[QREG ? s : 0] = hi;
         else *reinterpret_cast<uint2*>(sm_q + ((nt * C32 + (s >> 1)) * 32 + lane) * 4 + 2 * (s & 1)) = hi;
         if (WIDE) {
-          const uint2 lo = make_uint2(f2_to_h2(f[0] - h_lo_to_f(hi.x), f[1] - h_lo_to_f(hi.x >> 16)),
-                                      f2_to_h2(f[2] - h_lo_to_f(hi.y), f[3] - h_lo_to_f(hi.y >> 16)));
+          const uint2 lo = make_uint2(f2_to_h2(f[0] - h_lo_to_f(hi.x), f[2] - h_lo_to_f(hi.x >> 16)),
+                                      f2_to_h2(f[1] - h_lo_to_f(hi.y), f[3] - h_lo_to_f(hi.y >> 16)));
           mma_f16_16816(half, halves, lo.x, lo.y, half);
           if (QREG) ql[QREG ? s : 0] = lo;
           else *reinterpret_cast<uint2*>(sm_q + NT * D * 4 + ((nt * C32 + (s >> 1)) * 32 + lane) * 4 + 2 * (s & 1)) = lo;
@@ -520,8 +536,11 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : NT == 2 ? 2 : 1) attn_
         }
       }
       free_slot();
+      const uint8_t* vst = smem + slot * S::kSlot + w * kWarpPos * D;
       // ---- weights against the page's largest score, up by 2^15 into fp16's range
       const int pos0 = step * kStep + w * kWarpPos + 4 * (g >> 1) + (g & 1);  // token of operand row g; row g + 8 is two on
+      // positions that every row sees (rows past the last come along: nothing reads them)
+      const bool all_seen = step * kStep + (w + 1) * kWarpPos <= x.seen;
       uint32_t wb[2][NT][2], wl[WIDE ? 2 : 1][NT][2];
       float fv[2][NT][2];
 #pragma unroll
@@ -529,7 +548,17 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : NT == 2 ? 2 : 1) attn_
         const int rr = nt * 8 + 2 * t4;
         const float2 rff = QREG ? make_float2(rf[0][0], rf[0][1]) : lds_f2(sm_rf + rr);
         const int lim0 = QREG ? lim[0][0] : sm_lim[rr], lim1 = QREG ? lim[0][1] : sm_lim[rr + 1];
-        if (p.mask == nullptr) {
+        if (all_seen) {
+#pragma unroll
+          for (int st = 0; st < 2; ++st) {
+            const float r0 = rff.x * kf[st], r1 = rff.y * kf[st];
+            float* s = sc[st][nt];
+            s[0] *= r0;
+            s[1] *= r1;
+            s[2] *= r0;
+            s[3] *= r1;
+          }
+        } else if (p.mask == nullptr) {
 #pragma unroll
           for (int st = 0; st < 2; ++st) {
             const int p0 = pos0 + 16 * st, p1 = p0 + 2;
@@ -606,11 +635,10 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : NT == 2 ? 2 : 1) attn_
         for (int st = 0; st < 2; ++st) {
           const float* s = sc[st][nt];
           const uint32_t e0 = f2_to_h2(s[0], s[1]), e1 = f2_to_h2(s[2], s[3]);
-          wb[st][nt][0] = movmatrix(e0);
-          wb[st][nt][1] = movmatrix(e1);
+          weight_operand(wb[st][nt], movmatrix(e0), movmatrix(e1));
           if (WIDE) {
-            wl[WIDE ? st : 0][nt][0] = movmatrix(f2_to_h2(s[0] - h_lo_to_f(e0), s[1] - h_lo_to_f(e0 >> 16)));
-            wl[WIDE ? st : 0][nt][1] = movmatrix(f2_to_h2(s[2] - h_lo_to_f(e1), s[3] - h_lo_to_f(e1 >> 16)));
+            weight_operand(wl[WIDE ? st : 0][nt], movmatrix(f2_to_h2(s[0] - h_lo_to_f(e0), s[1] - h_lo_to_f(e0 >> 16))),
+                           movmatrix(f2_to_h2(s[2] - h_lo_to_f(e1), s[3] - h_lo_to_f(e1 >> 16))));
           }
         }
         if (__any_sync(~0u, moved)) {
@@ -623,8 +651,6 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : NT == 2 ? 2 : 1) attn_
           }
         }
       }
-      // ---- values: a page's products are added up before its scale
-      const uint8_t* vst = smem + slot * S::kSlot + w * kWarpPos * D;
       wait(&sm_full[slot], phase);
 #pragma unroll
       for (int cc = 0; cc < C32; ++cc) {
@@ -817,9 +843,10 @@ __global__ void __launch_bounds__(kCombThreads) attn_kv8_combine_kernel(const At
       const float inv = den == 0.f ? 0.f : 1.f / den;  // as a request of one segment
       const long long at = (tok0 + i) * p.os + (long long)hq * D + lane * E;
 #pragma unroll
-      for (int e = 0; e < E; ++e) {
-        if (p.o_f32) static_cast<float*>(p.o)[at + e] = acc[e] * inv;
-        else static_cast<uint16_t*>(p.o)[at + e] = f32_to_bf16_rn(acc[e] * inv);
+      for (int e = 0; e < E; e += 2) {
+        const float v0 = acc[e] * inv, v1 = acc[e + 1] * inv;
+        if (p.o_f32) *reinterpret_cast<float2*>(static_cast<float*>(p.o) + at + e) = make_float2(v0, v1);
+        else *reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(p.o) + at + e) = (uint32_t)f32_to_bf16_rn(v0) | (uint32_t)f32_to_bf16_rn(v1) << 16;
       }
     }
   }
@@ -851,7 +878,9 @@ int launch_typed(const AttnKV8Params& p, int num_sms, cudaStream_t s, std::strin
   if (launch_pdl(kernel, dim3(num_sms * per_sm), dim3(kThreads), smem, s, p, "attention_kv8", err) != 0) return -1;
   if (p.max_len <= kMinSegment) return 0;  // no request can have two segments
   const long long tasks = (long long)p.T * p.n_kv * p.group;
-  const int grid = (int)(tasks < (long long)num_sms * 8 ? tasks : (long long)num_sms * 8);
+  // no more CTAs than the longest request's rows would need: each forms the prefix sums
+  const long long want = (tasks * combine_warps(segments(p.max_len)) + kCombThreads / 32 - 1) / (kCombThreads / 32);
+  const int grid = (int)(want < (long long)num_sms * 8 ? want : (long long)num_sms * 8);
   return launch_pdl(attn_kv8_combine_kernel<D>, dim3(grid), dim3(kCombThreads), (size_t)(p.B + 1) * sizeof(Request), s, p,
                     "attention_kv8 combine", err);
 }
@@ -861,9 +890,9 @@ int launch_dim(const AttnKV8Params& p, int num_sms, cudaStream_t s, std::string*
   const long long rows = (long long)p.max_new * p.group;
   if (p.o_f32)
     return rows <= 8 ? launch_typed<D, 1, true>(p, num_sms, s, err)
-         : rows <= 16 ? launch_typed<D, 2, true>(p, num_sms, s, err) : launch_typed<D, 4, true>(p, num_sms, s, err);
+         : launch_typed<D, 2, true>(p, num_sms, s, err);
   return rows <= 8 ? launch_typed<D, 1, false>(p, num_sms, s, err)
-       : rows <= 16 ? launch_typed<D, 2, false>(p, num_sms, s, err) : launch_typed<D, 4, false>(p, num_sms, s, err);
+       : launch_typed<D, 2, false>(p, num_sms, s, err);
 }
 
 size_t part_rows(int max_new, int n_q, int n_kv) { return (size_t)(n_q / n_kv) * (max_new < kSplitTokens ? max_new : kSplitTokens); }
