@@ -131,6 +131,8 @@ def _check(rc: int):
 
 def _stream(stream) -> int:
     if stream is None:
+        if torch.cuda.is_initialized():  # the same stream as below, without building a Stream object (6 us of 7)
+            return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
         return torch.cuda.current_stream().cuda_stream
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
@@ -296,23 +298,26 @@ def _dtype(t) -> int:
         raise TypeError("tensors must be torch.bfloat16 or torch.float32") from None
 
 
-def _i32(name: str, t: torch.Tensor, *shape) -> int:
-    """The address of a contiguous int32 tensor of at least the given shape's size."""
-    n = 1
-    for d in shape:
-        n *= d
-    if t.dtype != torch.int32 or not t.is_contiguous() or t.numel() < n:
+_I32 = torch.int32
+
+
+def _i32(name: str, t: torch.Tensor, n: int) -> int:
+    """The address of a contiguous int32 tensor of at least n elements."""
+    if t.dtype is not _I32 or t.numel() < n or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous int32 tensor of at least {n} elements")
     return t.data_ptr()
 
 
 def _heads(name: str, t: torch.Tensor, heads: int | None = None, dim: int | None = None) -> int:
     """The token stride of a (T, heads, dim) tensor whose heads stand next to each other."""
-    if t.dim() != 3 or (t.stride(2) != 1 and t.shape[2] > 1) or (t.stride(1) != t.shape[2] and t.shape[1] > 1):
+    if t.dim() != 3:
+        raise ValueError(f"{name} must be (tokens, heads, head_dim)")
+    (T, H, D), (s0, s1, s2) = t.shape, t.stride()
+    if (s2 != 1 and D > 1) or (s1 != D and H > 1):
         raise ValueError(f"{name} must be (tokens, heads, head_dim) with contiguous heads")
-    if (heads is not None and t.shape[1] != heads) or (dim is not None and t.shape[2] != dim):
-        raise ValueError(f"{name} must have {heads} heads of {dim}")
-    return t.stride(0) if t.shape[0] > 1 else t.shape[1] * t.shape[2]
+    if (heads is not None and H != heads) or (dim is not None and D != dim):
+        raise ValueError(f"{name} must have {heads if heads is not None else 'any number of'} heads of {dim}")
+    return s0 if T > 1 else H * D
 
 
 class PagesPlan:
@@ -321,7 +326,7 @@ class PagesPlan:
 
     def __init__(self, B: int, T: int, device="cuda"):
         buf = torch.empty(B + 1 + 2 * T + 2, dtype=torch.int32, device=device)
-        self.cu, self.pos, self.slot, self.n_free, self.status = buf.split((B + 1, T, T, 1, 1))
+        self.cu, self.pos, self.slot, self.n_free, self.status = buf.split_with_sizes((B + 1, T, T, 1, 1))
 
 
 def pages_plan(ctx_len: torch.Tensor, new_len: torch.Tensor, block_table: torch.Tensor, free_pages: torch.Tensor,
@@ -331,11 +336,16 @@ def pages_plan(ctx_len: torch.Tensor, new_len: torch.Tensor, block_table: torch.
     B, width = block_table.shape
     if out is None:
         out = PagesPlan(B, T, block_table.device)
+        base = out.cu.data_ptr()
+        outs = (base + 4 * (B + 1 + 2 * T), base, base + 4 * (B + 1), base + 4 * (B + 1 + T))
+        status = base + 4 * (B + 2 + 2 * T)
+    else:
+        outs = (_i32("out.n_free", out.n_free, 1), _i32("out.cu", out.cu, B + 1), _i32("out.pos", out.pos, T),
+                _i32("out.slot", out.slot, T))
+        status = _i32("out.status", out.status, 1)
     _check(lib().kq_pages_plan(_i32("ctx_len", ctx_len, B), _i32("new_len", new_len, B), B, page_size,
-                               _i32("block_table", block_table, B, width), width, _i32("free_pages", free_pages, 0),
-                               free_pages.numel(), _i32("n_free", n_free, 1), _i32("out.n_free", out.n_free, 1),
-                               _i32("out.cu", out.cu, B + 1), _i32("out.pos", out.pos, T), _i32("out.slot", out.slot, T),
-                               T, _i32("out.status", out.status, 1), _stream(stream)))
+                               _i32("block_table", block_table, B * width), width, _i32("free_pages", free_pages, 0),
+                               free_pages.numel(), _i32("n_free", n_free, 1), *outs, T, status, _stream(stream)))
     return out
 
 
@@ -349,7 +359,7 @@ def pages_release(length: torch.Tensor, done: torch.Tensor, block_table: torch.T
     if status is None:
         status = torch.empty(1, dtype=torch.int32, device=block_table.device)
     _check(lib().kq_pages_release(_i32("length", length, B), done.data_ptr(), B, page_size,
-                                  _i32("block_table", block_table, B, width), width, _i32("free_pages", free_pages, 0),
+                                  _i32("block_table", block_table, B * width), width, _i32("free_pages", free_pages, 0),
                                   free_pages.numel(), _i32("n_free", n_free, 1), _i32("n_free_out", n_free_out, 1),
                                   _i32("status", status, 1), _stream(stream)))
     return status
@@ -371,28 +381,32 @@ def rope(q: torch.Tensor | None, k: torch.Tensor | None, pos: torch.Tensor, inv_
         raise ValueError("inv_freq must be contiguous fp32")
     if pair_axis is not None and (pair_axis.dtype != torch.uint8 or not pair_axis.is_contiguous() or pair_axis.numel() != pairs):
         raise ValueError("pair_axis must be contiguous uint8, one per pair")
-    args, outs, y_dtype = [], [], None
-    for name, x, y in (("q", q, q_out), ("k", k, k_out)):
-        if x is None:
-            args.append((None, 0, None, 0, 0))
-            outs.append(None)
-            continue
-        if x.dtype != ref.dtype or x.shape[0] != T or x.shape[2] != D:
-            raise ValueError("q and k must agree in type, tokens and head_dim")
-        if y is None:
-            y = torch.empty(x.shape, dtype=out_dtype or x.dtype, device=x.device)
-        elif y.shape != x.shape or (out_dtype is not None and y.dtype != out_dtype):
-            raise ValueError(f"{name}_out must have {name}'s shape and out_dtype")
-        if y_dtype is not None and y.dtype != y_dtype:
-            raise ValueError("q_out and k_out must have one type")
-        y_dtype = y.dtype
-        args.append((x.data_ptr(), _heads(name, x), y.data_ptr(), _heads(name + "_out", y), x.shape[1]))
-        outs.append(y)
+    y_dtype = out_dtype or (q_out if q_out is not None else k_out if k_out is not None else ref).dtype
+    none = (None, 0, None, 0, 0)
+    qa = ka = none
+    if q is not None:
+        q_out, qa = _rope_side("q", q, q_out, ref, y_dtype)
+    if k is not None:
+        k_out, ka = _rope_side("k", k, k_out, ref, y_dtype)
     flags = (KQ_ROPE_ADJACENT if adjacent else 0) | (KQ_ROPE_INVERSE if inverse else 0)
-    _check(lib().kq_rope(_dtype(ref.dtype), _dtype(y_dtype), *args[0], *args[1], T, D, 2 * pairs,
-                         inv_freq.data_ptr(), pair_axis.data_ptr() if pair_axis is not None else None,
-                         _i32("pos", pos, axes, T), axes, flags, _stream(stream)))
-    return outs[0], outs[1]
+    _check(lib().kq_rope(_dtype(ref.dtype), _dtype(y_dtype), *qa, *ka, T, D, 2 * pairs, inv_freq.data_ptr(),
+                         pair_axis.data_ptr() if pair_axis is not None else None, _i32("pos", pos, axes * T), axes,
+                         flags, _stream(stream)))
+    return q_out if q is not None else None, k_out if k is not None else None
+
+
+def _rope_side(name, x, y, ref, y_dtype):
+    """The output of one of rope's tensors, and its five arguments."""
+    if x is not ref and (x.dtype is not ref.dtype or x.shape[0] != ref.shape[0] or x.shape[2] != ref.shape[2]):
+        raise ValueError("q and k must agree in type, tokens and head_dim")
+    xs = _heads(name, x)
+    H, D = x.shape[1], x.shape[2]
+    if y is None:
+        y = torch.empty(x.shape, dtype=y_dtype, device=x.device)
+        return y, (x.data_ptr(), xs, y.data_ptr(), H * D, H)
+    if y.shape != x.shape or y.dtype is not y_dtype:
+        raise ValueError(f"{name}_out must have {name}'s shape, and both outputs one type")
+    return y, (x.data_ptr(), xs, y.data_ptr(), _heads(name + "_out", y), H)
 
 
 class KV8CacheC(ctypes.Structure):
@@ -451,19 +465,21 @@ def attention_kv8(q: torch.Tensor, cache: KV8Cache, block_table: torch.Tensor, c
     if total_len is None:
         total_len = B * max_len
     if out is None:
-        out = torch.empty((T, n_q, D), dtype=out_dtype or q.dtype, device=q.device)
+        out, out_stride = torch.empty((T, n_q, D), dtype=out_dtype or q.dtype, device=q.device), n_q * D
     elif out.shape != q.shape or (out_dtype is not None and out.dtype != out_dtype):
         raise ValueError("out must have q's shape and out_dtype")
-    need = attention_kv8_workspace_size(B, total_len, max_new, n_q, cache.n_kv, D)
+    else:
+        out_stride = _heads("out", out, n_q, D)
     if workspace is None:
+        need = attention_kv8_workspace_size(B, total_len, max_new, n_q, cache.n_kv, D)
         workspace = torch.empty(max(need, 256), dtype=torch.uint8, device=q.device)
     _check(lib().kq_attention_kv8(cache._ref, _dtype(q.dtype), q.data_ptr(), _heads("q", q, None, cache.head_dim),
-                                  _dtype(out.dtype), out.data_ptr(), _heads("out", out, n_q, D), n_q,
+                                  _dtype(out.dtype), out.data_ptr(), out_stride, n_q,
                                   _i32("ctx_len", ctx_len, B), _i32("new_len", new_len, B), B, T, max_new, max_len,
-                                  total_len, _i32("block_table", block_table, B, width), width,
+                                  total_len, _i32("block_table", block_table, B * width), width,
                                   _i32("mask", mask, T) if mask is not None else None,
                                   D ** -0.5 if scale is None else scale, workspace.data_ptr(),
-                                  workspace.numel() * workspace.element_size(), _stream(stream)))
+                                  workspace.nbytes, _stream(stream)))
     return out
 
 

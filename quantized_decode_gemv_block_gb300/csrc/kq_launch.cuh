@@ -17,9 +17,9 @@ __device__ __forceinline__ void grid_launch_dependents() { asm volatile("griddep
 // while that kernel drains, and waits for it in grid_dependency_wait().
 template <typename Params>
 int launch_pdl(void (*kernel)(const Params), dim3 grid, dim3 block, size_t smem, cudaStream_t s, const Params& p,
-               const char* what, std::string* err) {
+               const char* what, std::string* err, bool smem_is_allowed = false) {
   cudaError_t e = cudaSuccess;
-  if (smem > 48 * 1024) e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  if (smem > 48 * 1024 && !smem_is_allowed) e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e == cudaSuccess) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = grid;

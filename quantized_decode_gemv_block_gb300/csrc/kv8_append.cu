@@ -9,10 +9,14 @@
 //
 // Bound by DRAM for prompts (k, v in once, one byte per value out), by latency for single tokens.
 // The tokens of one call that share a page stand next to each other with ascending slots (a run).
-// The CTA whose token range holds a run's first token takes the whole run for one head and one of
-// k / v: a pass for max|x| (16-byte loads), then a pass that reads the values again (from L1 / L2)
-// and writes codes in the cache's order (kv8.cuh), 16 bytes per thread where a group of 16 tokens
-// is whole. No CTA waits for another and no atomics meet in memory, so results never vary.
+// The CTA whose token range holds a run's first token takes the whole run, for one head's k or v or
+// for several of them where a page has few values. A thread holds 4 tokens x 8 dims of the page in
+// registers between the pass for max|x| and the coding, so k and v are read once; the codes of such
+// a tile are whole words of the cache's order (kv8.cuh), both for k (4 dims of a token) and for v
+// (4 tokens of a dim), so a thread shares no word with another and rewrites the ones that it must
+// shift without any exchange. A word's four codes are the low bytes of fma(x, 1 / s, 1.5 * 2^23)
+// rounded down: floor(x / s) in one instruction. No CTA waits for another and no atomics meet in
+// memory, so results never vary.
 #include <cuda_bf16.h>
 
 #include <cstdint>
@@ -26,7 +30,8 @@
 namespace kq {
 namespace {
 
-constexpr int kThreads = 128;
+constexpr int kThreads = 256;
+constexpr int MINB = 4;
 
 __device__ unsigned int g_kv8_append_errors = 0;  // bit 1: a slot beyond the cache's pages
 
@@ -36,37 +41,52 @@ struct AppendParams {
   int8_t* codes[2];
   float* scale[2];
   const int* slot;
-  int T, log2p, n_pages, n_kv, D, range;
+  int T, log2p, n_pages, n_kv, range;
 };
 
-template <typename X>
-__device__ __forceinline__ float value(const X* p);
-template <>
-__device__ __forceinline__ float value<float>(const float* p) { return *p; }
-template <>
-__device__ __forceinline__ float value<uint16_t>(const uint16_t* p) { return __uint_as_float((uint32_t)*p << 16); }
-
-__device__ __forceinline__ void value4(float (&v)[4], const float* p) {
-  const float4 x = *reinterpret_cast<const float4*>(p);
-  v[0] = x.x;
-  v[1] = x.y;
-  v[2] = x.z;
-  v[3] = x.w;
+// Eight dims of a token, raw.
+struct RowF32 {
+  uint4 a, b;
+};
+struct RowBf16 {
+  uint4 a;
+};
+__device__ __forceinline__ void load_row(RowF32& r, const float* p) {
+  r.a = reinterpret_cast<const uint4*>(p)[0];
+  r.b = reinterpret_cast<const uint4*>(p)[1];
 }
-__device__ __forceinline__ void value4(float (&v)[4], const uint16_t* p) {
-  const uint2 x = *reinterpret_cast<const uint2*>(p);
-  v[0] = __uint_as_float(x.x << 16);
-  v[1] = __uint_as_float(x.x & 0xFFFF0000u);
-  v[2] = __uint_as_float(x.y << 16);
-  v[3] = __uint_as_float(x.y & 0xFFFF0000u);
+__device__ __forceinline__ void load_row(RowBf16& r, const uint16_t* p) { r.a = *reinterpret_cast<const uint4*>(p); }
+__device__ __forceinline__ void clear_row(RowF32& r) { r.a = r.b = make_uint4(0u, 0u, 0u, 0u); }
+__device__ __forceinline__ void clear_row(RowBf16& r) { r.a = make_uint4(0u, 0u, 0u, 0u); }
+__device__ __forceinline__ unsigned top4(const uint4& v) {
+  constexpr unsigned M = 0x7FFFFFFFu;
+  return max(max(v.x & M, v.y & M), max(v.z & M, v.w & M));
+}
+// Largest |x| of the row by its fp32 bits: a NaN or infinity is above every finite value.
+__device__ __forceinline__ unsigned top_of(const RowF32& r) { return max(top4(r.a), top4(r.b)); }
+__device__ __forceinline__ unsigned top_of(const RowBf16& r) {
+  constexpr unsigned M = 0x7FFF7FFFu;
+  const unsigned m = __vmaxu2(__vmaxu2(r.a.x & M, r.a.y & M), __vmaxu2(r.a.z & M, r.a.w & M));
+  return max(m & 0xFFFF0000u, m << 16);
+}
+__device__ __forceinline__ void values(float (&v)[8], const RowF32& r) {
+  const unsigned w[8] = {r.a.x, r.a.y, r.a.z, r.a.w, r.b.x, r.b.y, r.b.z, r.b.w};
+#pragma unroll
+  for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(w[i]);
+}
+__device__ __forceinline__ void values(float (&v)[8], const RowBf16& r) {
+  const unsigned w[4] = {r.a.x, r.a.y, r.a.z, r.a.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    v[2 * i] = __uint_as_float(w[i] << 16);
+    v[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+  }
 }
 
-// floor(x * inv) as a byte; inv is a power of two (or 0: every code is 0). A negative x whose
-// product rounds to zero still has floor -1.
-__device__ __forceinline__ uint32_t code(float x, float inv) {
-  int c = __float2int_rd(x * inv);
-  if (x < 0.f && inv > 0.f) c = min(c, -1);
-  return (uint32_t)c & 0xFFu;
+// floor(x * inv) in the low byte; inv is a power of two, or 0 (code 0).
+__device__ __forceinline__ uint32_t code(float x, float inv) { return __float_as_uint(__fmaf_rd(x, inv, 12582912.f)); }
+__device__ __forceinline__ uint32_t pack4(uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+  return prmt(prmt(a, b, 0x0040), prmt(c, d, 0x0040), 0x5410);
 }
 
 // Each byte of w shifted right arithmetically by n (0..7).
@@ -77,113 +97,162 @@ __device__ __forceinline__ uint32_t shift_bytes(uint32_t w, int n) {
   return r;
 }
 
-template <typename X>
-__global__ void __launch_bounds__(kThreads) kv8_append_kernel(const AppendParams p) {
-  __shared__ int sm_run;
-  __shared__ unsigned sm_max[kThreads / 32];
-  const int tid = threadIdx.x, h = blockIdx.y, which = blockIdx.z;
-  const int P = 1 << p.log2p, D = p.D;
+// D dims. A thread holds two tiles of 4 tokens x 8 dims: one place of k and of v, or, for pages of more
+// than 256 tiles (BIG), two places of one of them.
+template <typename X, typename Row, int D, bool BIG>
+__global__ void __launch_bounds__(kThreads, sizeof(Row) == 16 ? MINB : 2) kv8_append_kernel(const AppendParams p) {
+  __shared__ unsigned sm_max[2][kThreads / 32], sm_lead[4], sm_ends[8];
+  __shared__ int sm_slot[257];  // slots of tokens t0 - 1 .. t0 + 255
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int P = 1 << p.log2p;
+  const int owners = BIG ? kThreads : (P / 4) * (D / 8);  // threads of one (page, head): whole warps
+  const int sub = tid / owners, tile0 = tid - sub * owners;
+  const int unit = blockIdx.y * (kThreads / owners) + sub;  // head; BIG: k's heads, then v's
+  const bool mine = unit < (BIG ? 2 : 1) * p.n_kv;
+  const int big_v = BIG && unit >= p.n_kv, h = big_v ? unit - p.n_kv : unit;
   grid_dependency_wait();
-  const int t0 = blockIdx.x * p.range, t1 = min(t0 + p.range, p.T);
-  for (int t = t0; t < t1; ++t) {
-    const int s0 = p.slot[t];
-    if (s0 < 0) continue;
-    const int page = s0 >> p.log2p, at = s0 & (P - 1);
-    if (page >= p.n_pages) {
-      if (tid == 0) atomicOr(&g_kv8_append_errors, 2u);
-      continue;
+  const int t0 = blockIdx.x * p.range, nt = min(p.range, p.T - t0);  // range <= 128
+  for (int i = tid; i < p.range + P && i < 257; i += kThreads) {
+    const int t = t0 - 1 + i;
+    sm_slot[i] = t >= 0 && t < p.T ? p.slot[t] : -1;
+  }
+  __syncthreads();
+  // the runs that begin in this CTA's tokens, and the tokens after which a run ends
+  {
+    const int s = sm_slot[1 + min(tid, p.range + P - 2)], before = sm_slot[min(tid, p.range + P - 2)];
+    const bool follows = s >= 0 && before == s - 1 && (s & (P - 1)) != 0;
+    bool lead = false;
+    if (tid < nt && s >= 0) {
+      const bool inside = (s >> p.log2p) < p.n_pages;
+      if (!inside) atomicOr(&g_kv8_append_errors, 2u);
+      lead = inside && !follows;
     }
-    if (t > 0 && at > 0 && p.slot[t - 1] == s0 - 1) continue;  // inside a run
-    // the run's length: up to the page's end
-    if (tid == 0) sm_run = min(P - at, p.T - t);
-    __syncthreads();
-    if (tid < min(P - at, p.T - t) && p.slot[t + tid] != s0 + tid) atomicMin(&sm_run, tid);
-    __syncthreads();
-    const int n = sm_run;
-    const long long xs = which ? p.xs[1] : p.xs[0];
-    const X* x = static_cast<const X*>(which ? p.x[1] : p.x[0]) + t * xs + (long long)h * D;
-    // largest |x| by its bits: a NaN or infinity is above every finite value
-    unsigned top = 0;
-    for (int i = tid; i < n * (D / 4); i += kThreads) {
-      const int j = i / (D / 4), d = (i - j * (D / 4)) * 4;
-      float v[4];
-      value4(v, x + j * xs + d);
-#pragma unroll
-      for (int e = 0; e < 4; ++e) top = max(top, __float_as_uint(v[e]) & 0x7FFFFFFFu);
+    const unsigned leads = __ballot_sync(~0u, lead), ends = __ballot_sync(~0u, !follows);
+    if (lane == 0) {
+      if (warp < 4) sm_lead[warp] = leads;
+      sm_ends[warp] = ends;
     }
-    top = __reduce_max_sync(~0u, top);
-    if ((tid & 31) == 0) sm_max[tid >> 5] = top;
-    __syncthreads();
-#pragma unroll
-    for (int i = 0; i < kThreads / 32; ++i) top = max(top, sm_max[i]);
-    float* sp = (which ? p.scale[1] : p.scale[0]) + (long long)page * p.n_kv + h;
-    const float old = at ? *sp : 0.f;  // a run from offset 0 starts the page afresh
-    const unsigned ex = top >> 23;
-    float need = top == 0 ? 0.f : __uint_as_float((ex > 7 ? ex - 6 : 1u) << 23);  // never below 2^-126
-    if (ex == 0xFF) need = __uint_as_float(0x7FC00000u);
-    const bool broken = old != old || need != need;
-    const float now = broken ? __uint_as_float(0x7FC00000u) : fmaxf(old, need);
-    const float inv = broken || now == 0.f ? 0.f : __uint_as_float((254u - (__float_as_uint(now) >> 23)) << 23);
-    int shift = 0;
-    if (!broken && old > 0.f && now > old)
-      shift = min((int)(__float_as_uint(now) >> 23) - (int)(__float_as_uint(old) >> 23), 7);
-    __syncthreads();  // every thread has read the old scale and the maxima
-    if (tid == 0) *sp = now;
-    int8_t* codes = (which ? p.codes[1] : p.codes[0]) + ((long long)page * p.n_kv + h) * P * D;
-    const int g0 = shift ? 0 : at >> 4, g1 = shift ? P >> 4 : (at + n + 15) >> 4;
-    for (int i = tid; i < (g1 - g0) * D; i += kThreads) {
-      const int grp = g0 + i / D, ci = i % D, c = ci >> 5, g = (ci >> 2) & 7, q4 = ci & 3;
-      uint4* dst = reinterpret_cast<uint4*>(codes + grp * 16 * D + ci * 16);
-      const int rel = grp * 16 - at;  // the group's first token in the run
-      uint32_t w[4], m[4];
-#pragma unroll
-      for (int k = 0; k < 4; ++k) w[k] = m[k] = 0;
-      if (which == 0) {
-#pragma unroll
-        for (int half = 0; half < 2; ++half) {
-          const int j = rel + 4 * (g >> 1) + 2 * half + (g & 1);
-          if (j < 0 || j >= n) continue;
-#pragma unroll
-          for (int s = 0; s < 2; ++s) {
-            float v[4];
-            value4(v, x + j * xs + 32 * c + 16 * s + 4 * q4);
-            w[2 * s + half] = code(v[0], inv) | code(v[1], inv) << 8 | code(v[2], inv) << 16 | code(v[3], inv) << 24;
-            m[2 * s + half] = ~0u;
-          }
+  }
+  __syncthreads();
+#pragma unroll 1
+  for (int q = 0; q < 4; ++q) {
+#pragma unroll 1
+    for (unsigned bits = sm_lead[q]; bits; bits &= bits - 1) {
+      const int at_token = 32 * q + __ffs(bits) - 1, t = t0 + at_token;
+      const int s0 = sm_slot[1 + at_token], page = s0 >> p.log2p, at = s0 & (P - 1);
+      // the run's length, up to the page's end: to the first token that does not follow
+      int n = min(P - at, p.T - t);
+      for (int i = (at_token + 1) >> 5, from = (at_token + 1) & 31; i < 8 && 32 * i < at_token + n; ++i, from = 0) {
+        const unsigned e = sm_ends[i] >> from << from;
+        if (e) {
+          n = min(n, 32 * i + __ffs(e) - 1 - at_token);
+          break;
         }
-      } else {
+      }
+      // this thread's values of the page and the largest of all
+      Row rows[2][4];
+      unsigned top[2];
+      float old[2];
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const bool v = BIG ? big_v : i == 1;
+        const long long xs = v ? p.xs[1] : p.xs[0];
+        const X* x = static_cast<const X*>(v ? p.x[1] : p.x[0]) + t * xs + (long long)h * D;
+        const int tile = tile0 + (BIG ? i * kThreads : 0), d = tile % (D / 8) * 8, j0 = tile / (D / 8) * 4 - at;
 #pragma unroll
         for (int b = 0; b < 4; ++b) {
-          const int j = rel + 4 * q4 + b;
-          if (j < 0 || j >= n) continue;
+          if (mine && j0 + b >= 0 && j0 + b < n) load_row(rows[i][b], x + (j0 + b) * xs + d);
+          else clear_row(rows[i][b]);
+        }
+        // a run from offset 0 starts the page afresh
+        old[i] = mine && at ? (v ? p.scale[1] : p.scale[0])[(long long)page * p.n_kv + h] : 0.f;
+      }
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            w[k] |= code(value<X>(x + j * xs + 32 * c + 8 * k + g), inv) << (8 * b);
-            m[k] |= 0xFFu << (8 * b);
+      for (int i = 0; i < 2; ++i) {
+        top[i] = max(max(top_of(rows[i][0]), top_of(rows[i][1])), max(top_of(rows[i][2]), top_of(rows[i][3])));
+        top[i] = __reduce_max_sync(~0u, top[i]);
+        if (lane == 0) sm_max[i][warp] = top[i];
+      }
+      __syncthreads();  // also: every thread has read the old scales
+      for (int i = 0; i < owners / 32; ++i) {
+        top[0] = max(top[0], sm_max[0][sub * (owners / 32) + i]);
+        top[1] = max(top[1], sm_max[1][sub * (owners / 32) + i]);
+      }
+      if (BIG) top[0] = top[1] = max(top[0], top[1]);
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const bool v = BIG ? big_v : i == 1;
+        const unsigned ex = top[i] >> 23;
+        float need = top[i] == 0 ? 0.f : __uint_as_float((ex > 6 ? ex - 6 : 1u) << 23);  // never below 2^-126
+        if (ex == 0xFF) need = __uint_as_float(0x7FC00000u);
+        const bool broken = old[i] != old[i] || need != need;
+        const float now = broken ? __uint_as_float(0x7FC00000u) : fmaxf(old[i], need);
+        const float inv = broken || now == 0.f ? 0.f : __uint_as_float((254u - (__float_as_uint(now) >> 23)) << 23);
+        int shift = 0;
+        if (!broken && old[i] > 0.f && now > old[i])
+          shift = min((int)(__float_as_uint(now) >> 23) - (int)(__float_as_uint(old[i]) >> 23), 7);
+        if (mine && tile0 == 0 && !(BIG && i == 1)) (v ? p.scale[1] : p.scale[0])[(long long)page * p.n_kv + h] = now;
+        const int tile = tile0 + (BIG ? i * kThreads : 0), e = tile % (D / 8), quad = tile / (D / 8), j0 = quad * 4 - at;
+        unsigned in = 0;  // which of the four tokens are the run's
+#pragma unroll
+        for (int b = 0; b < 4; ++b) in |= (j0 + b >= 0 && j0 + b < n ? 1u : 0u) << b;
+        if (!mine || (in == 0 && shift == 0)) continue;
+        uint32_t c[4][8];
+#pragma unroll
+        for (int b = 0; b < 4; ++b) {
+          float val[8];
+          values(val, rows[i][b]);
+#pragma unroll
+          for (int k = 0; k < 8; ++k) c[b][k] = code(val[k], inv);
+        }
+        // (group of 16 tokens, 32 dims, word of 4 tokens or of 4 dims): see kv8.cuh
+        int8_t* base = (v ? p.codes[1] : p.codes[0]) + ((long long)page * p.n_kv + h) * P * D + (quad >> 2) * 16 * D + (e >> 2) * 512;
+        if (!v) {
+          // tokens 2 o + {0, 1} and two on (adjacent words), dims 8 e + 4 k ..
+#pragma unroll
+          for (int o = 0; o < 2; ++o)
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+              uint32_t w0 = pack4(c[o][4 * k], c[o][4 * k + 1], c[o][4 * k + 2], c[o][4 * k + 3]);
+              uint32_t w1 = pack4(c[o + 2][4 * k], c[o + 2][4 * k + 1], c[o + 2][4 * k + 2], c[o + 2][4 * k + 3]);
+              uint2* dst = reinterpret_cast<uint2*>(base + ((quad & 3) * 2 + o) * 64 + ((e & 1) * 2 + k) * 16 + (e >> 1 & 1) * 8);
+              const bool i0 = in >> o & 1, i1 = in >> (o + 2) & 1;
+              if (shift && !(i0 && i1)) {
+                const uint2 was = *dst;
+                if (!i0) w0 = shift_bytes(was.x, shift);
+                if (!i1) w1 = shift_bytes(was.y, shift);
+              }
+              if ((i0 && i1) || shift) *dst = make_uint2(w0, w1);
+              else if (i0) reinterpret_cast<uint32_t*>(dst)[0] = w0;
+              else if (i1) reinterpret_cast<uint32_t*>(dst)[1] = w1;
+            }
+        } else {
+          const uint32_t in4 = (in & 1 ? 0xFFu : 0u) | (in & 2 ? 0xFF00u : 0u) | (in & 4 ? 0xFF0000u : 0u) | (in & 8 ? 0xFF000000u : 0u);
+#pragma unroll
+          for (int k = 0; k < 8; ++k) {  // dim 8 e + k of the four tokens
+            uint32_t word = pack4(c[0][k], c[1][k], c[2][k], c[3][k]);
+            uint32_t* dst = reinterpret_cast<uint32_t*>(base + k * 64 + (quad & 3) * 16 + (e >> 1 & 1) * 8 + (e & 1) * 4);
+            if (in != 15u && shift) word = (shift_bytes(*dst, shift) & ~in4) | (word & in4);
+            if (in == 15u || shift) {
+              *dst = word;
+            } else {
+#pragma unroll
+              for (int b = 0; b < 4; ++b)
+                if (in >> b & 1) reinterpret_cast<uint8_t*>(dst)[b] = (uint8_t)(word >> (8 * b));
+            }
           }
         }
       }
-      if ((m[0] & m[1] & m[2] & m[3]) == ~0u) {
-        *dst = make_uint4(w[0], w[1], w[2], w[3]);
-      } else if (shift) {
-        const uint4 o = *dst;
-        *dst = make_uint4((shift_bytes(o.x, shift) & ~m[0]) | w[0], (shift_bytes(o.y, shift) & ~m[1]) | w[1],
-                          (shift_bytes(o.z, shift) & ~m[2]) | w[2], (shift_bytes(o.w, shift) & ~m[3]) | w[3]);
-      } else {
-        uint32_t* dw = reinterpret_cast<uint32_t*>(dst);
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          if (m[k] == ~0u) dw[k] = w[k];
-          else if (m[k]) {
-#pragma unroll
-            for (int b = 0; b < 4; ++b)
-              if (m[k] >> (8 * b) & 1) reinterpret_cast<uint8_t*>(dw + k)[b] = (uint8_t)(w[k] >> (8 * b));
-          }
-        }
-      }
+      __syncthreads();  // the shared words are used again by the next run
     }
-    __syncthreads();  // the shared words are used again by the next run
   }
+}
+
+template <typename X, typename Row>
+int launch_typed(const AppendParams& p, int D, dim3 grid, bool two, cudaStream_t s, std::string* err) {
+  if (two) return launch_pdl(kv8_append_kernel<X, Row, 128, true>, grid, dim3(kThreads), 0, s, p, "kv8_append", err);
+  return D == 64 ? launch_pdl(kv8_append_kernel<X, Row, 64, false>, grid, dim3(kThreads), 0, s, p, "kv8_append", err)
+                 : launch_pdl(kv8_append_kernel<X, Row, 128, false>, grid, dim3(kThreads), 0, s, p, "kv8_append", err);
 }
 
 }  // namespace
@@ -211,14 +280,15 @@ int launch_kv8_append(const KV8Args& c, int x_dtype, const void* k, long long ks
   p.log2p = c.log2p;
   p.n_pages = c.n_pages;
   p.n_kv = c.n_kv;
-  p.D = c.D;
   // tokens per CTA: one while the grid is small (runs are short: single tokens in parallel), up to a page
-  const long long units = (long long)T * c.n_kv * 2;
-  long long range = units / ((long long)num_sms * 16);
+  const int tiles = (1 << c.log2p) / 4 * (c.D / 8), heads = tiles < kThreads ? kThreads / tiles : 1;
+  const bool two = tiles > kThreads;  // pages of 128 tokens of 128 dims
+  const unsigned gy = two ? 2u * c.n_kv : (unsigned)((c.n_kv + heads - 1) / heads);
+  const long long range = (long long)T * gy / ((long long)num_sms * 8);
   p.range = (int)(range < 1 ? 1 : range > (1 << c.log2p) ? (1 << c.log2p) : range);
-  const dim3 grid((unsigned)((T + p.range - 1) / p.range), (unsigned)c.n_kv, 2);
-  return x_dtype == KQ_F32 ? launch_pdl(kv8_append_kernel<float>, grid, dim3(kThreads), 0, s, p, "kv8_append", err)
-                           : launch_pdl(kv8_append_kernel<uint16_t>, grid, dim3(kThreads), 0, s, p, "kv8_append", err);
+  const dim3 grid((unsigned)((T + p.range - 1) / p.range), gy);
+  return x_dtype == KQ_F32 ? launch_typed<float, RowF32>(p, c.D, grid, two, s, err)
+                           : launch_typed<uint16_t, RowBf16>(p, c.D, grid, two, s, err);
 }
 
 }  // namespace kq

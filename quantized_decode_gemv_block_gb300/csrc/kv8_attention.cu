@@ -109,64 +109,66 @@ struct Request {
   int tok, item, slot, ctx;
 };
 template <int THREADS, bool ITEMS>
-__device__ __forceinline__ void scan_requests(const AttnKV8Params& p, int row_block, Request* req, int* sm) {
+__device__ __forceinline__ void scan_requests(const AttnKV8Params& p, int row_block, Request* req, long long* sm) {
   constexpr int W = THREADS / 32;
   const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
+  const int per = (p.B + THREADS - 1) / THREADS, r0 = min(tid * per, p.B), r1 = min(r0 + per, p.B);  // this thread's requests
+  long long a = 0;  // sums within them, then before them
+  int b = 0, c = 0;
+  bool bad = false;
+#pragma unroll 2
+  for (int r = r0; r < r1; ++r) {
+    const int n = p.fresh[r], ctx = p.ctx[r];
+    req[r] = {(int)min(a, (long long)INT_MAX), b, c, ctx};
+    a += n > 0 ? n : 0;
+    if (!request_ok(p, ctx, n)) bad = true;
+    else if (n > 0) {
+      const int nseg = n <= kSplitTokens ? segments(ctx + n) : 1, rows = n * p.group;
+      if (ITEMS) b += (rows + row_block - 1) / row_block * nseg;
+      else b += nseg <= 1 ? 0 : (rows * p.n_kv * combine_warps(nseg) + W - 1) / W;
+      c += nseg > 1 ? nseg : 0;
+    }
+  }
+  const long long a0 = a;
+  const int b0 = b, c0 = c;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long xa = __shfl_up_sync(~0u, a, o);
+    const int xb = __shfl_up_sync(~0u, b, o), xc = __shfl_up_sync(~0u, c, o);
+    if (lane >= o) {
+      a += xa;
+      b += xb;
+      c += xc;
+    }
+  }
+  if (lane == 31) {
+    sm[w] = a;
+    sm[W + w] = b;
+    sm[2 * W + w] = c;
+  }
+  __syncthreads();
   long long ct = 0;
   int ci = 0, cs = 0;
-  bool bad = false;
-  for (int base = 0; base < p.B; base += THREADS) {
-    const int r = base + tid;
-    int a = 0, b = 0, c = 0, ctx = 0;
-    if (r < p.B) {
-      const int n = p.fresh[r];
-      ctx = p.ctx[r];
-      a = n > 0 ? min(n, p.T + 1) : 0;
-      if (request_ok(p, ctx, n)) {
-        if (n > 0) {
-          const int nseg = n <= kSplitTokens ? segments(ctx + n) : 1, rows = n * p.group;
-          if (ITEMS) b = (rows + row_block - 1) / row_block * nseg;
-          else b = nseg <= 1 ? 0 : (rows * p.n_kv * combine_warps(nseg) + W - 1) / W;
-          c = nseg > 1 ? nseg : 0;
-        }
-      } else {
-        bad = true;
-      }
-    }
-    const int a0 = a, b0 = b, c0 = c;
+  a -= a0;
+  b -= b0;
+  c -= c0;
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int xa = __shfl_up_sync(~0u, a, o), xb = __shfl_up_sync(~0u, b, o), xc = __shfl_up_sync(~0u, c, o);
-      if (lane >= o) {
-        a += xa;
-        b += xb;
-        c += xc;
-      }
+  for (int i = 0; i < W; ++i) {
+    const long long xa = sm[i];
+    const int xb = (int)sm[W + i], xc = (int)sm[2 * W + i];
+    if (i < w) {
+      a += xa;
+      b += xb;
+      c += xc;
     }
-    __syncthreads();
-    if (lane == 31) {
-      sm[w] = a;
-      sm[W + w] = b;
-      sm[2 * W + w] = c;
-    }
-    __syncthreads();
-    int pa = 0, pb = 0, pc = 0, ta = 0, tb = 0, tc = 0;
-#pragma unroll
-    for (int i = 0; i < W; ++i) {
-      const int xa = sm[i], xb = sm[W + i], xc = sm[2 * W + i];
-      if (i < w) {
-        pa += xa;
-        pb += xb;
-        pc += xc;
-      }
-      ta += xa;
-      tb += xb;
-      tc += xc;
-    }
-    if (r < p.B) req[r] = {(int)min(ct + pa + a - a0, (long long)INT_MAX), ci + pb + b - b0, cs + pc + c - c0, ctx};
-    ct += ta;
-    ci += tb;
-    cs += tc;
+    ct += xa;
+    ci += xb;
+    cs += xc;
+  }
+  for (int r = r0; r < r1; ++r) {
+    req[r].tok = (int)min(a + req[r].tok, (long long)INT_MAX);
+    req[r].item += b;
+    req[r].slot += c;
   }
   // more tokens than q has rows, or too many items: nothing is done
   const bool over = ct > p.T || (long long)ci * p.n_kv > INT_MAX;
@@ -256,7 +258,7 @@ __global__ void __launch_bounds__(kThreads, D == 64 ? (NT == 1 ? 4 : 3) : NT == 
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ __align__(8) uint64_t sm_full[DEPTH], sm_empty[DEPTH];
   __shared__ __align__(16) float sm_scale[4][2][kStep / 16];  // [step & 3][k, v][group]
-  __shared__ int sm_scan[3 * (kThreads / 32)];
+  __shared__ long long sm_scan[3 * (kThreads / 32)];
   __shared__ __align__(16) float sm_hq[RB], sm_rf[RB];  // read in pairs
   __shared__ float sm_m[kWarps][RB], sm_l[kWarps][RB], sm_h[kWarps][RB];
   __shared__ int sm_lim[RB];
@@ -769,7 +771,7 @@ template <int D>
 __global__ void __launch_bounds__(kCombThreads) attn_kv8_combine_kernel(const AttnKV8Params p) {
   constexpr int W = kCombThreads / 32, E = D / 32;
   extern __shared__ __align__(16) int sm_req[];
-  __shared__ int sm_scan[3 * W];
+  __shared__ long long sm_scan[3 * W];
   __shared__ float sm_o[W][D], sm_sum[W];
   Request* req = reinterpret_cast<Request*>(sm_req);
   const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
@@ -875,7 +877,7 @@ int launch_typed(const AttnKV8Params& p, int num_sms, cudaStream_t s, std::strin
     *err = std::string("attention_kv8: ") + (e != cudaSuccess ? cudaGetErrorString(e) : "the kernel does not fit an SM");
     return -1;
   }
-  if (launch_pdl(kernel, dim3(num_sms * per_sm), dim3(kThreads), smem, s, p, "attention_kv8", err) != 0) return -1;
+  if (launch_pdl(kernel, dim3(num_sms * per_sm), dim3(kThreads), smem, s, p, "attention_kv8", err, true) != 0) return -1;
   if (p.max_len <= kMinSegment) return 0;  // no request can have two segments
   const long long tasks = (long long)p.T * p.n_kv * p.group;
   // no more CTAs than the longest request's rows would need: each forms the prefix sums

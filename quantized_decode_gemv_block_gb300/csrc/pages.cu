@@ -23,8 +23,7 @@
 namespace kq {
 namespace {
 
-constexpr int kThreads = 256;
-constexpr int kWarps = kThreads / 32;
+constexpr int kMaxThreads = 1024;  // 256 for small batches, 1024 where requests or tokens are many
 
 struct PagesParams {
   const int* ctx;    // plan: cached length; release: held length
@@ -42,10 +41,10 @@ struct PagesParams {
   unsigned* status;
 };
 
-// Inclusive sums of (a, b) over the block's threads in thread order; every thread gets its own
-// sums and the totals. All threads call it; `sm` holds 2 * kWarps values.
+// Exclusive sums of (a, b) over the block's threads in thread order, and the totals. `sm` holds 64 values.
 __device__ __forceinline__ void block_scan2(long long& a, long long& b, long long& ta, long long& tb, long long* sm) {
-  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5, warps = blockDim.x >> 5;
+  const long long a0 = a, b0 = b;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
     const long long xa = __shfl_up_sync(~0u, a, o), xb = __shfl_up_sync(~0u, b, o);
@@ -54,25 +53,23 @@ __device__ __forceinline__ void block_scan2(long long& a, long long& b, long lon
       b += xb;
     }
   }
-  __syncthreads();  // the previous call's readers are done
   if (lane == 31) {
     sm[w] = a;
-    sm[kWarps + w] = b;
+    sm[32 + w] = b;
   }
   __syncthreads();
-  long long pa = 0, pb = 0;
-  ta = tb = 0;
+  long long pa = lane < w ? sm[lane] : 0, pb = lane < w ? sm[32 + lane] : 0;
+  ta = lane < warps ? sm[lane] : 0;
+  tb = lane < warps ? sm[32 + lane] : 0;
 #pragma unroll
-  for (int i = 0; i < kWarps; ++i) {
-    if (i < w) {
-      pa += sm[i];
-      pb += sm[kWarps + i];
-    }
-    ta += sm[i];
-    tb += sm[kWarps + i];
+  for (int o = 1; o < 32; o <<= 1) {
+    pa += __shfl_xor_sync(~0u, pa, o);
+    pb += __shfl_xor_sync(~0u, pb, o);
+    ta += __shfl_xor_sync(~0u, ta, o);
+    tb += __shfl_xor_sync(~0u, tb, o);
   }
-  a += pa;
-  b += pb;
+  a += pa - a0;
+  b += pb - b0;
 }
 
 // Largest r with s[r] <= x (s ascending, s[0] = 0 <= x): the request of token or page x, with
@@ -87,40 +84,42 @@ __device__ __forceinline__ int find_request(const int* s, int B, int x) {
   return lo;
 }
 
-__global__ void __launch_bounds__(kThreads) pages_plan_kernel(const PagesParams p) {
-  extern __shared__ int sm_cu[];  // B + 1 token prefixes, then B + 1 fresh-page prefixes
-  __shared__ long long sm_scan[2 * kWarps];
-  int* sm_pg = sm_cu + p.B + 1;
-  const int tid = threadIdx.x, P1 = (1 << p.log2p) - 1;
+__device__ __forceinline__ int clamp_int(long long v) { return (int)min(v, (long long)INT_MAX); }
+
+__global__ void __launch_bounds__(kMaxThreads) pages_plan_kernel(const PagesParams p) {
+  extern __shared__ int sm_cu[];  // B + 1 token prefixes, B + 1 fresh-page prefixes, B cached lengths
+  __shared__ long long sm_scan[64];
+  int *sm_pg = sm_cu + p.B + 1, *sm_ctx = sm_pg + p.B + 1;
+  const int tid = threadIdx.x, threads = blockDim.x, P1 = (1 << p.log2p) - 1;
   grid_dependency_wait();
   const int nfree = *p.n_free;
   unsigned bad = nfree < 0 || nfree > p.free_cap ? KQ_PAGES_BAD_ARG : 0u;
-  long long ct = 0, cp = 0;  // totals of the requests before this round of the loop
-  for (int base = 0; base < p.B; base += kThreads) {
-    const int r = base + tid;
-    long long a = 0, b = 0;
-    if (r < p.B) {
-      const int c = p.ctx[r], n = p.fresh[r];
-      if (c < 0 || n < 0) bad |= KQ_PAGES_BAD_ARG;
-      else {
-        const long long want = ((long long)c + n + P1) >> p.log2p;
-        if (want > p.max_blocks) bad |= KQ_PAGES_TABLE_FULL;
-        a = n;
-        b = want - (((long long)c + P1) >> p.log2p);
-      }
+  const int per = (p.B + threads - 1) / threads, r0 = min(tid * per, p.B), r1 = min(r0 + per, p.B);  // this thread's requests
+  long long a = 0, b = 0, ct, cp;
+#pragma unroll 4
+  for (int r = r0; r < r1; ++r) {
+    const int c = p.ctx[r], n = p.fresh[r];
+    long long pages = 0;
+    if (c < 0 || n < 0) bad |= KQ_PAGES_BAD_ARG;
+    else {
+      const long long want = ((long long)c + n + P1) >> p.log2p;
+      if (want > p.max_blocks) bad |= KQ_PAGES_TABLE_FULL;
+      pages = want - (((long long)c + P1) >> p.log2p);
     }
-    long long ta, tb, ia = a, ib = b;
-    block_scan2(ia, ib, ta, tb, sm_scan);
-    if (r < p.B) {  // clamped: a batch that overflows an int is refused below
-      sm_cu[r] = (int)min(ct + ia - a, (long long)INT_MAX);
-      sm_pg[r] = (int)min(cp + ib - b, (long long)INT_MAX);
-    }
-    ct += ta;
-    cp += tb;
+    sm_ctx[r] = c;
+    sm_cu[r] = clamp_int(a);  // within the thread's requests: the rest is added below
+    sm_pg[r] = clamp_int(b);
+    a += n > 0 ? n : 0;
+    b += pages;
+  }
+  block_scan2(a, b, ct, cp, sm_scan);
+  for (int r = r0; r < r1; ++r) {  // clamped: a batch that overflows an int is refused below
+    sm_cu[r] = clamp_int(a + sm_cu[r]);
+    sm_pg[r] = clamp_int(b + sm_pg[r]);
   }
   if (tid == 0) {
-    sm_cu[p.B] = (int)min(ct, (long long)INT_MAX);
-    sm_pg[p.B] = (int)min(cp, (long long)INT_MAX);
+    sm_cu[p.B] = clamp_int(ct);
+    sm_pg[p.B] = clamp_int(cp);
   }
   if (ct > p.T) bad |= KQ_PAGES_TOKENS_FULL;
   if (cp > nfree) bad |= KQ_PAGES_OUT_OF_PAGES;
@@ -135,9 +134,9 @@ __global__ void __launch_bounds__(kThreads) pages_plan_kernel(const PagesParams 
       *p.status = sm_bad;
       *p.n_free_out = bad ? nfree : nfree - (int)cp;
     }
-    for (int r = tid; r <= p.B; r += kThreads) p.cu[r] = bad ? 0 : sm_cu[r];
+    for (int r = tid; r <= p.B; r += threads) p.cu[r] = bad ? 0 : sm_cu[r];
   }
-  const int stride = gridDim.x * kThreads, first = blockIdx.x * kThreads + tid;
+  const int stride = gridDim.x * threads, first = blockIdx.x * threads + tid;
   if (bad) {  // nothing is handed out: every token is skipped by what follows, the table stays
     for (int t = first; t < p.T; t += stride) {
       p.pos[t] = 0;
@@ -148,13 +147,13 @@ __global__ void __launch_bounds__(kThreads) pages_plan_kernel(const PagesParams 
   const int nt = (int)ct, np = (int)cp;
   for (int j = first; j < np; j += stride) {
     const int r = find_request(sm_pg, p.B, j);
-    const int blk = (int)(((long long)p.ctx[r] + P1) >> p.log2p) + j - sm_pg[r];
+    const int blk = (int)(((long long)sm_ctx[r] + P1) >> p.log2p) + j - sm_pg[r];
     p.table[(long long)r * p.max_blocks + blk] = p.free_pages[nfree - 1 - j];
   }
   for (int t = first; t < p.T; t += stride) {
     int pos = 0, slot = -1;
     if (t < nt) {
-      const int r = find_request(sm_cu, p.B, t), c = p.ctx[r];
+      const int r = find_request(sm_cu, p.B, t), c = sm_ctx[r];
       pos = c + t - sm_cu[r];
       const int blk = pos >> p.log2p, held = (int)(((long long)c + P1) >> p.log2p);
       const int page = blk < held ? p.table[(long long)r * p.max_blocks + blk]
@@ -168,29 +167,30 @@ __global__ void __launch_bounds__(kThreads) pages_plan_kernel(const PagesParams 
 }
 
 // The pages of the requests marked done go back on the free list in request order.
-__global__ void __launch_bounds__(kThreads) pages_release_kernel(const PagesParams p) {
+__global__ void __launch_bounds__(kMaxThreads) pages_release_kernel(const PagesParams p) {
   extern __shared__ int sm_pg[];  // B + 1 prefixes
-  __shared__ long long sm_scan[2 * kWarps];
-  const int tid = threadIdx.x, P1 = (1 << p.log2p) - 1;
+  __shared__ long long sm_scan[64];
+  const int tid = threadIdx.x, threads = blockDim.x, P1 = (1 << p.log2p) - 1;
   grid_dependency_wait();
   const int nfree = *p.n_free;
   unsigned bad = nfree < 0 || nfree > p.free_cap ? KQ_PAGES_BAD_ARG : 0u;
-  long long cp = 0;
-  for (int base = 0; base < p.B; base += kThreads) {
-    const int r = base + tid;
-    long long b = 0, z = 0, tz, tb;
-    if (r < p.B && p.done[r]) {
-      const int c = p.ctx[r];
-      b = ((long long)c + P1) >> p.log2p;
-      if (c < 0) bad |= KQ_PAGES_BAD_ARG, b = 0;
-      else if (b > p.max_blocks) bad |= KQ_PAGES_TABLE_FULL;
+  const int per = (p.B + threads - 1) / threads, r0 = min(tid * per, p.B), r1 = min(r0 + per, p.B);
+  long long a = 0, b = 0, ta, cp;
+  for (int r = r0; r < r1; ++r) {
+    sm_pg[r] = clamp_int(b);
+    if (!p.done[r]) continue;
+    const int c = p.ctx[r];
+    if (c < 0) {
+      bad |= KQ_PAGES_BAD_ARG;
+      continue;
     }
-    long long ib = b;
-    block_scan2(z, ib, tz, tb, sm_scan);
-    if (r < p.B) sm_pg[r] = (int)min(cp + ib - b, (long long)INT_MAX);
-    cp += tb;
+    const long long pages = ((long long)c + P1) >> p.log2p;
+    if (pages > p.max_blocks) bad |= KQ_PAGES_TABLE_FULL;
+    b += pages;
   }
-  if (tid == 0) sm_pg[p.B] = (int)min(cp, (long long)INT_MAX);
+  block_scan2(a, b, ta, cp, sm_scan);
+  for (int r = r0; r < r1; ++r) sm_pg[r] = clamp_int(b + sm_pg[r]);
+  if (tid == 0) sm_pg[p.B] = clamp_int(cp);
   if (cp + nfree > p.free_cap) bad |= KQ_PAGES_OUT_OF_PAGES;
   bad = __syncthreads_or((int)bad) ? 0x80000000u | bad : 0u;
   if (blockIdx.x == 0) {
@@ -205,7 +205,7 @@ __global__ void __launch_bounds__(kThreads) pages_release_kernel(const PagesPara
     }
   }
   if (bad) return;
-  for (int j = blockIdx.x * kThreads + tid; j < (int)cp; j += gridDim.x * kThreads) {
+  for (int j = blockIdx.x * threads + tid; j < (int)cp; j += gridDim.x * threads) {
     const int r = find_request(sm_pg, p.B, j);
     int* e = p.table + (long long)r * p.max_blocks + (j - sm_pg[r]);
     p.free_pages[nfree + j] = *e;
@@ -238,11 +238,12 @@ int launch_pages_plan(const PagesArgs& a, int num_sms, cudaStream_t s, std::stri
   p.slot = a.slot;
   p.T = a.T;
   p.status = a.status;
-  const size_t smem = (size_t)2 * (a.B + 1) * sizeof(int);
+  const size_t smem = (size_t)3 * (a.B + 1) * sizeof(int);
   // one token per thread up to one CTA per SM; beyond it a CTA's share grows, as each CTA scans all requests
-  const long long want = ((long long)a.T + kThreads - 1) / kThreads;
+  const int threads = a.B > 256 || a.T > 256 * num_sms ? kMaxThreads : 256;
+  const long long want = ((long long)a.T + threads - 1) / threads;
   const int grid = (int)(want < 1 ? 1 : want > num_sms ? num_sms : want);
-  return launch_pdl(pages_plan_kernel, dim3(grid), dim3(kThreads), smem, s, p, "pages_plan", err);
+  return launch_pdl(pages_plan_kernel, dim3(grid), dim3(threads), smem, s, p, "pages_plan", err);
 }
 
 int launch_pages_release(const PagesArgs& a, const unsigned char* done, int num_sms, cudaStream_t s, std::string* err) {
@@ -259,9 +260,10 @@ int launch_pages_release(const PagesArgs& a, const unsigned char* done, int num_
   p.n_free_out = a.n_free_out;
   p.status = a.status;
   const size_t smem = (size_t)(a.B + 1) * sizeof(int);
-  const long long want = ((long long)a.free_cap + 4 * kThreads - 1) / (4 * kThreads);
+  const int threads = a.B > 256 ? kMaxThreads : 256;
+  const long long want = ((long long)a.free_cap + 4 * threads - 1) / (4 * threads);
   const int grid = (int)(want < 1 ? 1 : want > num_sms ? num_sms : want);
-  return launch_pdl(pages_release_kernel, dim3(grid), dim3(kThreads), smem, s, p, "pages_release", err);
+  return launch_pdl(pages_release_kernel, dim3(grid), dim3(threads), smem, s, p, "pages_release", err);
 }
 
 }  // namespace kq
