@@ -202,9 +202,10 @@ __device__ __forceinline__ void codes_to_h2(uint32_t w, uint32_t& even, uint32_t
   odd = h2_sub(o, 0x64806480u);
 }
 // Tokens (4 t, 4 t + 1) and (4 t + 2, 4 t + 3) of a row -> the pairs that codes_to_h2 makes.
-__device__ __forceinline__ void weight_operand(uint32_t (&b)[2], uint32_t lo, uint32_t hi) {
+__device__ __forceinline__ void weight_operand(uint32_t (&b)[4], uint32_t lo, uint32_t hi) {
   b[0] = prmt(lo, hi, 0x5410);
   b[1] = prmt(lo, hi, 0x7632);
+  b[2] = b[3] = 0u;
 }
 __device__ __forceinline__ float fast_exp2(float x) {
   float y;
@@ -212,16 +213,11 @@ __device__ __forceinline__ float fast_exp2(float x) {
   return y;
 }
 
-// Largest, and sum, over the eight lanes that hold one query row.
-__device__ __forceinline__ float max_over_rows(float v) {
+// Largest over the lanes that hold one query row: eight for 8 rows, four for 16.
+template <bool R16>
+__device__ __forceinline__ float max_over_row(float v) {
 #pragma unroll
-  for (int x = 4; x < 32; x <<= 1) v = fmaxf(v, __shfl_xor_sync(~0u, v, x));
-  return v;
-}
-
-__device__ __forceinline__ float sum_over_rows(float v) {
-#pragma unroll
-  for (int x = 4; x < 32; x <<= 1) v += __shfl_xor_sync(~0u, v, x);
+  for (int x = R16 ? 1 : 4; x < (R16 ? 4 : 32); x <<= 1) v = fmaxf(v, __shfl_xor_sync(~0u, v, x));
   return v;
 }
 
@@ -231,17 +227,18 @@ __device__ __forceinline__ void mbar_arrive(uint64_t* bar) {
 // The warps that multiply, without the one that copies.
 __device__ __forceinline__ void math_barrier() { asm volatile("bar.sync 1, %0;" ::"n"(kMath) : "memory"); }
 
-// Shared memory of a CTA: a ring of slots (a step's K or its V), the warps' outputs of an item, for
-// more than 8 query rows the item's query operands of each warp, the requests.
-template <int D, int NT, bool WIDE>
+// Shared memory of a CTA: a ring of slots (a step's K or its V), the warps' outputs of an item, for 16
+// query rows the item's query operands, the requests.
+template <int D, bool R16, bool WIDE>
 struct AttnSmem {
-  static constexpr int RB = 8 * NT, PARTS = WIDE ? 2 : 1;
+  static constexpr int RB = R16 ? 16 : 8, PARTS = WIDE ? 2 : 1;
   static constexpr int kDepth = D == 128 ? 3 : 6;
   static constexpr int kSlot = kStep * D;
-  static constexpr int kOut = kDepth * kSlot;                     // [warp][RB][D + 4] floats
+  static constexpr int kOut = kDepth * kSlot;              // [warp][RB][D + 4] floats
   static constexpr int kOutWarp = RB * (D + 4);
-  static constexpr int kQ = kOut + kWarps * kOutWarp * 4;         // [part][NT][D / 32][32 lanes][4 words]
-  static constexpr int kReq = kQ + (NT == 1 ? 0 : PARTS * NT * D * 16);
+  static constexpr int kQ = kOut + kWarps * kOutWarp * 4;  // [part][D / 16][32 lanes][4 words]
+  static constexpr int kQPart = R16 ? D / 16 * 512 : 0;
+  static constexpr int kReq = kQ + PARTS * kQPart;
   static constexpr size_t bytes(int B) { return kReq + (size_t)(B + 1) * sizeof(Request); }
 };
 
@@ -250,16 +247,22 @@ struct Item {  // (request, kv head, block of query rows, segment)
   int step0, step1, end, seen;  // steps of kStep; positions from `end` on are seen by no row, those below `seen` by all
 };
 
-template <int D, int NT, bool WIDE>
-__global__ void __launch_bounds__(kThreads, D == 64 ? (NT == 1 ? 4 : 3) : NT == 1 ? 3 : NT == 2 ? 2 : 1) attn_kv8_kernel(const AttnKV8Params p) {
-  using S = AttnSmem<D, NT, WIDE>;
-  constexpr int RB = S::RB, C32 = D / 32, DEPTH = S::kDepth;
-  constexpr bool QREG = NT == 1;  // query operands stay in registers
+// R16: 16 query rows as the A operand (scores of rows g, g + 8 in a lane); otherwise 8 as the B operand
+// (rows 2 t4, 2 t4 + 1). Both give a row the same bits: every sum over dims, positions or lanes is the
+// tensor cores' own, in the same order of k.
+template <int D, bool R16, bool WIDE>
+__global__ void __launch_bounds__(kThreads, R16 ? (D == 64 ? 3 : 2) : D == 64 ? 4 : 3) attn_kv8_kernel(const AttnKV8Params p) {
+  using S = AttnSmem<D, R16, WIDE>;
+  constexpr int RB = S::RB, C32 = D / 32, K16 = D / 16, DEPTH = S::kDepth;
+  constexpr int PARTS = S::PARTS;              // fp16 parts of queries and weights
+  constexpr int NV = R16 ? 4 : 2;              // scores of a row per lane and group of 16 tokens
+  constexpr int NO = R16 ? 2 * K16 : K16;      // output tiles: 8 dims by 16 rows, or 16 dims by 8 rows
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ __align__(8) uint64_t sm_full[DEPTH], sm_empty[DEPTH];
   __shared__ __align__(16) float sm_scale[4][2][kStep / 16];  // [step & 3][k, v][group]
   __shared__ long long sm_scan[3 * (kThreads / 32)];
-  __shared__ __align__(16) float sm_hq[RB], sm_rf[RB];  // read in pairs
+  __shared__ __align__(16) float sm_hq[RB];  // written in pairs
+  __shared__ float sm_rf[RB];
   __shared__ float sm_m[kWarps][RB], sm_l[kWarps][RB], sm_h[kWarps][RB];
   __shared__ int sm_lim[RB];
   __shared__ uint32_t sm_mask[RB];
@@ -396,21 +399,23 @@ __global__ void __launch_bounds__(kThreads, D == 64 ? (NT == 1 ? 4 : 3) : NT == 
   for (Place at = place0; at.item < total; move(at)) {
     const Item x = item_of(at);
     const int group = p.group;
-    // ---- query operands: lane (g, t4) holds row g of each block of 8 at dims 16 s + 4 t4 .. + 3; rows
-    // past the last are zeros that see nothing
-    uint2 qh[QREG ? 2 * C32 : 1], ql[QREG && WIDE ? 2 * C32 : 1];
-    float hq[QREG ? 1 : NT][2], rf[QREG ? 1 : NT][2];
-    int lim[QREG ? 1 : NT][2];
-#pragma unroll 1
-    for (int nt = QREG ? 0 : w; nt < NT; nt += QREG ? 1 : kWarps) {  // each warp for itself, or its blocks for all
+    // ---- query operands: lane (g, t4) takes row g of a block of 8 at dims 16 s + 4 t4 .. + 3; rows past
+    // the last are zeros that see nothing. 8 rows: each warp for itself, in registers; 16: warps 0 and 1
+    // for all, in shared memory
+    uint2 qh[R16 ? 1 : K16], ql[!R16 && WIDE ? K16 : 1];
+    float hq[2], rf[2];
+    int lim[2];
+    uint32_t see[2];
+    if (!R16 || w < 2) {
+      const int nt = R16 ? w : 0;
       const int row = x.row0 + 8 * nt + g, ti = row / group;
       const bool live = row < x.rows;
-      float v[2 * C32][4];
+      float v[K16][4];
       const long long from = (x.tok0 + ti) * p.qs + (long long)(x.h * group + row - ti * group) * D + 4 * t4;
       if (p.q_f32) {
         const float4* src = reinterpret_cast<const float4*>(static_cast<const float*>(p.q) + from);
 #pragma unroll
-        for (int s = 0; s < 2 * C32; ++s) {
+        for (int s = 0; s < K16; ++s) {
           const float4 q = live ? src[4 * s] : make_float4(0.f, 0.f, 0.f, 0.f);
           v[s][0] = q.x;
           v[s][1] = q.y;
@@ -420,7 +425,7 @@ __global__ void __launch_bounds__(kThreads, D == 64 ? (NT == 1 ? 4 : 3) : NT == 
       } else {
         const uint2* src = reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(p.q) + from);
 #pragma unroll
-        for (int s = 0; s < 2 * C32; ++s) {
+        for (int s = 0; s < K16; ++s) {
           const uint2 q = live ? src[4 * s] : make_uint2(0u, 0u);
           v[s][0] = __uint_as_float(q.x << 16);
           v[s][1] = __uint_as_float(q.x & 0xFFFF0000u);
@@ -430,7 +435,7 @@ __global__ void __launch_bounds__(kThreads, D == 64 ? (NT == 1 ? 4 : 3) : NT == 
       }
       unsigned top = 0;
 #pragma unroll
-      for (int s = 0; s < 2 * C32; ++s)
+      for (int s = 0; s < K16; ++s)
 #pragma unroll
         for (int e = 0; e < 4; ++e) top = max(top, __float_as_uint(v[s][e]) & 0x7FFFFFFFu);
       top = max(top, __shfl_xor_sync(~0u, top, 1));
@@ -444,223 +449,245 @@ __global__ void __launch_bounds__(kThreads, D == 64 ? (NT == 1 ? 4 : 3) : NT == 
       float half[4] = {0.f, 0.f, 0.f, 0.f};
       const uint32_t halves[4] = {0x38003800u, 0x38003800u, 0x38003800u, 0x38003800u};
 #pragma unroll
-      for (int s = 0; s < 2 * C32; ++s) {
+      for (int s = 0; s < K16; ++s) {
         const float f[4] = {v[s][0] * up, v[s][1] * up, v[s][2] * up, v[s][3] * up};
         const uint2 hi = make_uint2(f2_to_h2(f[0], f[2]), f2_to_h2(f[1], f[3]));
         mma_f16_16816(half, halves, hi.x, hi.y, half);
-        if (QREG) qh[QREG ? s : 0] = hi;
-        else *reinterpret_cast<uint2*>(sm_q + ((nt * C32 + (s >> 1)) * 32 + lane) * 4 + 2 * (s & 1)) = hi;
+        uint32_t* q16 = sm_q + (s * 32 + lane) * 4 + nt;  // rows g: words 0, 2; rows g + 8: words 1, 3
+        if (R16) {
+          q16[0] = hi.x;
+          q16[2] = hi.y;
+        } else {
+          qh[R16 ? 0 : s] = hi;
+        }
         if (WIDE) {
           const uint2 lo = make_uint2(f2_to_h2(f[0] - h_lo_to_f(hi.x), f[2] - h_lo_to_f(hi.x >> 16)),
                                       f2_to_h2(f[1] - h_lo_to_f(hi.y), f[3] - h_lo_to_f(hi.y >> 16)));
           mma_f16_16816(half, halves, lo.x, lo.y, half);
-          if (QREG) ql[QREG ? s : 0] = lo;
-          else *reinterpret_cast<uint2*>(sm_q + NT * D * 4 + ((nt * C32 + (s >> 1)) * 32 + lane) * 4 + 2 * (s & 1)) = lo;
+          if (R16) {
+            q16[S::kQPart / 4] = lo.x;
+            q16[S::kQPart / 4 + 2] = lo.y;
+          } else {
+            ql[!R16 && WIDE ? s : 0] = lo;
+          }
         }
       }
       const int last = live ? x.ctx + ti : -1;
-      if (QREG) {
-#pragma unroll
-        for (int k = 0; k < 2; ++k) {
-          hq[0][k] = half[k];
-          rf[0][k] = __shfl_sync(~0u, factor, 8 * t4 + 4 * k);
-          lim[0][k] = __shfl_sync(~0u, last, 8 * t4 + 4 * k);
-        }
-      } else {
+      const uint32_t word = live && p.mask ? p.mask[x.tok0 + ti] : 0u;
+      if (R16) {
         if (g == 0) *reinterpret_cast<float2*>(sm_hq + 8 * nt + 2 * t4) = make_float2(half[0], half[1]);
         if (t4 == 0) {
           sm_rf[8 * nt + g] = factor;
           sm_lim[8 * nt + g] = last;
+          sm_mask[8 * nt + g] = word;
+        }
+      } else {
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          hq[k] = half[k];
+          rf[k] = __shfl_sync(~0u, factor, 8 * t4 + 4 * k);
+          lim[k] = __shfl_sync(~0u, last, 8 * t4 + 4 * k);
+          see[k] = __shfl_sync(~0u, word, 8 * t4 + 4 * k);
         }
       }
-      if (p.mask && t4 == 0) sm_mask[8 * nt + g] = live ? p.mask[x.tok0 + ti] : 0u;
     }
-    if (!QREG || p.mask) math_barrier();
-
-    // rows 2 t4 and 2 t4 + 1 of each block of 8; l and hv are this lane's share of the row's sums
-    float o[2 * C32][NT][4], m[NT][2], l[NT][2], hv[NT][2];
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
+    if (R16) {
+      math_barrier();
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
-        m[nt][k] = -INFINITY;
-        l[nt][k] = hv[nt][k] = 0.f;
+        hq[k] = sm_hq[g + 8 * k];
+        rf[k] = sm_rf[g + 8 * k];
+        lim[k] = sm_lim[g + 8 * k];
+        see[k] = sm_mask[g + 8 * k];
       }
-#pragma unroll
-      for (int s = 0; s < 2 * C32; ++s) o[s][nt][0] = o[s][nt][1] = o[s][nt][2] = o[s][nt][3] = 0.f;
     }
+
+    // this lane's two rows: reference, sum of weights, sum of weights times v scales; output tiles
+    float o[NO][4], m[2], l[2], hv[2];
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      m[k] = -INFINITY;
+      l[k] = hv[k] = 0.f;
+    }
+#pragma unroll
+    for (int s = 0; s < NO; ++s) o[s][0] = o[s][1] = o[s][2] = o[s][3] = 0.f;
 
     for (int step = x.step0; step < x.step1; ++step, ++steps) {
       const uint8_t* kst = smem + slot * S::kSlot + w * kWarpPos * D;
-      // ---- scores
-      float sc[2][NT][4];
+      // ---- scores: [group][R16: the group's token pairs 4 t, 4 t + 1 and 4 t + 2, 4 t + 3]
+      float sc[2][R16 ? 2 : 1][4];
 #pragma unroll
       for (int st = 0; st < 2; ++st)
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-          const float2 h = QREG ? make_float2(hq[0][0], hq[0][1]) : lds_f2(sm_hq + nt * 8 + 2 * t4);
-          sc[st][nt][0] = sc[st][nt][2] = h.x;
-          sc[st][nt][1] = sc[st][nt][3] = h.y;
-        }
+        for (int i = 0; i < (R16 ? 2 : 1); ++i)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) sc[st][i][e] = hq[R16 ? e >> 1 : e & 1];
       wait(&sm_full[slot], phase);
       const float2 kf2 = lds_f2(&sm_scale[steps & 3][0][2 * w]), vf2 = lds_f2(&sm_scale[steps & 3][1][2 * w]);
       const float kf[2] = {kf2.x, kf2.y}, vf[2] = {vf2.x, vf2.y};
 #pragma unroll
       for (int cc = 0; cc < C32; ++cc) {
-        uint32_t a[2][2][4];
+        uint32_t qa[PARTS][2][4];
+        if (R16) {
+#pragma unroll
+          for (int part = 0; part < PARTS; ++part)
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              const uint4 q = lds128(sm_q + part * (S::kQPart / 4) + ((2 * cc + i) * 32 + lane) * 4);
+              qa[part][i][0] = q.x;
+              qa[part][i][1] = q.y;
+              qa[part][i][2] = q.z;
+              qa[part][i][3] = q.w;
+            }
+        }
 #pragma unroll
         for (int st = 0; st < 2; ++st) {
           const uint4 k = lds128(kst + st * 16 * D + cc * 512 + lane * 16);
-          codes_to_h2(k.x, a[st][0][0], a[st][0][2]);
-          codes_to_h2(k.y, a[st][0][1], a[st][0][3]);
-          codes_to_h2(k.z, a[st][1][0], a[st][1][2]);
-          codes_to_h2(k.w, a[st][1][1], a[st][1][3]);
-        }
+          uint32_t a[2][4];  // [16 dims][rows g, g + 8 of even pairs, then of odd ones]
+          codes_to_h2(k.x, a[0][0], a[0][2]);
+          codes_to_h2(k.y, a[0][1], a[0][3]);
+          codes_to_h2(k.z, a[1][0], a[1][2]);
+          codes_to_h2(k.w, a[1][1], a[1][3]);
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-          const uint4 q = QREG ? make_uint4(qh[QREG ? 2 * cc : 0].x, qh[QREG ? 2 * cc : 0].y, qh[QREG ? 2 * cc + 1 : 0].x, qh[QREG ? 2 * cc + 1 : 0].y)
-                               : lds128(sm_q + ((nt * C32 + cc) * 32 + lane) * 4);
+          for (int i = 0; i < 2; ++i) {
+            if (R16) {
 #pragma unroll
-          for (int st = 0; st < 2; ++st) {
-            mma_f16_16816(sc[st][nt], a[st][0], q.x, q.y, sc[st][nt]);
-            mma_f16_16816(sc[st][nt], a[st][1], q.z, q.w, sc[st][nt]);
-          }
-          if (WIDE) {
-            const uint4 q2 = QREG ? make_uint4(ql[QREG && WIDE ? 2 * cc : 0].x, ql[QREG && WIDE ? 2 * cc : 0].y,
-                                               ql[QREG && WIDE ? 2 * cc + 1 : 0].x, ql[QREG && WIDE ? 2 * cc + 1 : 0].y)
-                                  : lds128(sm_q + NT * D * 4 + ((nt * C32 + cc) * 32 + lane) * 4);
-#pragma unroll
-            for (int st = 0; st < 2; ++st) {
-              mma_f16_16816(sc[st][nt], a[st][0], q2.x, q2.y, sc[st][nt]);
-              mma_f16_16816(sc[st][nt], a[st][1], q2.z, q2.w, sc[st][nt]);
+              for (int part = 0; part < PARTS; ++part) {
+                mma_f16_16816(sc[st][0], qa[part][i], a[i][0], a[i][2], sc[st][0]);
+                mma_f16_16816(sc[st][R16 ? 1 : 0], qa[part][i], a[i][1], a[i][3], sc[st][R16 ? 1 : 0]);
+              }
+            } else {
+              const int s = R16 ? 0 : 2 * cc + i;
+              mma_f16_16816(sc[st][0], a[i], qh[s].x, qh[s].y, sc[st][0]);
+              if (WIDE) mma_f16_16816(sc[st][0], a[i], ql[WIDE ? s : 0].x, ql[WIDE ? s : 0].y, sc[st][0]);
             }
           }
         }
       }
       free_slot();
-      const uint8_t* vst = smem + slot * S::kSlot + w * kWarpPos * D;
       // ---- weights against the page's largest score, up by 2^15 into fp16's range
-      const int pos0 = step * kStep + w * kWarpPos + 4 * (g >> 1) + (g & 1);  // token of operand row g; row g + 8 is two on
-      // positions that every row sees (rows past the last come along: nothing reads them)
-      const bool all_seen = step * kStep + (w + 1) * kWarpPos <= x.seen;
-      uint32_t wb[2][NT][2], wl[WIDE ? 2 : 1][NT][2];
-      float fv[2][NT][2];
+      // value v of row k in group st is score sc[st][..] below, of position pos0 + 16 st + (R16 ? v : 2 v)
+      const int pos0 = step * kStep + w * kWarpPos + (R16 ? 4 * t4 : 4 * (g >> 1) + (g & 1));
+      float sv[2][2][NV];
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt) {
-        const int rr = nt * 8 + 2 * t4;
-        const float2 rff = QREG ? make_float2(rf[0][0], rf[0][1]) : lds_f2(sm_rf + rr);
-        const int lim0 = QREG ? lim[0][0] : sm_lim[rr], lim1 = QREG ? lim[0][1] : sm_lim[rr + 1];
-        if (all_seen) {
-#pragma unroll
-          for (int st = 0; st < 2; ++st) {
-            const float r0 = rff.x * kf[st], r1 = rff.y * kf[st];
-            float* s = sc[st][nt];
-            s[0] *= r0;
-            s[1] *= r1;
-            s[2] *= r0;
-            s[3] *= r1;
-          }
-        } else if (p.mask == nullptr) {
-#pragma unroll
-          for (int st = 0; st < 2; ++st) {
-            const int p0 = pos0 + 16 * st, p1 = p0 + 2;
-            const float r0 = rff.x * kf[st], r1 = rff.y * kf[st];
-            float* s = sc[st][nt];
-            s[0] = p0 <= lim0 ? s[0] * r0 : -INFINITY;
-            s[1] = p0 <= lim1 ? s[1] * r1 : -INFINITY;
-            s[2] = p1 <= lim0 ? s[2] * r0 : -INFINITY;
-            s[3] = p1 <= lim1 ? s[3] * r1 : -INFINITY;
-          }
-        } else {
-          const uint32_t mk0 = sm_mask[rr], mk1 = sm_mask[rr + 1];
-          auto sees = [&](int pos, int lim, uint32_t mk) {
-            const int j = pos - x.ctx;
-            return lim >= 0 && pos < x.len && (j < 0 || (mk >> (j & 31) & 1u) != 0);
-          };
-#pragma unroll
-          for (int st = 0; st < 2; ++st) {
-            const int p0 = pos0 + 16 * st, p1 = p0 + 2;
-            const float r0 = rff.x * kf[st], r1 = rff.y * kf[st];
-            float* s = sc[st][nt];
-            s[0] = sees(p0, lim0, mk0) ? s[0] * r0 : -INFINITY;
-            s[1] = sees(p0, lim1, mk1) ? s[1] * r1 : -INFINITY;
-            s[2] = sees(p1, lim0, mk0) ? s[2] * r0 : -INFINITY;
-            s[3] = sees(p1, lim1, mk1) ? s[3] * r1 : -INFINITY;
-          }
-        }
-        float al[2];
-        bool moved = false;
+      for (int st = 0; st < 2; ++st)
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
-          float* s0 = sc[0][nt] + k;
-          float* s1 = sc[1][nt] + k;
-          float g0 = fmaxf(s0[0], s0[2]), g1 = fmaxf(s1[0], s1[2]);
-          if (P > 16) {
-            g0 = g1 = max_over_rows(fmaxf(g0, g1));
-          } else {
-            g0 = max_over_rows(g0);
-            g1 = max_over_rows(g1);
-          }
-          // the row's reference follows its largest score only when that is 2^16 weights above it
-          const float top = fmaxf(g0, g1), was = m[nt][k], ref = top > was + 16.f ? top : was;
-          al[k] = ref == was ? 1.f : fast_exp2(was - ref);
-          moved |= ref != was;
-          m[nt][k] = ref;
-          // a group that the row sees nothing of has weights of 0 and takes nothing of its scale, even of a NaN
-          const float c0 = fmaxf(g0, kLowest) - 15.f;
-          const float u0 = fast_exp2(c0 - fmaxf(ref, kLowest));
-          const float f0 = g0 == -INFINITY ? 0.f : u0 * vf[0];
-          s0[0] = fast_exp2(s0[0] - c0);
-          s0[2] = fast_exp2(s0[2] - c0);
-          const float sum0 = s0[0] + s0[2];
-          fv[0][nt][k] = f0;
-          if (P > 16) {
-            s1[0] = fast_exp2(s1[0] - c0);
-            s1[2] = fast_exp2(s1[2] - c0);
-            const float sum = sum0 + (s1[0] + s1[2]);
-            fv[1][nt][k] = f0;
-            l[nt][k] = l[nt][k] * al[k] + sum * u0;
-            hv[nt][k] = hv[nt][k] * al[k] + sum * f0;
-          } else {
-            const float c1 = fmaxf(g1, kLowest) - 15.f;
-            const float u1 = fast_exp2(c1 - fmaxf(ref, kLowest));
-            const float f1 = g1 == -INFINITY ? 0.f : u1 * vf[1];
-            s1[0] = fast_exp2(s1[0] - c1);
-            s1[2] = fast_exp2(s1[2] - c1);
-            const float sum1 = s1[0] + s1[2];
-            fv[1][nt][k] = f1;
-            l[nt][k] = l[nt][k] * al[k] + sum0 * u0 + sum1 * u1;
-            hv[nt][k] = hv[nt][k] * al[k] + sum0 * f0 + sum1 * f1;
-          }
+          const float r = rf[k] * kf[st];
+#pragma unroll
+          for (int v = 0; v < NV; ++v) sv[st][k][v] = r * (R16 ? sc[st][R16 ? v >> 1 : 0][2 * k + (v & 1)] : sc[st][0][k + 2 * (v & 1)]);
         }
+      // all positions seen by every row: nothing to mask (rows past the last come along: nothing reads them)
+      if (step * kStep + (w + 1) * kWarpPos > x.seen) {
+#pragma unroll
+        for (int st = 0; st < 2; ++st)
+#pragma unroll
+          for (int k = 0; k < 2; ++k)
+#pragma unroll
+            for (int v = 0; v < NV; ++v) {
+              const int pos = pos0 + 16 * st + (R16 ? v : 2 * v), j = pos - x.ctx;
+              const bool sees = p.mask == nullptr ? pos <= lim[k]
+                                                  : lim[k] >= 0 && pos < x.len && (j < 0 || (see[k] >> (j & 31) & 1u) != 0);
+              if (!sees) sv[st][k][v] = -INFINITY;
+            }
+      }
+      float al[2], up[2][2], fv[2][2];  // [group][row]: the page's weight against the row's reference; times its v scale
+      bool moved = false;
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        float top[2];
 #pragma unroll
         for (int st = 0; st < 2; ++st) {
-          const float* s = sc[st][nt];
-          const uint32_t e0 = f2_to_h2(s[0], s[1]), e1 = f2_to_h2(s[2], s[3]);
-          weight_operand(wb[st][nt], movmatrix(e0), movmatrix(e1));
-          if (WIDE) {
-            weight_operand(wl[WIDE ? st : 0][nt], movmatrix(f2_to_h2(s[0] - h_lo_to_f(e0), s[1] - h_lo_to_f(e0 >> 16))),
-                           movmatrix(f2_to_h2(s[2] - h_lo_to_f(e1), s[3] - h_lo_to_f(e1 >> 16))));
-          }
+          top[st] = fmaxf(sv[st][k][0], sv[st][k][1]);
+          if (R16) top[st] = fmaxf(top[st], fmaxf(sv[st][k][NV - 2], sv[st][k][NV - 1]));
         }
-        if (__any_sync(~0u, moved)) {
+        if (P > 16) {
+          top[0] = top[1] = max_over_row<R16>(fmaxf(top[0], top[1]));
+        } else {
+          top[0] = max_over_row<R16>(top[0]);
+          top[1] = max_over_row<R16>(top[1]);
+        }
+        // the row's reference follows its largest score only when that is 2^16 weights above it
+        const float both = fmaxf(top[0], top[1]), was = m[k], ref = both > was + 16.f ? both : was;
+        al[k] = ref == was ? 1.f : fast_exp2(was - ref);
+        moved |= ref != was;
+        m[k] = ref;
+        const float base = fmaxf(ref, kLowest);
 #pragma unroll
-          for (int s = 0; s < 2 * C32; ++s) {
-            o[s][nt][0] *= al[0];
-            o[s][nt][1] *= al[1];
-            o[s][nt][2] *= al[0];
-            o[s][nt][3] *= al[1];
+        for (int st = 0; st < 2; ++st) {
+          if (st == 1 && P > 16) {  // one page
+            up[1][k] = up[0][k];
+            fv[1][k] = fv[0][k];
+          } else {
+            up[st][k] = fast_exp2(fmaxf(top[st], kLowest) - 15.f - base);
+            // a group that the row sees nothing of has weights of 0 and takes nothing of its scale, even of a NaN
+            fv[st][k] = top[st] == -INFINITY ? 0.f : up[st][k] * vf[st];
           }
+          const float c = fmaxf(top[st], kLowest) - 15.f;
+#pragma unroll
+          for (int v = 0; v < NV; ++v) sv[st][k][v] = fast_exp2(sv[st][k][v] - c);
+        }
+      }
+      // the weights as operands: pairs of tokens (4 t, 4 t + 2) and (4 t + 1, 4 t + 3), as codes_to_h2 makes them
+      uint32_t wt[2][PARTS][4];  // 8 rows: two of the four
+#pragma unroll
+      for (int st = 0; st < 2; ++st) {
+        if (R16) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {  // row g + 8 (i & 1), even or odd pair
+            const float a = sv[st][i & 1][i >> 1], b = sv[st][i & 1][R16 ? 2 + (i >> 1) : 0];
+            const uint32_t hi = f2_to_h2(a, b);
+            wt[st][0][i] = hi;
+            if (WIDE) wt[st][WIDE ? 1 : 0][i] = f2_to_h2(a - h_lo_to_f(hi), b - h_lo_to_f(hi >> 16));
+          }
+        } else {
+          const uint32_t e0 = f2_to_h2(sv[st][0][0], sv[st][1][0]), e1 = f2_to_h2(sv[st][0][1], sv[st][1][1]);
+          weight_operand(wt[st][0], movmatrix(e0), movmatrix(e1));
+          if (WIDE)
+            weight_operand(wt[st][WIDE ? 1 : 0], movmatrix(f2_to_h2(sv[st][0][0] - h_lo_to_f(e0), sv[st][1][0] - h_lo_to_f(e0 >> 16))),
+                           movmatrix(f2_to_h2(sv[st][0][1] - h_lo_to_f(e1), sv[st][1][1] - h_lo_to_f(e1 >> 16))));
+        }
+      }
+      if (__any_sync(~0u, moved)) {
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          l[k] *= al[k];
+          hv[k] *= al[k];
+        }
+#pragma unroll
+        for (int s = 0; s < NO; ++s)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) o[s][e] *= al[R16 ? e >> 1 : e & 1];
+      }
+      // ---- sums of the weights, then values: a page's products are added up before its scale
+      const uint8_t* vst = smem + slot * S::kSlot + w * kWarpPos * D;
+      constexpr uint32_t kOnes = 0x3C003C00u;
+      const uint32_t ones[4] = {kOnes, kOnes, kOnes, kOnes};
+      float acc[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int st = 0; st < 2; ++st) {
+#pragma unroll
+        for (int part = 0; part < PARTS; ++part) {
+          if (R16) mma_f16_16816(acc, wt[st][part], kOnes, kOnes, acc);
+          else mma_f16_16816(acc, ones, wt[st][part][0], wt[st][part][1], acc);
+        }
+        if (st == 1 || P == 16) {
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            const float sum = acc[R16 ? 2 * k : k];
+            l[k] = __fmaf_rn(up[st][k], sum, l[k]);
+            hv[k] = __fmaf_rn(fv[st][k], sum, hv[k]);
+          }
+          acc[0] = acc[1] = acc[2] = acc[3] = 0.f;
         }
       }
       wait(&sm_full[slot], phase);
 #pragma unroll
       for (int cc = 0; cc < C32; ++cc) {
-        float acc[2][NT][4];
+        constexpr int NA = R16 ? 4 : 2;  // output tiles of 32 dims
+        float av[NA][4];
 #pragma unroll
-        for (int s = 0; s < 2; ++s)
-#pragma unroll
-          for (int nt = 0; nt < NT; ++nt) acc[s][nt][0] = acc[s][nt][1] = acc[s][nt][2] = acc[s][nt][3] = 0.f;
+        for (int s = 0; s < NA; ++s) av[s][0] = av[s][1] = av[s][2] = av[s][3] = 0.f;
 #pragma unroll
         for (int st = 0; st < 2; ++st) {
           const uint4 v = lds128(vst + st * 16 * D + cc * 512 + lane * 16);
@@ -670,24 +697,20 @@ __global__ void __launch_bounds__(kThreads, D == 64 ? (NT == 1 ? 4 : 3) : NT == 
           codes_to_h2(v.z, a[1][0], a[1][2]);
           codes_to_h2(v.w, a[1][1], a[1][3]);
 #pragma unroll
-          for (int nt = 0; nt < NT; ++nt)
+          for (int part = 0; part < PARTS; ++part)
 #pragma unroll
-            for (int s = 0; s < 2; ++s) {
-              mma_f16_16816(acc[s][nt], a[s], wb[st][nt][0], wb[st][nt][1], acc[s][nt]);
-              if (WIDE) mma_f16_16816(acc[s][nt], a[s], wl[WIDE ? st : 0][nt][0], wl[WIDE ? st : 0][nt][1], acc[s][nt]);
+            for (int s = 0; s < NA; ++s) {
+              if (R16) mma_f16_16816(av[s], wt[st][part], a[s >> 1][s & 1], a[s >> 1][2 + (s & 1)], av[s]);
+              else mma_f16_16816(av[s], a[R16 ? 0 : s], wt[st][part][0], wt[st][part][1], av[s]);
             }
           if (st == 1 || P == 16) {
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
+            for (int s = 0; s < NA; ++s)
 #pragma unroll
-              for (int s = 0; s < 2; ++s) {
-                float* oo = o[2 * cc + s][nt];
-                float* aa = acc[s][nt];
-                oo[0] += fv[st][nt][0] * aa[0];
-                oo[1] += fv[st][nt][1] * aa[1];
-                oo[2] += fv[st][nt][0] * aa[2];
-                oo[3] += fv[st][nt][1] * aa[3];
-                if (st == 0) aa[0] = aa[1] = aa[2] = aa[3] = 0.f;
+              for (int e = 0; e < 4; ++e) {
+                float& oo = o[NA * cc + s][e];
+                oo = __fmaf_rn(fv[st][R16 ? e >> 1 : e & 1], av[s][e], oo);
+                if (st == 0) av[s][e] = 0.f;
               }
           }
         }
@@ -697,24 +720,26 @@ __global__ void __launch_bounds__(kThreads, D == 64 ? (NT == 1 ? 4 : 3) : NT == 
 
     // ---- the four warps' results meet
     float* out = reinterpret_cast<float*>(smem + S::kOut);
-    float* mine = out + w * S::kOutWarp + g;
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
+    float* mine = out + w * S::kOutWarp;
+    if (R16 ? t4 == 0 : g == 0) {
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
-        const int rr = nt * 8 + 2 * t4 + k;
-        const float den = sum_over_rows(l[nt][k]), half = 0.5f * sum_over_rows(hv[nt][k]);
-        if (g == 0) {
-          sm_m[w][rr] = m[nt][k];
-          sm_l[w][rr] = den;
-          sm_h[w][rr] = half;
-        }
-#pragma unroll
-        for (int s = 0; s < 2 * C32; ++s) {
-          mine[rr * (D + 4) + 16 * s] = o[s][nt][k];
-          mine[rr * (D + 4) + 16 * s + 8] = o[s][nt][k + 2];
-        }
+        const int rr = R16 ? g + 8 * k : 2 * t4 + k;
+        sm_m[w][rr] = m[k];
+        sm_l[w][rr] = l[k];
+        sm_h[w][rr] = 0.5f * hv[k];
       }
+    }
+#pragma unroll
+    for (int s = 0; s < NO; ++s) {
+      if (R16) {  // dims 8 s + 2 t4, + 1 of rows g, g + 8
+        *reinterpret_cast<float2*>(mine + g * (D + 4) + 8 * s + 2 * t4) = make_float2(o[s][0], o[s][1]);
+        *reinterpret_cast<float2*>(mine + (g + 8) * (D + 4) + 8 * s + 2 * t4) = make_float2(o[s][2], o[s][3]);
+      } else {    // dims 16 s + g, + 8 of rows 2 t4, + 1
+#pragma unroll
+        for (int e = 0; e < 4; ++e) mine[(2 * t4 + (e & 1)) * (D + 4) + 16 * s + 8 * (e >> 1) + g] = o[s][e];
+      }
+    }
     math_barrier();
     const bool partial = x.nseg > 1;
     const long long part_slot = (long long)x.slot + x.seg;
@@ -854,10 +879,10 @@ __global__ void __launch_bounds__(kCombThreads) attn_kv8_combine_kernel(const At
   }
 }
 
-template <int D, int NT, bool WIDE>
+template <int D, bool R16, bool WIDE>
 int launch_typed(const AttnKV8Params& p, int num_sms, cudaStream_t s, std::string* err) {
-  const size_t smem = AttnSmem<D, NT, WIDE>::bytes(p.B);
-  auto* kernel = attn_kv8_kernel<D, NT, WIDE>;
+  const size_t smem = AttnSmem<D, R16, WIDE>::bytes(p.B);
+  auto* kernel = attn_kv8_kernel<D, R16, WIDE>;
   // CTAs per SM at this shared-memory size, asked for once per host thread, device and size
   static thread_local int known_dev = -1, per_sm = 0;
   static thread_local size_t known_smem = 0;
@@ -889,12 +914,9 @@ int launch_typed(const AttnKV8Params& p, int num_sms, cudaStream_t s, std::strin
 
 template <int D>
 int launch_dim(const AttnKV8Params& p, int num_sms, cudaStream_t s, std::string* err) {
-  const long long rows = (long long)p.max_new * p.group;
-  if (p.o_f32)
-    return rows <= 8 ? launch_typed<D, 1, true>(p, num_sms, s, err)
-         : launch_typed<D, 2, true>(p, num_sms, s, err);
-  return rows <= 8 ? launch_typed<D, 1, false>(p, num_sms, s, err)
-       : launch_typed<D, 2, false>(p, num_sms, s, err);
+  const bool r16 = (long long)p.max_new * p.group > 8;
+  if (p.o_f32) return r16 ? launch_typed<D, true, true>(p, num_sms, s, err) : launch_typed<D, false, true>(p, num_sms, s, err);
+  return r16 ? launch_typed<D, true, false>(p, num_sms, s, err) : launch_typed<D, false, false>(p, num_sms, s, err);
 }
 
 size_t part_rows(int max_new, int n_q, int n_kv) { return (size_t)(n_q / n_kv) * (max_new < kSplitTokens ? max_new : kSplitTokens); }
