@@ -1,34 +1,52 @@
 // Attention over the paged 8-bit KV cache: single tokens, verify windows and prompts of a batch
 // of requests of uneven length, grouped-query heads.
 //
-//   o = sum_p w_p v_p / sum_p w_p,  w_p = 2^(x_p - max x),  x_p = log2(e) scale q.k_p
-// over the positions p that the row sees. k_p = (c + 1/2) s with int8 codes c and one scale s per
-// (page, kv head), so q.k_p = s (q.c + sum(q) / 2), and v's halves add sum_p w_p s_p / 2 to every
-// dim: the tensor cores multiply the codes alone, exact in fp16 (two byte permutes and one
-// subtraction per pair; the cache's byte order is that of the MMA operands, see kv8.cuh).
+//   o = sum_p w_p v_p / sum_p w_p,  w_p = 2^(x_p - r),  x_p = log2(e) scale q.k_p
+// over the positions p that the row sees; r is a reference that follows the row's largest x_p.
+// k_p = (c + 1/2) s with int8 codes c and one scale s per (page, kv head), so q.k_p =
+// s (q.c + sum(q) / 2), and v's halves add sum_p w_p s_p / 2 to every dim: the tensor cores multiply
+// the codes alone, exact in fp16 (a LOP3 and a subtraction per pair; the cache's byte order is that of
+// the MMA operands, see kv8.cuh).
 //
-// Products: S^T = K q^T and O^T = V^T w^T on mma.sync.m16n8k16 with the cache as the A operand:
-// 16 tokens (or dims) by 8 query rows, so a lone token's few rows pad to 8 and not to 16. w^T goes
-// from the accumulators of S^T to the B operand by one movmatrix per 8x8 block. q is scaled per row
-// by the power of two that puts its largest value in [2^14, 2^15) and rounded to fp16: exact for
-// bf16 values within 2^-28 of the row's largest; for fp32 queries a relative 2^-12, below the
-// rounding of a bf16 output. For fp32 outputs q and w are split into fp16 hi + lo parts (22 bits).
-// The weights that enter a product are those against the page's largest score, up by 2^15 (fp16
-// then holds weights down to 2^-29 of the page's largest in full, and an absolute 2^-40 below), and
-// the accumulators take the page's share of the softmax and its v scale in fp32: pages whose scales
-// lie far apart lose nothing to one another.
+// Precision. q is scaled per row by the power of two that puts its largest value in [2^14, 2^15)
+// and rounded to fp16: exact for bf16 values within 2^-28 of the row's largest; for fp32 queries a
+// relative 2^-12, below the rounding of a bf16 output. For fp32 outputs (WIDE) q and w are split into
+// fp16 hi + lo parts (22 bits). The weights that enter a product are those against the largest score of
+// their page (of up to 32 positions of it), up by 2^15: fp16 then holds weights down to 2^-29 of that in
+// full, and an absolute 2^-40 below. The accumulators take the page's share of the softmax and its v scale
+// in fp32, so pages whose scales lie far apart lose nothing to one another. Weight sums are products with
+// ones, of the same rounded weights. References, sums and outputs are fp32.
 //
-// Work: a tile is 256 positions, 64 per warp. The positions of a request are cut into segments of
-// 1, 2, 4 .. tiles (at most 128 segments; a function of its own length, so a row's bits depend on
-// its request and its window alone, never on the batch). An item is (request, block of query rows,
-// segment, kv head); a persistent grid walks the items, each CTA finding its requests in prefix
-// sums that it forms itself from the lengths, so nothing is planned on the host and the call can be
-// captured. Each warp brings its 64 positions' K and V by bulk copies of whole 16-token groups (2 KB
-// at D = 128), all requested before the first is used, and works on them alone; the four warps meet
-// in shared memory once per item. A request of one segment writes its output there; others write
-// partials that a second kernel adds in segment order. Windows of more than 32 tokens are not cut.
+// Products, on mma.sync.m16n8k16 with the codes converted in registers (the codes would have to be
+// written to shared memory twice as wide to reach tcgen05, and a few query rows leave its 128-row
+// operand empty). Up to 8 query rows per kv head: the cache is the A operand, S^T = K q^T and
+// O^T = V^T w^T, 16 tokens (or dims) by 8 rows, so that a lone token's few rows pad to 8 and not to
+// 16; the weights turn from accumulators into the B operand by one movmatrix per 8x8 block. More rows
+// (R16): the rows are the A operand, 16 at a time, and the weights become operands where they stand.
+// With 16 rows in the first form (two blocks of 8) a batch of windows of 32 rows of 64 took 48.7 us
+// in place of 41, and 32 rows at a time 79.
 //
-// Bound by DRAM: every code of the context is read once per block of query rows.
+// Work. The positions of a request are cut into segments of 512 (longer ones from 32768 positions on,
+// at most 64): a function of its own length, so that a row's bits depend on its own request alone. An
+// item is (request, block of rows, segment, kv head). A persistent grid walks the items; each CTA finds
+// them in prefix sums that it forms itself from the lengths on the device, so the host plans nothing and
+// the call can be captured. In a CTA four warps multiply and a fifth copies: it reads page ids and
+// scales 512 positions at a time and fills a ring of slots, each a step of 128 positions of K or of V, by
+// bulk copies of whole pages, across items. Each of the four takes 32 positions of a step through both
+// products alone, and they meet in shared memory once per item. A request of one segment writes its
+// output there; others write partials that a second kernel joins. Windows of more than 32 tokens are not cut.
+// Measured on the way: a CTA of four warps with nothing copied ahead across items 168 us on the decoding
+// batch below; warps that share the second product by dims, with a barrier per step, 177 us; each warp with
+// items and a ring of its own 112 to 132 us (its copies' and its items' bookkeeping weighed as much as its
+// products); the fifth warp 100 us. Segments of 256 positions 115 us and of 1024 100 us; one token
+// over 4096 positions 9.6, 10.4 and 14.4 us with segments of 256, 512 and 1024.
+//
+// Bound by DRAM for single tokens: 64 requests of 1 to 8191 positions, 32 / 8 heads of 128, 543 MB in
+// 99.6 us, 5.45 TB/s, of which 5 us are the join and about 10 the start and the end; four contexts of 128k
+// positions 166 us, 6.3 TB/s (of 6.79 copied). Windows and prompts are bound by the multiplying warps'
+// latency (two or three of them per scheduler): the conversions, the softmax and the products follow one
+// another in each, 92 us for 16 requests x 8 tokens x 4 heads per kv head of 128 over 1000 to 9000
+// positions, 178 MB, and 150 to 175 TFLOP/s for prompts.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -49,7 +67,7 @@ constexpr int kMath = 32 * kWarps, kThreads = kMath + 32;
 constexpr int kWarpPos = 32, kStep = kWarps * kWarpPos;  // positions of a step, 32 per warp
 constexpr int kMinSegment = 512, kMaxSegments = 64;      // positions of a segment at least, segments of a request at most
 constexpr int kWindow = 32 * 16 / kStep;                 // steps whose page ids are read at once, a group of 16 tokens per lane
-constexpr int kSplitTokens = 32;  // windows up to this many tokens are cut along the context
+constexpr int kSplitTokens = 32;                         // windows up to this many tokens are cut along the context
 constexpr float kLowest = -3e38f;  // below every finite score in use: keeps -inf out of differences
 constexpr uint64_t kWaitNs = 2000000000ull;
 constexpr int kCombThreads = 256;
@@ -69,6 +87,7 @@ struct AttnKV8Params {
   const int *ctx, *fresh;
   const uint32_t* mask;
   int B, T, max_new, max_len, n_pages, log2p, n_kv, group;
+  unsigned group_inv;  // 2^32 / group rounded up; 0 for a group of one
   float scale_log2e;
   float* part;      // [slot][n_kv][row_cap][D]
   float2* part_ml;  // [slot][n_kv][row_cap]: largest x, sum of weights
@@ -96,6 +115,9 @@ __host__ __device__ inline int segments(int len) {
 
 // Warps that share a row of the combine: 8 segments each, and up to 8 warps.
 __host__ __device__ constexpr int combine_warps(int nseg) { return nseg <= 8 ? 1 : nseg <= 16 ? 2 : nseg <= 32 ? 4 : 8; }
+
+// row / group for rows below 2^26 (group <= 64): row * (group * group_inv - 2^32) < 2^32.
+__device__ __forceinline__ int token_of(const AttnKV8Params& p, int row) { return p.group_inv ? (int)__umulhi((unsigned)row, p.group_inv) : row; }
 
 // A request whose lengths do not fit the call's bounds takes no part.
 __device__ __forceinline__ bool request_ok(const AttnKV8Params& p, int c, int n) {
@@ -317,8 +339,8 @@ __global__ void __launch_bounds__(kThreads, R16 ? (D == 64 ? 3 : 2) : D == 64 ? 
     }
     x.seg = local;
     x.row0 = rb * RB;
-    x.end = p.mask || n == 1 ? x.len : x.ctx + (min(x.row0 + RB, x.rows) - 1) / p.group + 1;
-    x.seen = x.ctx + (p.mask ? 0 : x.row0 / p.group + 1);
+    x.end = p.mask || n == 1 ? x.len : x.ctx + token_of(p, min(x.row0 + RB, x.rows) - 1) + 1;
+    x.seen = x.ctx + (p.mask ? 0 : token_of(p, x.row0) + 1);
     const int last = (x.end + kStep - 1) / kStep;
     x.step0 = cut ? x.seg << log2 : 0;
     x.step1 = cut ? min(x.step0 + (1 << log2), last) : last;
@@ -408,7 +430,7 @@ __global__ void __launch_bounds__(kThreads, R16 ? (D == 64 ? 3 : 2) : D == 64 ? 
     uint32_t see[2];
     if (!R16 || w < 2) {
       const int nt = R16 ? w : 0;
-      const int row = x.row0 + 8 * nt + g, ti = row / group;
+      const int row = x.row0 + 8 * nt + g, ti = token_of(p, row);
       const bool live = row < x.rows;
       float v[K16][4];
       const long long from = (x.tok0 + ti) * p.qs + (long long)(x.h * group + row - ti * group) * D + 4 * t4;
@@ -775,7 +797,7 @@ __global__ void __launch_bounds__(kThreads, R16 ? (D == 64 ? 3 : 2) : D == 64 ? 
         if (d == 0) p.part_ml[to] = make_float2(mm, den);
       } else {
         const float inv = den == 0.f ? 0.f : 1.f / den;
-        const int ti = row / group;
+        const int ti = token_of(p, row);
         const long long to = (x.tok0 + ti) * p.os + (long long)(x.h * group + row - ti * group) * D + d;
         if (p.o_f32)
           *reinterpret_cast<float4*>(static_cast<float*>(p.o) + to) = make_float4(sum.x * inv, sum.y * inv, sum.z * inv, sum.w * inv);
@@ -960,6 +982,7 @@ int launch_attention_kv8(const KV8Args& c, const AttnKV8Args& a, int num_sms, cu
   p.log2p = c.log2p;
   p.n_kv = c.n_kv;
   p.group = a.n_q / c.n_kv;
+  p.group_inv = p.group == 1 ? 0u : (unsigned)(((1ull << 32) + p.group - 1) / p.group);
   p.scale_log2e = a.scale * 1.4426950408889634f;
   p.slots = (int)part_slots(a.B, a.total_len);
   p.row_cap = (int)part_rows(a.max_new, a.n_q, c.n_kv);

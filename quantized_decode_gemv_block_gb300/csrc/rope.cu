@@ -12,9 +12,11 @@
 // quarter turn and a rest in [-1/8, 1/8] turn, whose sine and cosine come from sincospif.
 //
 // Bound by DRAM: q and k are read and written once. A CTA forms the angles of its tokens once, in
-// shared memory, and turns eight pairs per thread and turn (16-byte accesses for bf16) of all of
-// its heads. Formed by each thread for eight heads instead, in registers, the sines cost a prompt of
-// 32768 tokens, 32 + 8 heads of 128, 116.5 us in place of 111 us, 6.0 TB/s.
+// shared memory, and turns eight pairs per thread and turn (16-byte accesses for bf16) of all of its
+// heads. A prompt of 32768 tokens, 32 + 8 heads of 128 in bf16, takes 110 us, 6.1 TB/s read and written
+// (115 us with five CTAs per SM, 123 with eight, whose registers spill). With the angles formed by each
+// thread for eight heads, in registers, it took 116.5 us, and 1999 tokens of 20 heads of 64, which leave a
+// thread one head, 8.8 us in place of 4.5.
 #include <cuda_bf16.h>
 
 #include <cstdint>
@@ -144,7 +146,7 @@ __device__ __forceinline__ void store(uint16_t* p, const float (&v)[V]) {
 
 // V pairs per thread and turn: 8 where every row, head and half starts on 16 bytes, else 1.
 template <typename X, typename Y, int V, bool ADJ>
-__global__ void __launch_bounds__(kThreads) rope_kernel(const RopeParams p) {
+__global__ void __launch_bounds__(kThreads, sizeof(X) == 2 ? 6 : 5) rope_kernel(const RopeParams p) {
   __shared__ __align__(16) float sm_c[kTable], sm_s[kTable];  // [token][pair]
   const int t0 = blockIdx.x * p.tokens, nt = min(p.tokens, p.T - t0), pairs = p.pairs;
   const int h0 = blockIdx.y * p.heads, nh = min(p.heads, p.h0 + p.h1 - h0);
