@@ -7,12 +7,13 @@
 // table[r][pos / P] * P + pos % P.
 //
 // Bound by latency: a decode step's plan moves a few KB. One launch: every CTA forms both prefix
-// sums over all requests itself (two coalesced reads of 4 bytes per request from L2, a scan in
-// shared memory), then takes its share of the fresh pages and of the tokens, each found by a
-// binary search in shared memory. Sharing one scan between CTAs would need a second launch or a
-// grid barrier, each dearer than the repeated scan. A token whose page is fresh takes its id from
-// the free list, not from the table entry that another CTA may be writing, so no CTA waits for
-// another. No atomics: the result is the same in every run.
+// sums over all requests itself (two reads of 4 bytes per request from L2, one scan across the CTA),
+// then takes its share of the fresh pages and of the tokens, each found by a binary search in
+// shared memory. Sharing one scan between CTAs would need a second launch or a grid barrier, each
+// dearer than the repeated scan. A token whose page is fresh takes its id from the free list, not from
+// the table entry that another CTA may be writing, so no CTA waits for another. No atomics: the
+// result is the same in every run. Measured: 64 requests, a token each, 2.9 us; 4096 requests with
+// 524000 tokens 10.6 us (22.5 us with the scan in rounds of 256 requests).
 #include <climits>
 #include <cstdint>
 
