@@ -34,7 +34,10 @@
 // scales 512 positions at a time and fills a ring of slots, each a step of 128 positions of K or of V, by
 // bulk copies of whole pages, across items. Each of the four takes 32 positions of a step through both
 // products alone, and they meet in shared memory once per item. A request of one segment writes its
-// output there; others write partials that a second kernel joins. Windows of more than 32 tokens are not cut.
+// output there; others write partials that a second kernel joins. Windows of more than 32 tokens have blocks
+// of rows of their own to share out; over contexts from 4096 positions on, those of fewer than 32 blocks per
+// kv head are cut until there are about 32 items (one request of 40 tokens, 32 / 8 heads of 128, over
+// 131k positions takes 539 us, of 32 tokens 395).
 // Measured on the way: a CTA of four warps with nothing copied ahead across items 168 us on the decoding
 // batch below; warps that share the second product by dims, with a barrier per step, 177 us; each warp with
 // items and a ring of its own 112 to 132 us (its copies' and its items' bookkeeping weighed as much as its
@@ -67,7 +70,8 @@ constexpr int kMath = 32 * kWarps, kThreads = kMath + 32;
 constexpr int kWarpPos = 32, kStep = kWarps * kWarpPos;  // positions of a step, 32 per warp
 constexpr int kMinSegment = 512, kMaxSegments = 64;      // positions of a segment at least, segments of a request at most
 constexpr int kWindow = 32 * 16 / kStep;                 // steps whose page ids are read at once, a group of 16 tokens per lane
-constexpr int kSplitTokens = 32;                         // windows up to this many tokens are cut along the context
+constexpr int kSplitTokens = 32;                         // windows up to this many tokens are cut as above
+constexpr int kLongContext = 4096, kItems = 32;          // larger ones, over at least so many positions, into about so many items
 constexpr float kLowest = -3e38f;  // below every finite score in use: keeps -inf out of differences
 constexpr uint64_t kWaitNs = 2000000000ull;
 constexpr int kCombThreads = 256;
@@ -89,28 +93,31 @@ struct AttnKV8Params {
   int B, T, max_new, max_len, n_pages, log2p, n_kv, group;
   unsigned group_inv;  // 2^32 / group rounded up; 0 for a group of one
   float scale_log2e;
-  float* part;      // [slot][n_kv][row_cap][D]
-  float2* part_ml;  // [slot][n_kv][row_cap]: largest x, sum of weights
-  int slots, row_cap;
+  float* part;          // a request's partial rows: [kv head][segment][row][D]
+  float2* part_ml;      // [kv head][segment][row]: reference, sum of weights
+  long long part_rows;  // room per kv head
 };
 
-// log2 of a segment's positions: kMinSegment doubled until kMaxSegments hold the request.
-__host__ __device__ inline int segment_log2(int len) {
-  constexpr int kBase = kMinSegment * kMaxSegments;
-  static_assert((kBase & (kBase - 1)) == 0, "powers of two");
-  int log2 = 0;
-  while ((1 << log2) < kMinSegment) ++log2;  // a constant
+// How a request's positions are cut: a function of its own lengths.
+struct Cut {
+  int len, count;  // positions of a segment (a multiple of a step), segments
+};
+__host__ __device__ inline Cut cut_of(int len, int n, int group) {
+  if (n <= kSplitTokens) {  // segments doubled until kMaxSegments hold the request
+    constexpr int kBase = kMinSegment * kMaxSegments;
+    static_assert((kBase & (kBase - 1)) == 0 && kMinSegment == 1 << 9, "powers of two");
+    int log2 = 9;
 #ifdef __CUDA_ARCH__
-  const int over = (len - 1) / kBase;
-  return log2 + (over > 0 ? 32 - __clz(over) : 0);
+    log2 += 32 - __clz((len - 1) / kBase);
 #else
-  for (int over = (len - 1) / kBase; over > 0; over >>= 1) ++log2;
-  return log2;
+    for (int over = (len - 1) / kBase; over > 0; over >>= 1) ++log2;
 #endif
-}
-__host__ __device__ inline int segments(int len) {
-  const int s = segment_log2(len);
-  return (len + (1 << s) - 1) >> s;
+    return {1 << log2, (len + (1 << log2) - 1) >> log2};
+  }
+  const int blocks = (n * group + 15) / 16;
+  if (len < kLongContext || blocks >= kItems) return {1 << 29, 1};
+  const int want = kItems / blocks, size = ((len + want - 1) / want + kMinSegment - 1) / kMinSegment * kMinSegment;
+  return {size, (len + size - 1) / size};
 }
 
 // Warps that share a row of the combine: 8 segments each, and up to 8 warps.
@@ -125,38 +132,39 @@ __device__ __forceinline__ bool request_ok(const AttnKV8Params& p, int c, int n)
          ((c + n + (1 << p.log2p) - 1) >> p.log2p) <= p.max_blocks;
 }
 
-// The requests in shared memory: each one's first token, work item and partial slot, and its cached
+// The requests in shared memory: each one's first token, work item and partial row, and its cached
 // length. ITEMS: items of the attention kernel; otherwise CTA tasks of the combine.
 struct Request {
-  int tok, item, slot, ctx;
+  int tok, item, ctx;
+  long long part;
 };
 template <int THREADS, bool ITEMS>
 __device__ __forceinline__ void scan_requests(const AttnKV8Params& p, int row_block, Request* req, long long* sm) {
   constexpr int W = THREADS / 32;
   const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
   const int per = (p.B + THREADS - 1) / THREADS, r0 = min(tid * per, p.B), r1 = min(r0 + per, p.B);  // this thread's requests
-  long long a = 0;  // sums within them, then before them
-  int b = 0, c = 0;
+  long long a = 0, c = 0;  // sums within them, then before them
+  int b = 0;
   bool bad = false;
 #pragma unroll 2
   for (int r = r0; r < r1; ++r) {
     const int n = p.fresh[r], ctx = p.ctx[r];
-    req[r] = {(int)min(a, (long long)INT_MAX), b, c, ctx};
+    req[r] = {(int)min(a, (long long)INT_MAX), b, ctx, c};
     a += n > 0 ? n : 0;
     if (!request_ok(p, ctx, n)) bad = true;
     else if (n > 0) {
-      const int nseg = n <= kSplitTokens ? segments(ctx + n) : 1, rows = n * p.group;
+      const int nseg = cut_of(ctx + n, n, p.group).count, rows = n * p.group;
       if (ITEMS) b += (rows + row_block - 1) / row_block * nseg;
       else b += nseg <= 1 ? 0 : (rows * p.n_kv * combine_warps(nseg) + W - 1) / W;
-      c += nseg > 1 ? nseg : 0;
+      c += nseg > 1 ? (long long)nseg * rows : 0;
     }
   }
-  const long long a0 = a;
-  const int b0 = b, c0 = c;
+  const long long a0 = a, c0 = c;
+  const int b0 = b;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const long long xa = __shfl_up_sync(~0u, a, o);
-    const int xb = __shfl_up_sync(~0u, b, o), xc = __shfl_up_sync(~0u, c, o);
+    const long long xa = __shfl_up_sync(~0u, a, o), xc = __shfl_up_sync(~0u, c, o);
+    const int xb = __shfl_up_sync(~0u, b, o);
     if (lane >= o) {
       a += xa;
       b += xb;
@@ -170,31 +178,28 @@ __device__ __forceinline__ void scan_requests(const AttnKV8Params& p, int row_bl
   }
   __syncthreads();
   long long ct = 0;
-  int ci = 0, cs = 0;
+  int ci = 0;
   a -= a0;
   b -= b0;
   c -= c0;
 #pragma unroll
   for (int i = 0; i < W; ++i) {
-    const long long xa = sm[i];
-    const int xb = (int)sm[W + i], xc = (int)sm[2 * W + i];
     if (i < w) {
-      a += xa;
-      b += xb;
-      c += xc;
+      a += sm[i];
+      b += (int)sm[W + i];
+      c += sm[2 * W + i];
     }
-    ct += xa;
-    ci += xb;
-    cs += xc;
+    ct += sm[i];
+    ci += (int)sm[W + i];
   }
   for (int r = r0; r < r1; ++r) {
     req[r].tok = (int)min(a + req[r].tok, (long long)INT_MAX);
     req[r].item += b;
-    req[r].slot += c;
+    req[r].part += c;
   }
   // more tokens than q has rows, or too many items: nothing is done
   const bool over = ct > p.T || (long long)ci * p.n_kv > INT_MAX;
-  if (tid == 0) req[p.B] = {(int)min(ct, (long long)INT_MAX), over ? 0 : ci, cs, 0};
+  if (tid == 0) req[p.B] = {(int)min(ct, (long long)INT_MAX), over ? 0 : ci, 0, 0};
   if (ITEMS && (bad || over)) atomicOr(&g_kv8_errors, 2u);
   __syncthreads();
 }
@@ -265,7 +270,8 @@ struct AttnSmem {
 };
 
 struct Item {  // (request, kv head, block of query rows, segment)
-  int r, h, row0, rows, seg, nseg, ctx, len, tok0, slot;
+  int r, h, row0, rows, seg, nseg, ctx, len, tok0;
+  long long part;
   int step0, step1, end, seen;  // steps of kStep; positions from `end` on are seen by no row, those below `seen` by all
 };
 
@@ -324,14 +330,12 @@ __global__ void __launch_bounds__(kThreads, R16 ? (D == 64 ? 3 : 2) : D == 64 ? 
     const Request q = req[x.r];
     x.tok0 = q.tok;
     x.ctx = q.ctx;
-    x.slot = q.slot;
+    x.part = q.part;
     const int n = req[x.r + 1].tok - q.tok;
     x.len = q.ctx + n;
     x.rows = n * p.group;
-    const bool cut = n <= kSplitTokens;
-    const int log2 = segment_log2(x.len) - 7;  // of steps
-    static_assert(kStep == 128, "segments are cut into steps of 128");
-    x.nseg = cut ? segments(x.len) : 1;
+    const Cut cut = cut_of(x.len, n, p.group);
+    x.nseg = cut.count;
     int local = at.item - q.item, rb = 0;
     if (local >= x.nseg) {
       rb = local / x.nseg;
@@ -342,8 +346,9 @@ __global__ void __launch_bounds__(kThreads, R16 ? (D == 64 ? 3 : 2) : D == 64 ? 
     x.end = p.mask || n == 1 ? x.len : x.ctx + token_of(p, min(x.row0 + RB, x.rows) - 1) + 1;
     x.seen = x.ctx + (p.mask ? 0 : token_of(p, x.row0) + 1);
     const int last = (x.end + kStep - 1) / kStep;
-    x.step0 = cut ? x.seg << log2 : 0;
-    x.step1 = cut ? min(x.step0 + (1 << log2), last) : last;
+    static_assert(kMinSegment % kStep == 0, "segments are cut into steps");
+    x.step0 = x.seg * (cut.len / kStep);
+    x.step1 = min(x.step0 + cut.len / kStep, last);
     return x;
   };
 
@@ -764,8 +769,8 @@ __global__ void __launch_bounds__(kThreads, R16 ? (D == 64 ? 3 : 2) : D == 64 ? 
     }
     math_barrier();
     const bool partial = x.nseg > 1;
-    const long long part_slot = (long long)x.slot + x.seg;
-    const bool room = !partial || (part_slot < p.slots && x.rows <= p.row_cap);
+    const bool room = !partial || x.part + (long long)x.nseg * x.rows <= p.part_rows;
+    const long long part_row = x.part * p.n_kv + ((long long)x.h * x.nseg + x.seg) * x.rows;
     if (!room && tid == 0) atomicOr(&g_kv8_errors, 2u);
     const int live_rows = room ? min(RB, x.rows - x.row0) : 0;
     for (int e = tid; e < live_rows * (D / 4); e += kMath) {
@@ -792,7 +797,7 @@ __global__ void __launch_bounds__(kThreads, R16 ? (D == 64 ? 3 : 2) : D == 64 ? 
       sum.z += hs;
       sum.w += hs;
       if (partial) {
-        const long long to = (part_slot * p.n_kv + x.h) * p.row_cap + row;
+        const long long to = part_row + row;
         *reinterpret_cast<float4*>(p.part + to * D + d) = sum;
         if (d == 0) p.part_ml[to] = make_float2(mm, den);
       } else {
@@ -829,13 +834,13 @@ __global__ void __launch_bounds__(kCombThreads) attn_kv8_combine_kernel(const At
   const int n_q = p.n_kv * p.group, total = req[p.B].item;
   for (int it = blockIdx.x; it < total; it += gridDim.x) {
     const int r = find_request(req, p.B, it), local = it - req[r].item, tok0 = req[r].tok;
-    const int n = req[r + 1].tok - tok0, nseg = segments(req[r].ctx + n);
-    if ((long long)req[r].slot + nseg > p.slots || n * p.group > p.row_cap) continue;
+    const int n = req[r + 1].tok - tok0, nseg = cut_of(req[r].ctx + n, n, p.group).count;
+    if (req[r].part + (long long)nseg * n * p.group > p.part_rows) continue;
     const int k = combine_warps(nseg), sub = w & (k - 1);
     const int task = (local * W + w) / k;  // (token, query head) of the request
     const bool live = task < n * n_q;
     const int i = task / n_q, hq = task - i * n_q, h = hq / p.group, row = i * p.group + hq - h * p.group;
-    const long long first = ((long long)req[r].slot * p.n_kv + h) * p.row_cap + row, step = (long long)p.n_kv * p.row_cap;
+    const long long step = (long long)n * p.group, first = req[r].part * p.n_kv + h * nseg * step + row;
     float acc[E], den = 0.f;
 #pragma unroll
     for (int e = 0; e < E; ++e) acc[e] = 0.f;
@@ -928,7 +933,7 @@ int launch_typed(const AttnKV8Params& p, int num_sms, cudaStream_t s, std::strin
   if (p.max_len <= kMinSegment) return 0;  // no request can have two segments
   const long long tasks = (long long)p.T * p.n_kv * p.group;
   // no more CTAs than the longest request's rows would need: each forms the prefix sums
-  const long long want = (tasks * combine_warps(segments(p.max_len)) + kCombThreads / 32 - 1) / (kCombThreads / 32);
+  const long long want = (tasks * combine_warps(cut_of(p.max_len, 1, 1).count) + kCombThreads / 32 - 1) / (kCombThreads / 32);
   const int grid = (int)(want < (long long)num_sms * 8 ? want : (long long)num_sms * 8);
   return launch_pdl(attn_kv8_combine_kernel<D>, dim3(grid), dim3(kCombThreads), (size_t)(p.B + 1) * sizeof(Request), s, p,
                     "attention_kv8 combine", err);
@@ -941,8 +946,13 @@ int launch_dim(const AttnKV8Params& p, int num_sms, cudaStream_t s, std::string*
   return r16 ? launch_typed<D, true, false>(p, num_sms, s, err) : launch_typed<D, false, false>(p, num_sms, s, err);
 }
 
-size_t part_rows(int max_new, int n_q, int n_kv) { return (size_t)(n_q / n_kv) * (max_new < kSplitTokens ? max_new : kSplitTokens); }
-size_t part_slots(int B, long long total_len) { return (size_t)(total_len / kMinSegment) + B; }
+// Partial rows at most: windows of up to 32 tokens have len / 512 + 1 segments, larger ones segments x rows
+// <= 512, where their context is long.
+size_t part_rows(int B, long long total_len, int max_new, int group) {
+  const size_t small = (size_t)group * (max_new < kSplitTokens ? max_new : kSplitTokens) * ((size_t)(total_len / kMinSegment) + B);
+  const long long many = total_len / kLongContext < B ? total_len / kLongContext : B;
+  return small + (max_new > kSplitTokens ? (size_t)many * kItems * 16 : 0);
+}
 
 }  // namespace
 
@@ -954,7 +964,7 @@ unsigned int take_kv8_errors() {
 }
 
 size_t attention_kv8_workspace(int B, long long total_len, int max_new, int n_q, int n_kv, int D) {
-  return part_slots(B, total_len) * n_kv * part_rows(max_new, n_q, n_kv) * (D + 2) * sizeof(float);
+  return part_rows(B, total_len, max_new, n_q / n_kv) * n_kv * (D + 2) * sizeof(float);
 }
 
 int launch_attention_kv8(const KV8Args& c, const AttnKV8Args& a, int num_sms, cudaStream_t s, std::string* err) {
@@ -984,10 +994,9 @@ int launch_attention_kv8(const KV8Args& c, const AttnKV8Args& a, int num_sms, cu
   p.group = a.n_q / c.n_kv;
   p.group_inv = p.group == 1 ? 0u : (unsigned)(((1ull << 32) + p.group - 1) / p.group);
   p.scale_log2e = a.scale * 1.4426950408889634f;
-  p.slots = (int)part_slots(a.B, a.total_len);
-  p.row_cap = (int)part_rows(a.max_new, a.n_q, c.n_kv);
+  p.part_rows = (long long)part_rows(a.B, a.total_len, a.max_new, p.group);
   p.part = static_cast<float*>(a.ws);
-  p.part_ml = reinterpret_cast<float2*>(p.part + (size_t)p.slots * c.n_kv * p.row_cap * c.D);
+  p.part_ml = reinterpret_cast<float2*>(p.part + (size_t)p.part_rows * c.n_kv * c.D);
   return c.D == 64 ? launch_dim<64>(p, num_sms, s, err) : launch_dim<128>(p, num_sms, s, err);
 }
 

@@ -106,6 +106,29 @@ def test_many_requests_in_one_call_with_skipped_tokens_and_strides():
     check_pages(cache, v, "v", at)
 
 
+@pytest.mark.parametrize("P,D,n_kv,dtype", [(16, 64, 3, "f32"), (32, 128, 8, "bf16"), (64, 128, 2, "f32"), (128, 128, 4, "bf16")])
+def test_prompts_and_tokens_of_several_requests(P, D, n_kv, dtype):
+    """Calls of several thousand tokens, whose CTAs take many tokens each, over pages that hold tokens already."""
+    rng = np.random.default_rng(P)
+    lens, more = rng.integers(1, 700, 20), rng.integers(1, 300, 20)
+    nb = -(-(lens + more) // P)
+    k, v = values(int((lens + more).sum()), n_kv, D, dtype, P)
+    cache, pages = kq.KV8Cache(int(nb.sum()) + 2, P, n_kv, D), rng.permutation(int(nb.sum()) + 2)
+    first = np.concatenate([[0], np.cumsum(nb)])
+    rows, at, t = [[], []], {}, 0
+    for r in range(20):
+        for i in range(lens[r] + more[r]):
+            page = int(pages[first[r] + i // P])
+            at.setdefault(page, []).append(t)
+            rows[int(i >= lens[r])].append((t, page * P + i % P))
+            t += 1
+    for part in rows:
+        sel = torch.tensor([a for a, _ in part], device="cuda")
+        kq.kv8_append(cache, k[sel], v[sel], dev([b for _, b in part]))
+    check_pages(cache, k, "k", at)
+    check_pages(cache, v, "v", at)
+
+
 def test_borders_tiny_and_zero_values():
     P, D = 16, 64
     x = torch.zeros((16, 1, D), device="cuda")
@@ -222,6 +245,19 @@ def test_windows_and_prompts(x, y, P, D, n_q, n_kv):
 
 def test_a_context_of_more_than_128_tiles():
     attn_case([(33100, 1), (32767, 1), (70, 1)], 128, 64, 2, 1, "bf16", "f32")
+
+
+@pytest.mark.parametrize("x,y", [("bf16", "bf16"), ("f32", "f32")])
+def test_windows_of_more_than_32_tokens_over_long_contexts(x, y):
+    """Cut along the context too where their blocks of rows are few; next to requests that are cut otherwise."""
+    attn_case([(5000, 33), (4055, 40), (4056, 40), (9000, 64), (6000, 1), (4500, 300), (7, 35)], 32, 64, 4, 2, x, y)
+    attn_case([(12000, 50), (3, 3)], 16, 128, 1, 1, x, y)
+
+
+@pytest.mark.parametrize("B", [1000, 4096])
+def test_many_requests(B):
+    rng = np.random.default_rng(B)
+    attn_case([(int(c), int(n)) for c, n in zip(rng.integers(0, 60, B), rng.integers(0, 3, B))], 16, 64, 4, 1, "bf16", "f32")
 
 
 @pytest.mark.parametrize("y", ["bf16", "f32"])

@@ -74,6 +74,12 @@ def test_matches_the_formula(x, y, adjacent, T, nq, nk, D, rot, axes, view):
     case(T, nq, nk, D, rot, axes, x, y, adjacent, inverse=T % 2 == 0, view=view)
 
 
+@pytest.mark.parametrize("D,rot", [(32, 32), (24, 20)])
+def test_many_tokens(D, rot):
+    """CTAs that take several tokens each, the last of them fewer."""
+    case(5003, 2, 1, D, rot, 3, "bf16", "f32", True, False)
+
+
 def test_rows_that_start_off_16_bytes():
     rows = torch.randn((11, 3 * 64 + 1), device="cuda")
     q = rows[:, 1:1 + 128].unflatten(1, (2, 64))
