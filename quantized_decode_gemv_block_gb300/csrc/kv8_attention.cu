@@ -71,7 +71,8 @@ constexpr int kWarpPos = 32, kStep = kWarps * kWarpPos;  // positions of a step,
 constexpr int kMinSegment = 512, kMaxSegments = 64;      // positions of a segment at least, segments of a request at most
 constexpr int kWindow = 32 * 16 / kStep;                 // steps whose page ids are read at once, a group of 16 tokens per lane
 constexpr int kSplitTokens = 32;                         // windows up to this many tokens are cut as above
-constexpr int kLongContext = 4096, kItems = 32;          // larger ones, over at least so many positions, into about so many items
+constexpr int kPromptRows = 64;                          // query rows of an item of larger windows (prompts)
+constexpr int kLongContext = 4096, kItems = 32;          // prompts over at least so many positions: cut into about so many items
 constexpr float kLowest = -3e38f;  // below every finite score in use: keeps -inf out of differences
 constexpr uint64_t kWaitNs = 2000000000ull;
 constexpr int kCombThreads = 256;
@@ -114,7 +115,7 @@ __host__ __device__ inline Cut cut_of(int len, int n, int group) {
 #endif
     return {1 << log2, (len + (1 << log2) - 1) >> log2};
   }
-  const int blocks = (n * group + 15) / 16;
+  const int blocks = (n * group + kPromptRows - 1) / kPromptRows;
   if (len < kLongContext || blocks >= kItems) return {1 << 29, 1};
   const int want = kItems / blocks, size = ((len + want - 1) / want + kMinSegment - 1) / kMinSegment * kMinSegment;
   return {size, (len + size - 1) / size};
@@ -133,12 +134,13 @@ __device__ __forceinline__ bool request_ok(const AttnKV8Params& p, int c, int n)
 }
 
 // The requests in shared memory: each one's first token, work item and partial row, and its cached
-// length. ITEMS: items of the attention kernel; otherwise CTA tasks of the combine.
+// length. Items: windows of up to 32 tokens (kWindows), larger ones (kPrompts), or CTA tasks of the combine.
+enum Kind { kWindows, kPrompts, kCombine };
 struct Request {
   int tok, item, ctx;
   long long part;
 };
-template <int THREADS, bool ITEMS>
+template <int THREADS, Kind KIND>
 __device__ __forceinline__ void scan_requests(const AttnKV8Params& p, int row_block, Request* req, long long* sm) {
   constexpr int W = THREADS / 32;
   const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
@@ -154,7 +156,7 @@ __device__ __forceinline__ void scan_requests(const AttnKV8Params& p, int row_bl
     if (!request_ok(p, ctx, n)) bad = true;
     else if (n > 0) {
       const int nseg = cut_of(ctx + n, n, p.group).count, rows = n * p.group;
-      if (ITEMS) b += (rows + row_block - 1) / row_block * nseg;
+      if (KIND != kCombine) b += (n <= kSplitTokens) == (KIND == kWindows) ? (rows + row_block - 1) / row_block * nseg : 0;
       else b += nseg <= 1 ? 0 : (rows * p.n_kv * combine_warps(nseg) + W - 1) / W;
       c += nseg > 1 ? (long long)nseg * rows : 0;
     }
@@ -200,7 +202,7 @@ __device__ __forceinline__ void scan_requests(const AttnKV8Params& p, int row_bl
   // more tokens than q has rows, or too many items: nothing is done
   const bool over = ct > p.T || (long long)ci * p.n_kv > INT_MAX;
   if (tid == 0) req[p.B] = {(int)min(ct, (long long)INT_MAX), over ? 0 : ci, 0, 0};
-  if (ITEMS && (bad || over)) atomicOr(&g_kv8_errors, 2u);
+  if (KIND != kCombine && (bad || over)) atomicOr(&g_kv8_errors, 2u);
   __syncthreads();
 }
 
@@ -256,16 +258,17 @@ __device__ __forceinline__ void math_barrier() { asm volatile("bar.sync 1, %0;" 
 
 // Shared memory of a CTA: a ring of slots (a step's K or its V), the warps' outputs of an item, for 16
 // query rows the item's query operands, the requests.
-template <int D, bool R16, bool WIDE>
+enum Form { kRows8, kRows16, kPrompt };
+template <int D, Form FORM, bool WIDE>
 struct AttnSmem {
-  static constexpr int RB = R16 ? 16 : 8, PARTS = WIDE ? 2 : 1;
-  static constexpr int kDepth = D == 128 ? 3 : 6;
+  static constexpr int RB = FORM == kPrompt ? kPromptRows : FORM == kRows16 ? 16 : 8, PARTS = WIDE ? 2 : 1;
+  static constexpr int kDepth = D == 64 ? 6 : FORM == kPrompt ? 4 : 3;
   static constexpr int kSlot = kStep * D;
-  static constexpr int kOut = kDepth * kSlot;              // [warp][RB][D + 4] floats
-  static constexpr int kOutWarp = RB * (D + 4);
-  static constexpr int kQ = kOut + kWarps * kOutWarp * 4;  // [part][D / 16][32 lanes][4 words]
-  static constexpr int kQPart = R16 ? D / 16 * 512 : 0;
-  static constexpr int kReq = kQ + PARTS * kQPart;
+  static constexpr int kOut = kDepth * kSlot;                                            // [warp][RB][D + 4] floats
+  static constexpr int kOutWarp = FORM == kPrompt ? 0 : RB * (D + 4);
+  static constexpr int kQ = kOut + kWarps * kOutWarp * 4;                                // [part][D / 16][32 lanes][4 words]
+  static constexpr int kQPart = FORM == kRows8 ? 0 : D / 16 * 512;
+  static constexpr int kReq = kQ + (FORM == kPrompt ? kWarps : 1) * PARTS * kQPart;      // prompts: for each warp
   static constexpr size_t bytes(int B) { return kReq + (size_t)(B + 1) * sizeof(Request); }
 };
 
@@ -275,12 +278,14 @@ struct Item {  // (request, kv head, block of query rows, segment)
   int step0, step1, end, seen;  // steps of kStep; positions from `end` on are seen by no row, those below `seen` by all
 };
 
-// R16: 16 query rows as the A operand (scores of rows g, g + 8 in a lane); otherwise 8 as the B operand
-// (rows 2 t4, 2 t4 + 1). Both give a row the same bits: every sum over dims, positions or lanes is the
-// tensor cores' own, in the same order of k.
-template <int D, bool R16, bool WIDE>
-__global__ void __launch_bounds__(kThreads, R16 ? (D == 64 ? 3 : 2) : D == 64 ? 4 : 3) attn_kv8_kernel(const AttnKV8Params p) {
-  using S = AttnSmem<D, R16, WIDE>;
+// kRows8: 8 query rows as the B operand (rows 2 t4, 2 t4 + 1 in a lane); the others: 16 as the A operand (rows
+// g, g + 8). kRows8 and kRows16 give a row the same bits: every sum over dims, positions or lanes is the
+// tensor cores' own, in the same order of k. kPrompt: windows of more than 32 tokens, 64 rows an item, 16 for
+// each warp over all positions of a step, so that nothing is joined at the end.
+template <int D, Form FORM, bool WIDE>
+__global__ void __launch_bounds__(kThreads, FORM == kRows8 ? (D == 64 ? 4 : 3) : D == 64 ? 3 : 2) attn_kv8_kernel(const AttnKV8Params p) {
+  constexpr bool R16 = FORM != kRows8, PR = FORM == kPrompt;
+  using S = AttnSmem<D, FORM, WIDE>;
   constexpr int RB = S::RB, C32 = D / 32, K16 = D / 16, DEPTH = S::kDepth;
   constexpr int PARTS = S::PARTS;              // fp16 parts of queries and weights
   constexpr int NV = R16 ? 4 : 2;              // scores of a row per lane and group of 16 tokens
@@ -291,12 +296,13 @@ __global__ void __launch_bounds__(kThreads, R16 ? (D == 64 ? 3 : 2) : D == 64 ? 
   __shared__ long long sm_scan[3 * (kThreads / 32)];
   __shared__ __align__(16) float sm_hq[RB];  // written in pairs
   __shared__ float sm_rf[RB];
-  __shared__ float sm_m[kWarps][RB], sm_l[kWarps][RB], sm_h[kWarps][RB];
+  __shared__ float sm_m[kWarps][PR ? 1 : RB], sm_l[kWarps][PR ? 1 : RB], sm_h[kWarps][PR ? 1 : RB];
   __shared__ int sm_lim[RB];
   __shared__ uint32_t sm_mask[RB];
   Request* req = reinterpret_cast<Request*>(smem + S::kReq);
   const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5, g = lane >> 2, t4 = lane & 3;
-  uint32_t* sm_q = reinterpret_cast<uint32_t*>(smem + S::kQ);
+  const int wrow = PR ? 16 * w : 0;  // the warp's first row of the item
+  uint32_t* sm_q = reinterpret_cast<uint32_t*>(smem + S::kQ) + (PR ? w * S::PARTS * (S::kQPart / 4) : 0);
   if (tid == 0) {
     for (int k = 0; k < DEPTH; ++k) {
       mbar_init(&sm_full[k], 1);
@@ -305,7 +311,7 @@ __global__ void __launch_bounds__(kThreads, R16 ? (D == 64 ? 3 : 2) : D == 64 ? 
     fence_mbar_init();
   }
   grid_dependency_wait();
-  scan_requests<kThreads, true>(p, RB, req, sm_scan);
+  scan_requests<kThreads, PR ? kPrompts : kWindows>(p, RB, req, sm_scan);
   grid_launch_dependents();
   const int total = req[p.B].item, P = 1 << p.log2p;
   // items x kv heads, a CTA's shares gridDim.x apart: (item, head) moves by (d_item, d_head)
@@ -417,10 +423,9 @@ __global__ void __launch_bounds__(kThreads, R16 ? (D == 64 ? 3 : 2) : D == 64 ? 
     return;
   }
 
-  auto free_slot = [&]() {  // its codes are used
+  auto free_slot = [&](int s) {  // its codes are used
     __syncwarp();
-    if (lane == 0) mbar_arrive(&sm_empty[slot]);
-    next_slot();
+    if (lane == 0) mbar_arrive(&sm_empty[s]);
   };
   int steps = 0;
   for (Place at = place0; at.item < total; move(at)) {
@@ -433,9 +438,9 @@ __global__ void __launch_bounds__(kThreads, R16 ? (D == 64 ? 3 : 2) : D == 64 ? 
     float hq[2], rf[2];
     int lim[2];
     uint32_t see[2];
-    if (!R16 || w < 2) {
-      const int nt = R16 ? w : 0;
-      const int row = x.row0 + 8 * nt + g, ti = token_of(p, row);
+#pragma unroll 1
+    for (int nt = R16 && !PR ? w : 0; nt < (R16 ? 2 : 1); nt += R16 && !PR ? kWarps : 1) {
+      const int row = x.row0 + wrow + 8 * nt + g, ti = token_of(p, row);
       const bool live = row < x.rows;
       float v[K16][4];
       const long long from = (x.tok0 + ti) * p.qs + (long long)(x.h * group + row - ti * group) * D + 4 * t4;
@@ -502,11 +507,11 @@ __global__ void __launch_bounds__(kThreads, R16 ? (D == 64 ? 3 : 2) : D == 64 ? 
       const int last = live ? x.ctx + ti : -1;
       const uint32_t word = live && p.mask ? p.mask[x.tok0 + ti] : 0u;
       if (R16) {
-        if (g == 0) *reinterpret_cast<float2*>(sm_hq + 8 * nt + 2 * t4) = make_float2(half[0], half[1]);
+        if (g == 0) *reinterpret_cast<float2*>(sm_hq + wrow + 8 * nt + 2 * t4) = make_float2(half[0], half[1]);
         if (t4 == 0) {
-          sm_rf[8 * nt + g] = factor;
-          sm_lim[8 * nt + g] = last;
-          sm_mask[8 * nt + g] = word;
+          sm_rf[wrow + 8 * nt + g] = factor;
+          sm_lim[wrow + 8 * nt + g] = last;
+          sm_mask[wrow + 8 * nt + g] = word;
         }
       } else {
 #pragma unroll
@@ -519,13 +524,14 @@ __global__ void __launch_bounds__(kThreads, R16 ? (D == 64 ? 3 : 2) : D == 64 ? 
       }
     }
     if (R16) {
-      math_barrier();
+      if (PR) __syncwarp();
+      else math_barrier();
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
-        hq[k] = sm_hq[g + 8 * k];
-        rf[k] = sm_rf[g + 8 * k];
-        lim[k] = sm_lim[g + 8 * k];
-        see[k] = sm_mask[g + 8 * k];
+        hq[k] = sm_hq[wrow + g + 8 * k];
+        rf[k] = sm_rf[wrow + g + 8 * k];
+        lim[k] = sm_lim[wrow + g + 8 * k];
+        see[k] = sm_mask[wrow + g + 8 * k];
       }
     }
 
@@ -539,8 +545,22 @@ __global__ void __launch_bounds__(kThreads, R16 ? (D == 64 ? 3 : 2) : D == 64 ? 
 #pragma unroll
     for (int s = 0; s < NO; ++s) o[s][0] = o[s][1] = o[s][2] = o[s][3] = 0.f;
 
+    // prompts: what this warp's rows see ends, and is seen by all of them, of its own
+    const int w_end = PR ? x.ctx + token_of(p, max(min(x.row0 + wrow + 16, x.rows) - 1, 0)) + 1 : x.end;
+    const int w_seen = PR ? x.ctx + token_of(p, x.row0 + wrow) + 1 : x.seen;
     for (int step = x.step0; step < x.step1; ++step, ++steps) {
-      const uint8_t* kst = smem + slot * S::kSlot + w * kWarpPos * D;
+      const int k_slot = slot;
+      wait(&sm_full[slot], phase);
+      next_slot();
+      const int v_slot = slot;
+      const uint32_t v_phase = phase;
+      next_slot();
+      if (PR) wait(&sm_full[v_slot], v_phase);
+#pragma unroll 1
+      for (int part32 = PR ? 0 : w; part32 < (PR ? kWarps : w + 1); ++part32) {  // 32 positions
+      const int pos32 = step * kStep + part32 * kWarpPos;
+      if (PR && (pos32 >= w_end || x.row0 + wrow >= x.rows)) break;
+      const uint8_t* kst = smem + k_slot * S::kSlot + part32 * kWarpPos * D;
       // ---- scores: [group][R16: the group's token pairs 4 t, 4 t + 1 and 4 t + 2, 4 t + 3]
       float sc[2][R16 ? 2 : 1][4];
 #pragma unroll
@@ -549,8 +569,7 @@ __global__ void __launch_bounds__(kThreads, R16 ? (D == 64 ? 3 : 2) : D == 64 ? 
         for (int i = 0; i < (R16 ? 2 : 1); ++i)
 #pragma unroll
           for (int e = 0; e < 4; ++e) sc[st][i][e] = hq[R16 ? e >> 1 : e & 1];
-      wait(&sm_full[slot], phase);
-      const float2 kf2 = lds_f2(&sm_scale[steps & 3][0][2 * w]), vf2 = lds_f2(&sm_scale[steps & 3][1][2 * w]);
+      const float2 kf2 = lds_f2(&sm_scale[steps & 3][0][2 * part32]), vf2 = lds_f2(&sm_scale[steps & 3][1][2 * part32]);
       const float kf[2] = {kf2.x, kf2.y}, vf[2] = {vf2.x, vf2.y};
 #pragma unroll
       for (int cc = 0; cc < C32; ++cc) {
@@ -591,10 +610,10 @@ __global__ void __launch_bounds__(kThreads, R16 ? (D == 64 ? 3 : 2) : D == 64 ? 
           }
         }
       }
-      free_slot();
+      if (!PR) free_slot(k_slot);
       // ---- weights against the page's largest score, up by 2^15 into fp16's range
       // value v of row k in group st is score sc[st][..] below, of position pos0 + 16 st + (R16 ? v : 2 v)
-      const int pos0 = step * kStep + w * kWarpPos + (R16 ? 4 * t4 : 4 * (g >> 1) + (g & 1));
+      const int pos0 = pos32 + (R16 ? 4 * t4 : 4 * (g >> 1) + (g & 1));
       float sv[2][2][NV];
 #pragma unroll
       for (int st = 0; st < 2; ++st)
@@ -605,7 +624,7 @@ __global__ void __launch_bounds__(kThreads, R16 ? (D == 64 ? 3 : 2) : D == 64 ? 
           for (int v = 0; v < NV; ++v) sv[st][k][v] = r * (R16 ? sc[st][R16 ? v >> 1 : 0][2 * k + (v & 1)] : sc[st][0][k + 2 * (v & 1)]);
         }
       // all positions seen by every row: nothing to mask (rows past the last come along: nothing reads them)
-      if (step * kStep + (w + 1) * kWarpPos > x.seen) {
+      if (pos32 + kWarpPos > w_seen) {
 #pragma unroll
         for (int st = 0; st < 2; ++st)
 #pragma unroll
@@ -687,7 +706,7 @@ __global__ void __launch_bounds__(kThreads, R16 ? (D == 64 ? 3 : 2) : D == 64 ? 
           for (int e = 0; e < 4; ++e) o[s][e] *= al[R16 ? e >> 1 : e & 1];
       }
       // ---- sums of the weights, then values: a page's products are added up before its scale
-      const uint8_t* vst = smem + slot * S::kSlot + w * kWarpPos * D;
+      const uint8_t* vst = smem + v_slot * S::kSlot + part32 * kWarpPos * D;
       constexpr uint32_t kOnes = 0x3C003C00u;
       const uint32_t ones[4] = {kOnes, kOnes, kOnes, kOnes};
       float acc[4] = {0.f, 0.f, 0.f, 0.f};
@@ -708,7 +727,7 @@ __global__ void __launch_bounds__(kThreads, R16 ? (D == 64 ? 3 : 2) : D == 64 ? 
           acc[0] = acc[1] = acc[2] = acc[3] = 0.f;
         }
       }
-      wait(&sm_full[slot], phase);
+      if (!PR) wait(&sm_full[v_slot], v_phase);
 #pragma unroll
       for (int cc = 0; cc < C32; ++cc) {
         constexpr int NA = R16 ? 4 : 2;  // output tiles of 32 dims
@@ -742,9 +761,34 @@ __global__ void __launch_bounds__(kThreads, R16 ? (D == 64 ? 3 : 2) : D == 64 ? 
           }
         }
       }
-      free_slot();
+      }
+      if (PR) free_slot(k_slot);
+      free_slot(v_slot);
     }
 
+    const bool partial = x.nseg > 1;
+    const bool room = !partial || x.part + (long long)x.nseg * x.rows <= p.part_rows;
+    const long long part_row = x.part * p.n_kv + ((long long)x.h * x.nseg + x.seg) * x.rows;
+    if (!room && tid == 0) atomicOr(&g_kv8_errors, 2u);
+    if (PR) {  // this warp's rows are done
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        const int row = x.row0 + wrow + g + 8 * k, ti = token_of(p, row);
+        if (row >= x.rows || !room) continue;
+        const float half = 0.5f * hv[k], inv = partial ? 1.f : l[k] == 0.f ? 0.f : 1.f / l[k];
+        const long long to = partial ? (part_row + row) * D : (x.tok0 + ti) * p.os + (long long)(x.h * group + row - ti * group) * D;
+#pragma unroll
+        for (int s = 0; s < NO; ++s) {  // dims 8 s + 2 t4, + 1
+          const float v0 = (o[s][R16 ? 2 * k : 0] + half) * inv, v1 = (o[s][R16 ? 2 * k + 1 : 0] + half) * inv;
+          const long long at_d = to + 8 * s + 2 * t4;
+          if (partial) *reinterpret_cast<float2*>(p.part + at_d) = make_float2(v0, v1);
+          else if (p.o_f32) *reinterpret_cast<float2*>(static_cast<float*>(p.o) + at_d) = make_float2(v0, v1);
+          else *reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(p.o) + at_d) = (uint32_t)f32_to_bf16_rn(v0) | (uint32_t)f32_to_bf16_rn(v1) << 16;
+        }
+        if (partial && t4 == 0) p.part_ml[part_row + row] = make_float2(m[k], l[k]);
+      }
+      continue;
+    }
     // ---- the four warps' results meet
     float* out = reinterpret_cast<float*>(smem + S::kOut);
     float* mine = out + w * S::kOutWarp;
@@ -768,10 +812,6 @@ __global__ void __launch_bounds__(kThreads, R16 ? (D == 64 ? 3 : 2) : D == 64 ? 
       }
     }
     math_barrier();
-    const bool partial = x.nseg > 1;
-    const bool room = !partial || x.part + (long long)x.nseg * x.rows <= p.part_rows;
-    const long long part_row = x.part * p.n_kv + ((long long)x.h * x.nseg + x.seg) * x.rows;
-    if (!room && tid == 0) atomicOr(&g_kv8_errors, 2u);
     const int live_rows = room ? min(RB, x.rows - x.row0) : 0;
     for (int e = tid; e < live_rows * (D / 4); e += kMath) {
       const int rr = e / (D / 4), d = (e - rr * (D / 4)) * 4, row = x.row0 + rr;
@@ -829,7 +869,7 @@ __global__ void __launch_bounds__(kCombThreads) attn_kv8_combine_kernel(const At
   const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
   // the lengths were written before the attention kernel passed its own wait, after which alone this
   // kernel can start
-  scan_requests<kCombThreads, false>(p, 1, req, sm_scan);
+  scan_requests<kCombThreads, kCombine>(p, 1, req, sm_scan);
   grid_dependency_wait();
   const int n_q = p.n_kv * p.group, total = req[p.B].item;
   for (int it = blockIdx.x; it < total; it += gridDim.x) {
@@ -906,10 +946,10 @@ __global__ void __launch_bounds__(kCombThreads) attn_kv8_combine_kernel(const At
   }
 }
 
-template <int D, bool R16, bool WIDE>
-int launch_typed(const AttnKV8Params& p, int num_sms, cudaStream_t s, std::string* err) {
-  const size_t smem = AttnSmem<D, R16, WIDE>::bytes(p.B);
-  auto* kernel = attn_kv8_kernel<D, R16, WIDE>;
+template <int D, Form FORM, bool WIDE>
+int launch_form(const AttnKV8Params& p, int num_sms, cudaStream_t s, std::string* err) {
+  const size_t smem = AttnSmem<D, FORM, WIDE>::bytes(p.B);
+  auto* kernel = attn_kv8_kernel<D, FORM, WIDE>;
   // CTAs per SM at this shared-memory size, asked for once per host thread, device and size
   static thread_local int known_dev = -1, per_sm = 0;
   static thread_local size_t known_smem = 0;
@@ -929,7 +969,16 @@ int launch_typed(const AttnKV8Params& p, int num_sms, cudaStream_t s, std::strin
     *err = std::string("attention_kv8: ") + (e != cudaSuccess ? cudaGetErrorString(e) : "the kernel does not fit an SM");
     return -1;
   }
-  if (launch_pdl(kernel, dim3(num_sms * per_sm), dim3(kThreads), smem, s, p, "attention_kv8", err, true) != 0) return -1;
+  return launch_pdl(kernel, dim3(num_sms * per_sm), dim3(kThreads), smem, s, p, "attention_kv8", err, true);
+}
+
+// Windows of up to 32 tokens, and, where max_new allows larger ones, those in a launch of their own: which
+// form a request takes, and its bits, do not depend on the others.
+template <int D, bool WIDE>
+int launch_all(const AttnKV8Params& p, int num_sms, cudaStream_t s, std::string* err) {
+  const bool rows8 = (long long)p.max_new * p.group <= 8;
+  if ((rows8 ? launch_form<D, kRows8, WIDE>(p, num_sms, s, err) : launch_form<D, kRows16, WIDE>(p, num_sms, s, err)) != 0) return -1;
+  if (p.max_new > kSplitTokens && launch_form<D, kPrompt, WIDE>(p, num_sms, s, err) != 0) return -1;
   if (p.max_len <= kMinSegment) return 0;  // no request can have two segments
   const long long tasks = (long long)p.T * p.n_kv * p.group;
   // no more CTAs than the longest request's rows would need: each forms the prefix sums
@@ -941,17 +990,15 @@ int launch_typed(const AttnKV8Params& p, int num_sms, cudaStream_t s, std::strin
 
 template <int D>
 int launch_dim(const AttnKV8Params& p, int num_sms, cudaStream_t s, std::string* err) {
-  const bool r16 = (long long)p.max_new * p.group > 8;
-  if (p.o_f32) return r16 ? launch_typed<D, true, true>(p, num_sms, s, err) : launch_typed<D, false, true>(p, num_sms, s, err);
-  return r16 ? launch_typed<D, true, false>(p, num_sms, s, err) : launch_typed<D, false, false>(p, num_sms, s, err);
+  return p.o_f32 ? launch_all<D, true>(p, num_sms, s, err) : launch_all<D, false>(p, num_sms, s, err);
 }
 
 // Partial rows at most: windows of up to 32 tokens have len / 512 + 1 segments, larger ones segments x rows
-// <= 512, where their context is long.
+// <= 32 blocks of 64, where their context is long.
 size_t part_rows(int B, long long total_len, int max_new, int group) {
   const size_t small = (size_t)group * (max_new < kSplitTokens ? max_new : kSplitTokens) * ((size_t)(total_len / kMinSegment) + B);
   const long long many = total_len / kLongContext < B ? total_len / kLongContext : B;
-  return small + (max_new > kSplitTokens ? (size_t)many * kItems * 16 : 0);
+  return small + (max_new > kSplitTokens ? (size_t)many * kItems * kPromptRows : 0);
 }
 
 }  // namespace
