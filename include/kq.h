@@ -459,7 +459,8 @@ int kq_kv8_append(const kq_kv8_cache* cache, int x_dtype, const void* k, long lo
  * on its own request alone: not on the other requests, nor, in windows of up to 32 tokens, on how many
  * tokens follow it (for the same pages: appending a token may coarsen its page's codes).
  * T <= 2^20, B <= KQ_KV8_MAX_REQUESTS, n_q / n_kv <= 64, max_len <= 2^28.
- * workspace: kq_attention_kv8_workspace_size() bytes, 256-byte aligned. At most two launches.
+ * workspace: kq_attention_kv8_workspace_size() bytes, 256-byte aligned. At most two launches, three where
+ * max_new > 32.
  * Errors: KQ_ERR_ARG, KQ_ERR_UNSUPPORTED, KQ_ERR_WORKSPACE, KQ_ERR_CUDA. */
 enum { KQ_KV8_MAX_REQUESTS = 4096 };
 size_t kq_attention_kv8_workspace_size(int B, long long total_len, int max_new, int n_q, int n_kv, int head_dim);

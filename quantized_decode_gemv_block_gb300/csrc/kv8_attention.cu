@@ -34,10 +34,14 @@
 // scales 512 positions at a time and fills a ring of slots, each a step of 128 positions of K or of V, by
 // bulk copies of whole pages, across items. Each of the four takes 32 positions of a step through both
 // products alone, and they meet in shared memory once per item. A request of one segment writes its
-// output there; others write partials that a second kernel joins. Windows of more than 32 tokens have blocks
-// of rows of their own to share out; over contexts from 4096 positions on, those of fewer than 32 blocks per
-// kv head are cut until there are about 32 items (one request of 40 tokens, 32 / 8 heads of 128, over
-// 131k positions takes 539 us, of 32 tokens 395).
+// output there; others write partials that a second kernel joins.
+//   Windows of more than 32 tokens (prompts) run in a launch of their own, where max_new allows them: blocks of
+// 64 rows, 16 for each warp, which takes its rows over all positions and writes them alone. Contexts from 4096
+// positions on with fewer than 32 blocks per kv head are cut until there are about 32 items (one request over
+// 131k positions, 32 / 8 heads of 128: 395 us for 32 tokens, 611 for 33, 757 for 64). In the windows' form 2 x
+// 2048 tokens took 437 us in place of 368, 38 requests of 155 to 311 tokens (fp32, 16 / 8 heads) 221 in place
+// of 163. Codes converted once for all warps into shared memory: with 8 warps and 128 rows 374 and 198 us, with
+// 4 warps 393 and 198 us; the barriers cost more than the conversions.
 // Measured on the way: a CTA of four warps with nothing copied ahead across items 168 us on the decoding
 // batch below; warps that share the second product by dims, with a barrier per step, 177 us; each warp with
 // items and a ring of its own 112 to 132 us (its copies' and its items' bookkeeping weighed as much as its
@@ -49,7 +53,7 @@
 // positions 166 us, 6.3 TB/s (of 6.79 copied). Windows and prompts are bound by the multiplying warps'
 // latency (two or three of them per scheduler): the conversions, the softmax and the products follow one
 // another in each, 92 us for 16 requests x 8 tokens x 4 heads per kv head of 128 over 1000 to 9000
-// positions, 178 MB, and 150 to 175 TFLOP/s for prompts.
+// positions, 178 MB, and 175 to 210 TFLOP/s for prompts.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
