@@ -320,12 +320,24 @@ def _heads(name: str, t: torch.Tensor, heads: int | None = None, dim: int | None
     return s0 if T > 1 else H * D
 
 
+def _empty(shape, dtype, device, stream) -> torch.Tensor:
+    """An output or workspace of a call on `stream`: from that stream's pool, so that its memory goes back to
+    work that runs behind the call, and not to another stream's."""
+    if stream is None or torch.device(device).type != "cuda":
+        return torch.empty(shape, dtype=dtype, device=device)
+    if not isinstance(stream, torch.cuda.Stream):
+        raw = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+        stream = torch.cuda.ExternalStream(raw, device) if raw else torch.cuda.default_stream(device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
 class PagesPlan:
     """Outputs of pages_plan (device tensors): cu [B+1], pos [T], slot [T], n_free [1], status [1]."""
     __slots__ = ("cu", "pos", "slot", "n_free", "status")
 
-    def __init__(self, B: int, T: int, device="cuda"):
-        buf = torch.empty(B + 1 + 2 * T + 2, dtype=torch.int32, device=device)
+    def __init__(self, B: int, T: int, device="cuda", stream=None):
+        buf = _empty(B + 1 + 2 * T + 2, torch.int32, device, stream)
         self.cu, self.pos, self.slot, self.n_free, self.status = buf.split_with_sizes((B + 1, T, T, 1, 1))
 
 
@@ -335,7 +347,7 @@ def pages_plan(ctx_len: torch.Tensor, new_len: torch.Tensor, block_table: torch.
     (B x max_blocks) is updated; n_free is read, the new count is in the result."""
     B, width = block_table.shape
     if out is None:
-        out = PagesPlan(B, T, block_table.device)
+        out = PagesPlan(B, T, block_table.device, stream)
         base = out.cu.data_ptr()
         outs = (base + 4 * (B + 1 + 2 * T), base, base + 4 * (B + 1), base + 4 * (B + 1 + T))
         status = base + 4 * (B + 2 + 2 * T)
@@ -357,7 +369,7 @@ def pages_release(length: torch.Tensor, done: torch.Tensor, block_table: torch.T
     if done.dtype not in (torch.bool, torch.uint8) or not done.is_contiguous() or done.numel() < B:
         raise ValueError("done must be a contiguous bool or uint8 tensor with one element per request")
     if status is None:
-        status = torch.empty(1, dtype=torch.int32, device=block_table.device)
+        status = _empty(1, torch.int32, block_table.device, stream)
     _check(lib().kq_pages_release(_i32("length", length, B), done.data_ptr(), B, page_size,
                                   _i32("block_table", block_table, B * width), width, _i32("free_pages", free_pages, 0),
                                   free_pages.numel(), _i32("n_free", n_free, 1), _i32("n_free_out", n_free_out, 1),
@@ -385,9 +397,9 @@ def rope(q: torch.Tensor | None, k: torch.Tensor | None, pos: torch.Tensor, inv_
     none = (None, 0, None, 0, 0)
     qa = ka = none
     if q is not None:
-        q_out, qa = _rope_side("q", q, q_out, ref, y_dtype)
+        q_out, qa = _rope_side("q", q, q_out, ref, y_dtype, stream)
     if k is not None:
-        k_out, ka = _rope_side("k", k, k_out, ref, y_dtype)
+        k_out, ka = _rope_side("k", k, k_out, ref, y_dtype, stream)
     flags = (KQ_ROPE_ADJACENT if adjacent else 0) | (KQ_ROPE_INVERSE if inverse else 0)
     _check(lib().kq_rope(_dtype(ref.dtype), _dtype(y_dtype), *qa, *ka, T, D, 2 * pairs, inv_freq.data_ptr(),
                          pair_axis.data_ptr() if pair_axis is not None else None, _i32("pos", pos, axes * T), axes,
@@ -395,14 +407,14 @@ def rope(q: torch.Tensor | None, k: torch.Tensor | None, pos: torch.Tensor, inv_
     return q_out if q is not None else None, k_out if k is not None else None
 
 
-def _rope_side(name, x, y, ref, y_dtype):
+def _rope_side(name, x, y, ref, y_dtype, stream):
     """The output of one of rope's tensors, and its five arguments."""
     if x is not ref and (x.dtype is not ref.dtype or x.shape[0] != ref.shape[0] or x.shape[2] != ref.shape[2]):
         raise ValueError("q and k must agree in type, tokens and head_dim")
     xs = _heads(name, x)
     H, D = x.shape[1], x.shape[2]
     if y is None:
-        y = torch.empty(x.shape, dtype=y_dtype, device=x.device)
+        y = _empty(x.shape, y_dtype, x.device, stream)
         return y, (x.data_ptr(), xs, y.data_ptr(), H * D, H)
     if y.shape != x.shape or y.dtype is not y_dtype:
         raise ValueError(f"{name}_out must have {name}'s shape, and both outputs one type")
@@ -465,14 +477,14 @@ def attention_kv8(q: torch.Tensor, cache: KV8Cache, block_table: torch.Tensor, c
     if total_len is None:
         total_len = B * max_len
     if out is None:
-        out, out_stride = torch.empty((T, n_q, D), dtype=out_dtype or q.dtype, device=q.device), n_q * D
+        out, out_stride = _empty((T, n_q, D), out_dtype or q.dtype, q.device, stream), n_q * D
     elif out.shape != q.shape or (out_dtype is not None and out.dtype != out_dtype):
         raise ValueError("out must have q's shape and out_dtype")
     else:
         out_stride = _heads("out", out, n_q, D)
     if workspace is None:
         need = attention_kv8_workspace_size(B, total_len, max_new, n_q, cache.n_kv, D)
-        workspace = torch.empty(max(need, 256), dtype=torch.uint8, device=q.device)
+        workspace = _empty(max(need, 256), torch.uint8, q.device, stream)
     _check(lib().kq_attention_kv8(cache._ref, _dtype(q.dtype), q.data_ptr(), _heads("q", q, None, cache.head_dim),
                                   _dtype(out.dtype), out.data_ptr(), out_stride, n_q,
                                   _i32("ctx_len", ctx_len, B), _i32("new_len", new_len, B), B, T, max_new, max_len,

@@ -423,3 +423,37 @@ def test_offsets_beyond_32_bits():
     parts = (plain.codes_of(k[sub].cpu().numpy(), P, D, "k"), cache.k_scale[sub].cpu().numpy(),
              plain.codes_of(v[sub].cpu().numpy(), P, D, "v"), cache.v_scale[sub].cpu().numpy())
     check(o, q, parts, np.array([[0, 1, 2]]), np.array([299]), np.array([1]), P, n_kv, D ** -0.5)
+
+
+@pytest.mark.parametrize("handle", [False, True])
+def test_memory_of_calls_on_a_given_stream(handle, monkeypatch):
+    """What a call allocates itself comes from its stream's pool: what the current stream asks for next is elsewhere."""
+    P, D, n_q, n_kv = 16, 64, 4, 2
+    cache, parts, table, ctx, new, q = make([(1300, 1), (50, 1)], P, D, n_q, n_kv, "bf16", 12)
+    td, cd, nd = dev(table), dev(ctx), dev(new)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    real, seen = kq.lib(), []
+
+    class Spy:
+        def __getattr__(self, name):
+            def call(*args):
+                if name == "kq_attention_kv8":
+                    seen.append((args[5], args[-3]))  # o, workspace
+                return getattr(real, name)(*args)
+            return call
+
+    monkeypatch.setattr(kq, "lib", Spy)
+    stream = s.cuda_stream if handle else s
+    o = kq.attention_kv8(q, cache, td, cd, nd, 1, 1400, total_len=1400, out_dtype=torch.float32, stream=stream)
+    need = kq.attention_kv8_workspace_size(2, 1400, 1, n_q, n_kv, D)
+    other = torch.full((need,), 255, dtype=torch.uint8, device="cuda")
+    assert seen[0][0] == o.data_ptr() and seen[0][1] != other.data_ptr()
+    table2, free, n_free, pos, freq = td.clone(), dev([1, 2, 3]), dev([3]), dev([0, 0]), torch.ones(8, device="cuda")
+    s.wait_stream(torch.cuda.current_stream())
+    plan = kq.pages_plan(cd, nd, table2, free, n_free, P, 2, stream=stream)
+    turned, _ = kq.rope(q, None, pos, freq, stream=stream)
+    s.synchronize()
+    check(o, q, parts, table, ctx, new, P, n_kv, D ** -0.5)
+    assert plan.pos.tolist() == [1300, 50] and plan.status.item() == 0
+    assert torch.equal(turned, q)
