@@ -301,10 +301,21 @@ def _dtype(t) -> int:
 _I32 = torch.int32
 
 
+class HostMemoryError(KQError, ValueError):
+    """A tensor in host memory where a kernel would read its address."""
+
+
+def _not_on_gpu(name: str):
+    if torch.cuda.is_available():  # without a GPU the library refuses the call
+        raise HostMemoryError(KQ_ERR_ARG, f"{name} must be on the GPU")
+
+
 def _i32(name: str, t: torch.Tensor, n: int) -> int:
     """The address of a contiguous int32 tensor of at least n elements."""
     if t.dtype is not _I32 or t.numel() < n or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous int32 tensor of at least {n} elements")
+    if not t.is_cuda:
+        _not_on_gpu(name)
     return t.data_ptr()
 
 
@@ -312,6 +323,8 @@ def _heads(name: str, t: torch.Tensor, heads: int | None = None, dim: int | None
     """The token stride of a (T, heads, dim) tensor whose heads stand next to each other."""
     if t.dim() != 3:
         raise ValueError(f"{name} must be (tokens, heads, head_dim)")
+    if not t.is_cuda:
+        _not_on_gpu(name)
     (T, H, D), (s0, s1, s2) = t.shape, t.stride()
     if (s2 != 1 and D > 1) or (s1 != D and H > 1):
         raise ValueError(f"{name} must be (tokens, heads, head_dim) with contiguous heads")
@@ -368,6 +381,8 @@ def pages_release(length: torch.Tensor, done: torch.Tensor, block_table: torch.T
     B, width = block_table.shape
     if done.dtype not in (torch.bool, torch.uint8) or not done.is_contiguous() or done.numel() < B:
         raise ValueError("done must be a contiguous bool or uint8 tensor with one element per request")
+    if not done.is_cuda:
+        _not_on_gpu("done")
     if status is None:
         status = _empty(1, torch.int32, block_table.device, stream)
     _check(lib().kq_pages_release(_i32("length", length, B), done.data_ptr(), B, page_size,
@@ -393,6 +408,8 @@ def rope(q: torch.Tensor | None, k: torch.Tensor | None, pos: torch.Tensor, inv_
         raise ValueError("inv_freq must be contiguous fp32")
     if pair_axis is not None and (pair_axis.dtype != torch.uint8 or not pair_axis.is_contiguous() or pair_axis.numel() != pairs):
         raise ValueError("pair_axis must be contiguous uint8, one per pair")
+    if not inv_freq.is_cuda or (pair_axis is not None and not pair_axis.is_cuda):
+        _not_on_gpu("inv_freq and pair_axis")
     y_dtype = out_dtype or (q_out if q_out is not None else k_out if k_out is not None else ref).dtype
     none = (None, 0, None, 0, 0)
     qa = ka = none
@@ -449,14 +466,17 @@ class KV8Cache:
         self.c = KV8CacheC(self.k.data_ptr(), self.v.data_ptr(), self.k_scale.data_ptr(), self.v_scale.data_ptr(),
                            n_pages, page_size, n_kv, head_dim)
         self._ref = ctypes.addressof(self.c)
+        self._on_gpu = all(t.is_cuda for t in (self.k, self.v, self.k_scale, self.v_scale))
 
 
 def kv8_append(cache: KV8Cache, k: torch.Tensor, v: torch.Tensor, slot: torch.Tensor, stream=None) -> None:
     """Quantize k and v (T, n_kv, head_dim) into their slots (int32 [T], -1 skips) through kq_kv8_append."""
     if k.dtype != v.dtype or k.shape[0] != v.shape[0]:
         raise ValueError("k and v must agree in type and tokens")
-    T = k.shape[0]
-    _check(lib().kq_kv8_append(cache._ref, _dtype(k.dtype), k.data_ptr(), _heads("k", k, cache.n_kv, cache.head_dim),
+    T, x_dtype = k.shape[0], _dtype(k.dtype)
+    if not cache._on_gpu:
+        _not_on_gpu("the cache")
+    _check(lib().kq_kv8_append(cache._ref, x_dtype, k.data_ptr(), _heads("k", k, cache.n_kv, cache.head_dim),
                                v.data_ptr(), _heads("v", v, cache.n_kv, cache.head_dim), _i32("slot", slot, T), T,
                                _stream(stream)))
 
@@ -485,6 +505,10 @@ def attention_kv8(q: torch.Tensor, cache: KV8Cache, block_table: torch.Tensor, c
     if workspace is None:
         need = attention_kv8_workspace_size(B, total_len, max_new, n_q, cache.n_kv, D)
         workspace = _empty(max(need, 256), torch.uint8, q.device, stream)
+    elif not workspace.is_cuda:
+        _not_on_gpu("workspace")
+    if not cache._on_gpu:
+        _not_on_gpu("the cache")
     _check(lib().kq_attention_kv8(cache._ref, _dtype(q.dtype), q.data_ptr(), _heads("q", q, None, cache.head_dim),
                                   _dtype(out.dtype), out.data_ptr(), out_stride, n_q,
                                   _i32("ctx_len", ctx_len, B), _i32("new_len", new_len, B), B, T, max_new, max_len,

@@ -145,3 +145,17 @@ def test_binding_refuses_wrong_tensors(kq):
         kq.attention_kv8(q, cache, i(2, 1), i(2), i(2), 1, 16, out=q[:2], stream=0)
     with pytest.raises(kq.KQError):
         kq.attention_kv8(torch.zeros((3, 3, 64), dtype=torch.bfloat16), cache, i(2, 1), i(2), i(2), 1, 16, stream=0)
+
+
+def test_tensors_in_host_memory_are_refused_where_there_is_a_gpu(kq, monkeypatch):
+    i = lambda *s: torch.zeros(s, dtype=torch.int32)  # noqa: E731
+    cache = kq.KV8Cache(2, 16, 2, 64, device="cpu")
+    monkeypatch.setattr(torch.cuda, "is_available", lambda: True)
+    x = torch.zeros((3, 2, 64), dtype=torch.bfloat16)
+    for call in (lambda: kq.kv8_append(cache, x, x, i(3), stream=0),
+                 lambda: kq.attention_kv8(x, cache, i(2, 1), i(2), i(2), 1, 16, stream=0),
+                 lambda: kq.rope(x, None, i(3), torch.zeros(32), stream=0),
+                 lambda: kq.pages_plan(i(2), i(2), i(2, 4), i(9), i(1), 16, 8, stream=0),
+                 lambda: kq.pages_release(i(2), i(2).bool(), i(2, 4), i(9), i(1), i(1), 16, stream=0)):
+        with pytest.raises(ValueError, match="must be on the GPU"):
+            call()
