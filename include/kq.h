@@ -383,7 +383,7 @@ enum { KQ_PAGES_MAX_REQUESTS = 4096 };
  *   cu                B+1 ints (output); pos, slot: T ints (output), T the tokens' capacity.
  *                     slot = page * P + position % P. Rows past the last token get pos 0, slot -1
  *   status            one word (output)
- * max_blocks * P <= 2^30. One launch. Errors: KQ_ERR_ARG, KQ_ERR_CUDA. */
+ * max_blocks * P, free_capacity and T <= 2^30. One launch. Errors: KQ_ERR_ARG, KQ_ERR_CUDA. */
 int kq_pages_plan(const int* ctx_len, const int* new_len, int B, int page_size, int* block_table, int max_blocks,
                   const int* free_pages, int free_capacity, const int* n_free, int* n_free_out, int* cu, int* pos,
                   int* slot, int T, unsigned int* status, void* stream);
@@ -405,7 +405,7 @@ int kq_pages_release(const int* len, const unsigned char* done, int B, int page_
  *             pair, or NULL for axis 0 (an axis >= n_axes does not turn); pos: n_axes rows of T ints
  *   flags     KQ_ROPE_INVERSE turns by the negative angles: the gradient (and inverse) of the call
  *             without it
- * Errors: KQ_ERR_ARG, KQ_ERR_UNSUPPORTED, KQ_ERR_CUDA. */
+ * T <= 2^30. Errors: KQ_ERR_ARG, KQ_ERR_UNSUPPORTED, KQ_ERR_CUDA. */
 enum kq_rope_flags { KQ_ROPE_ADJACENT = 1u, KQ_ROPE_INVERSE = 2u };
 int kq_rope(int x_dtype, int y_dtype, const void* q, long long q_stride, void* q_out, long long q_out_stride, int n_q,
             const void* k, long long k_stride, void* k_out, long long k_out_stride, int n_k, int T, int head_dim,
@@ -438,7 +438,7 @@ size_t kq_kv8_bytes(int n_pages, int page_size, int n_kv, int head_dim);
  * written again). Scales do not shrink: overwriting a token (a rejected guess) keeps the page's.
  * The tokens of one call that go to one page stand next to each other at ascending slots, as
  * kq_pages_plan gives them; slots beyond the pages are skipped and set bit 1 of
- * kq_device_errors(). Errors: KQ_ERR_ARG, KQ_ERR_UNSUPPORTED, KQ_ERR_CUDA. */
+ * kq_device_errors(). T <= 2^30. Errors: KQ_ERR_ARG, KQ_ERR_UNSUPPORTED, KQ_ERR_CUDA. */
 int kq_kv8_append(const kq_kv8_cache* cache, int x_dtype, const void* k, long long k_stride, const void* v,
                   long long v_stride, const int* slot, int T, void* stream);
 

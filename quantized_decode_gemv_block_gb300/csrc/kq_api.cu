@@ -515,6 +515,9 @@ int kq_decode_step_static(const kq_decode_model* model, const void* x, float* lo
 
 // ---- Paged KV cache and rotary positions ----
 
+// Tokens or free pages of a call at most: the kernels' int indexes pass the last one by up to a grid of threads.
+constexpr int kMaxItems = 1 << 30;
+
 static bool dtype_known(int t) { return t == KQ_F32 || t == KQ_BF16; }
 static bool page_size_ok(int p) { return p == 16 || p == 32 || p == 64 || p == 128; }
 
@@ -525,7 +528,7 @@ static int pages_check(int B, int page_size, int max_blocks, int free_capacity, 
   if (!page_size_ok(page_size)) return fail(KQ_ERR_ARG, "page_size must be 16, 32, 64 or 128");
   if (max_blocks < 0 || (long long)max_blocks * page_size > 0x40000000LL)
     return fail(KQ_ERR_ARG, "max_blocks * page_size must be in 0..2^30");
-  if (free_capacity < 0) return fail(KQ_ERR_ARG, "free_capacity must be >= 0");
+  if (free_capacity < 0 || free_capacity > kMaxItems) return fail(KQ_ERR_ARG, "free_capacity must be in 0..2^30");
   if (!n_free || !n_free_out || !status) return fail(KQ_ERR_ARG, "n_free, n_free_out or status is NULL");
   if (n_free == n_free_out) return fail(KQ_ERR_ARG, "n_free and n_free_out must be two words");
   if (B > 0 && (!ctx || (max_blocks > 0 && !table) || (free_capacity > 0 && !free_pages)))
@@ -543,7 +546,7 @@ int kq_pages_plan(const int* ctx_len, const int* new_len, int B, int page_size, 
     const int rc = pages_check(B, page_size, max_blocks, free_capacity, ctx_len, block_table, free_pages, n_free,
                                n_free_out, status);
     if (rc != KQ_OK) return rc;
-    if (T < 0) return fail(KQ_ERR_ARG, "T must be >= 0");
+    if (T < 0 || T > kMaxItems) return fail(KQ_ERR_ARG, "T must be in 0..2^30");
     if (!cu || (B > 0 && !new_len) || (T > 0 && (!pos || !slot))) return fail(KQ_ERR_ARG, "new_len, cu, pos or slot is NULL");
     if (!aligned(new_len, 4) || !aligned(cu, 4) || !aligned(pos, 4) || !aligned(slot, 4))
       return fail(KQ_ERR_ARG, "arrays must be 4-byte aligned");
@@ -582,7 +585,7 @@ int kq_rope(int x_dtype, int y_dtype, const void* q, long long q_stride, void* q
   return guarded([&] {
     if (!dtype_known(x_dtype) || !dtype_known(y_dtype)) return fail(KQ_ERR_UNSUPPORTED, "x_dtype and y_dtype must be KQ_F32 or KQ_BF16");
     if (flags & ~(unsigned)(KQ_ROPE_ADJACENT | KQ_ROPE_INVERSE)) return fail(KQ_ERR_ARG, "unknown flag bits " + std::to_string(flags));
-    if (T < 0 || n_q < 0 || n_k < 0 || n_q > 65536 || n_k > 65536) return fail(KQ_ERR_ARG, "T, n_q or n_k out of range");
+    if (T < 0 || T > kMaxItems || n_q < 0 || n_k < 0 || n_q > 65536 || n_k > 65536) return fail(KQ_ERR_ARG, "T, n_q or n_k out of range");
     if (head_dim < 1 || head_dim > 4096 || rot_dim < 0 || rot_dim > head_dim || rot_dim % 2)
       return fail(KQ_ERR_ARG, "head_dim must be in 1..4096 and rot_dim an even number up to it");
     if (n_axes < 1 || n_axes > 255) return fail(KQ_ERR_ARG, "n_axes must be in 1..255");
@@ -643,7 +646,7 @@ int kq_kv8_append(const kq_kv8_cache* cache, int x_dtype, const void* k, long lo
     const int rc = kv8_check(cache, &c);
     if (rc != KQ_OK) return rc;
     if (!dtype_known(x_dtype)) return fail(KQ_ERR_UNSUPPORTED, "x_dtype must be KQ_F32 or KQ_BF16");
-    if (T < 0) return fail(KQ_ERR_ARG, "T must be >= 0");
+    if (T < 0 || T > kMaxItems) return fail(KQ_ERR_ARG, "T must be in 0..2^30");
     const long long w = (long long)c.n_kv * c.D;
     if (k_stride < w || v_stride < w || k_stride % 8 || v_stride % 8)
       return fail(KQ_ERR_ARG, "k_stride and v_stride must be multiples of 8 that hold a token's heads");

@@ -159,3 +159,14 @@ def test_tensors_in_host_memory_are_refused_where_there_is_a_gpu(kq, monkeypatch
                  lambda: kq.pages_release(i(2), i(2).bool(), i(2, 4), i(9), i(1), i(1), 16, stream=0)):
         with pytest.raises(ValueError, match="must be on the GPU"):
             call()
+
+
+def test_calls_of_more_tokens_than_the_kernels_count(kq):
+    """Above 2^30 an int index that moves by a grid of threads could pass 2^31."""
+    L, big = kq.lib(), (1 << 30) + 1
+    c = cache_c(kq)
+    assert L.kq_pages_plan(FAKE, FAKE, 4, 32, FAKE, 8, FAKE, 100, FAKE, FAKE + 4, FAKE, FAKE, FAKE, big, FAKE, None) == kq.KQ_ERR_ARG
+    assert L.kq_pages_plan(FAKE, FAKE, 4, 32, FAKE, 8, FAKE, big, FAKE, FAKE + 4, FAKE, FAKE, FAKE, 16, FAKE, None) == kq.KQ_ERR_ARG
+    assert L.kq_pages_release(FAKE, FAKE, 4, 32, FAKE, 8, FAKE, big, FAKE, FAKE + 4, FAKE, None) == kq.KQ_ERR_ARG
+    assert L.kq_rope(kq.BF16, kq.BF16, FAKE, 1, FAKE, 1, 1, None, 0, None, 0, 0, big, 1, 0, None, None, None, 1, 0, None) == kq.KQ_ERR_ARG
+    assert L.kq_kv8_append(ctypes.addressof(c), kq.BF16, FAKE, 128, FAKE, 128, FAKE, big, None) == kq.KQ_ERR_ARG
