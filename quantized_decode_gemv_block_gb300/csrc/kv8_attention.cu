@@ -26,8 +26,8 @@
 // With 16 rows in the first form (two blocks of 8) a batch of windows of 32 rows of 64 took 48.7 us
 // in place of 41, and 32 rows at a time 79.
 //
-// Work. The positions of a request are cut into segments of 512 (longer ones from 32768 positions on,
-// at most 64): a function of its own length, so that a row's bits depend on its own request alone. An
+// Work. The positions of a request, from 513 on, are cut into segments of 512, or 256 for one or two kv heads
+// (longer ones where 64 do not suffice): a function of its own length, so that a row's bits depend on its own request alone. An
 // item is (request, block of rows, segment, kv head). A persistent grid walks the items; each CTA finds
 // them in prefix sums that it forms itself from the lengths on the device, so the host plans nothing and
 // the call can be captured. In a CTA four warps multiply and a fifth copies: it reads page ids and
@@ -35,18 +35,24 @@
 // bulk copies of whole pages, across items. Each of the four takes 32 positions of a step through both
 // products alone, and they meet in shared memory once per item. A request of one segment writes its
 // output there; others write partials that a second kernel joins.
-//   Windows of more than 32 tokens (prompts) run in a launch of their own, where max_new allows them: blocks of
-// 64 rows, 16 for each warp, which takes its rows over all positions and writes them alone. Contexts from 4096
-// positions on with fewer than 32 blocks per kv head are cut until there are about 32 items (one request over
-// 131k positions, 32 / 8 heads of 128: 395 us for 32 tokens, 611 for 33, 757 for 64). In the windows' form 2 x
-// 2048 tokens took 437 us in place of 368, 38 requests of 155 to 311 tokens (fp32, 16 / 8 heads) 221 in place
-// of 163. Codes converted once for all warps into shared memory: with 8 warps and 128 rows 374 and 198 us, with
-// 4 warps 393 and 198 us; the barriers cost more than the conversions.
-// Measured on the way: a CTA of four warps with nothing copied ahead across items 168 us on the decoding
-// batch below; warps that share the second product by dims, with a barrier per step, 177 us; each warp with
-// items and a ring of its own 112 to 132 us (its copies' and its items' bookkeeping weighed as much as its
-// products); the fifth warp 100 us. Segments of 256 positions 115 us and of 1024 100 us; one token
-// over 4096 positions 9.6, 10.4 and 14.4 us with segments of 256, 512 and 1024.
+//   Windows of more than 32 tokens (prompts) run in a launch of their own, where max_new allows them: blocks of 64
+// rows, 16 for each warp, which takes its rows over all positions and writes them alone. Over contexts from 4096
+// positions on a request is cut so that it alone gives every CTA one item, or two where that comes out more even.
+// One request over 131k positions, 32 / 8 heads of 128: 395 us for 32 tokens, 511 for 33, 648 for 64, 2388 for 200
+// (616, 761 and 3012 with 32 items per kv head, 530, 678 and 2421 with 76, each rounded up to 512 positions); 4 / 1
+// heads: 79 us for 33. What it costs: 16 requests of 64 tokens over 6000 positions, which fill the machine
+// together, 614 us in place of 566. In the windows' form 2 x 2048 tokens took 437 us in place of 368, 38 requests
+// of 155 to 311 tokens (fp32, 16 / 8 heads) 221 in place of 163. Codes converted once for all warps into shared
+// memory: with 8 warps and 128 rows 374 and 198 us, with 4 warps 393 and 198 us; the barriers cost more than the
+// conversions.
+// Measured on the way: a CTA of four warps with nothing copied ahead across items 168 us on the decoding batch below;
+// warps that share the second product by dims, with a barrier per step, 177 us; each warp with items and a ring of
+// its own 112 to 132 us (its copies' and its items' bookkeeping weighed as much as its products); the fifth warp 100
+// us. Segments of 256 positions 115 us and of 1024 100 us; one token over 4096 positions 9.6, 10.4 and 14.4 us with
+// segments of 256, 512 and 1024. Few heads leave CTAs idle, so that short segments win: one token over 4096
+// positions, 16 / 2 heads, 9.5 us with segments of 256 and 11.4 with 512; 63 tokens over 1030 to 2060, 2 / 1 heads of
+// 64, 15.6 and 19.9; the other side, 64 tokens over 1 to 8191, 8 / 2 heads, 37.4 and 35.4, and with four heads 62 and
+// 57.
 //
 // Bound by DRAM for single tokens: 64 requests of 1 to 8191 positions, 32 / 8 heads of 128, 543 MB in
 // 99.6 us, 5.45 TB/s, of which 5 us are the join and about 10 the start and the end; four contexts of 128k
@@ -72,16 +78,55 @@ namespace {
 constexpr int kWarps = 4;                          // warps that multiply; one more brings the codes
 constexpr int kMath = 32 * kWarps, kThreads = kMath + 32;
 constexpr int kWarpPos = 32, kStep = kWarps * kWarpPos;  // positions of a step, 32 per warp
-constexpr int kMinSegment = 512, kMaxSegments = 64;      // positions of a segment at least, segments of a request at most
+constexpr int kSegLog2 = 9, kFewSegLog2 = 8;             // positions of a segment at least; for few kv heads
+constexpr int kMaxSegments = 64;                         // segments of a request at most
 constexpr int kWindow = 32 * 16 / kStep;                 // steps whose page ids are read at once, a group of 16 tokens per lane
 constexpr int kSplitTokens = 32;                         // windows up to this many tokens are cut as above
 constexpr int kPromptRows = 64;                          // query rows of an item of larger windows (prompts)
-constexpr int kLongContext = 4096, kItems = 32;          // prompts over at least so many positions: cut into about so many items
+constexpr int kFewHeads = 2;                             // kv heads that are few
+constexpr int kLongContext = 4096, kShortest = 512;      // prompts over at least so many positions are cut; into at least so many
+constexpr int kWaves = 2;                                // items per CTA that a prompt alone is cut into at most
 constexpr float kLowest = -3e38f;  // below every finite score in use: keeps -inf out of differences
 constexpr uint64_t kWaitNs = 2000000000ull;
 constexpr int kCombThreads = 256;
 
 __device__ unsigned int g_kv8_errors = 0;  // bit 0: a bounded wait gave up; bit 1: bad lengths or page ids
+
+// How a request's positions are cut: a function of its own lengths and the heads.
+struct Cut {
+  int len, count;  // positions of a segment (a multiple of a step), segments
+};
+struct Cutter {
+  int group, n_kv, seg_log2, wave;  // query heads per kv head; kv heads; windows' shortest segments; prompts' CTAs at once
+  __host__ __device__ Cut operator()(int len, int n) const {
+    if (n <= kSplitTokens) {  // segments doubled until kMaxSegments hold the request
+      static_assert(kMaxSegments == 64, "a power of two");
+      if (len <= 1 << kSegLog2) return {1 << kSegLog2, 1};  // nothing to join
+      int log2 = seg_log2;
+      const int over = (len - 1) >> (seg_log2 + 6);
+#ifdef __CUDA_ARCH__
+      log2 += 32 - __clz(over);
+#else
+      for (int v = over; v > 0; v >>= 1) ++log2;
+#endif
+      return {1 << log2, (len + (1 << log2) - 1) >> log2};
+    }
+    // as many segments as give all CTAs one item, or two where that shares the work out better by 5 %
+    const Cut whole = {1 << 29, 1};
+    const int blocks = (n * group + kPromptRows - 1) / kPromptRows;
+    if (len < kLongContext || blocks >= kWaves * wave) return whole;
+    const int items = blocks * n_kv, two = kWaves * wave / items;
+    int count = wave / items;
+    if (20 * two > 21 * kWaves * count) count = two;
+    count = count < len / kShortest ? count : len / kShortest;
+    if (count <= 1) return whole;
+    const int size = ((len + count - 1) / count + kStep - 1) / kStep * kStep;
+    return {size, (len + size - 1) / size};
+  }
+};
+Cutter cutter_of(int n_kv, int group, int D) {
+  return {group, n_kv, n_kv <= kFewHeads ? kFewSegLog2 : kSegLog2, 152 * (D == 64 ? 3 : 2)};
+}
 
 struct AttnKV8Params {
   const void* q;
@@ -96,34 +141,13 @@ struct AttnKV8Params {
   const int *ctx, *fresh;
   const uint32_t* mask;
   int B, T, max_new, max_len, n_pages, log2p, n_kv, group;
+  Cutter cut;
   unsigned group_inv;  // 2^32 / group rounded up; 0 for a group of one
   float scale_log2e;
   float* part;          // a request's partial rows: [kv head][segment][row][D]
   float2* part_ml;      // [kv head][segment][row]: reference, sum of weights
   long long part_rows;  // room per kv head
 };
-
-// How a request's positions are cut: a function of its own lengths.
-struct Cut {
-  int len, count;  // positions of a segment (a multiple of a step), segments
-};
-__host__ __device__ inline Cut cut_of(int len, int n, int group) {
-  if (n <= kSplitTokens) {  // segments doubled until kMaxSegments hold the request
-    constexpr int kBase = kMinSegment * kMaxSegments;
-    static_assert((kBase & (kBase - 1)) == 0 && kMinSegment == 1 << 9, "powers of two");
-    int log2 = 9;
-#ifdef __CUDA_ARCH__
-    log2 += 32 - __clz((len - 1) / kBase);
-#else
-    for (int over = (len - 1) / kBase; over > 0; over >>= 1) ++log2;
-#endif
-    return {1 << log2, (len + (1 << log2) - 1) >> log2};
-  }
-  const int blocks = (n * group + kPromptRows - 1) / kPromptRows;
-  if (len < kLongContext || blocks >= kItems) return {1 << 29, 1};
-  const int want = kItems / blocks, size = ((len + want - 1) / want + kMinSegment - 1) / kMinSegment * kMinSegment;
-  return {size, (len + size - 1) / size};
-}
 
 // Warps that share a row of the combine: 8 segments each, and up to 8 warps.
 __host__ __device__ constexpr int combine_warps(int nseg) { return nseg <= 8 ? 1 : nseg <= 16 ? 2 : nseg <= 32 ? 4 : 8; }
@@ -159,7 +183,7 @@ __device__ __forceinline__ void scan_requests(const AttnKV8Params& p, int row_bl
     a += n > 0 ? n : 0;
     if (!request_ok(p, ctx, n)) bad = true;
     else if (n > 0) {
-      const int nseg = cut_of(ctx + n, n, p.group).count, rows = n * p.group;
+      const int nseg = p.cut(ctx + n, n).count, rows = n * p.group;
       if (KIND != kCombine) b += (n <= kSplitTokens) == (KIND == kWindows) ? (rows + row_block - 1) / row_block * nseg : 0;
       else b += nseg <= 1 ? 0 : (rows * p.n_kv * combine_warps(nseg) + W - 1) / W;
       c += nseg > 1 ? (long long)nseg * rows : 0;
@@ -344,7 +368,7 @@ __global__ void __launch_bounds__(kThreads, FORM == kRows8 ? (D == 64 ? 4 : 3) :
     const int n = req[x.r + 1].tok - q.tok;
     x.len = q.ctx + n;
     x.rows = n * p.group;
-    const Cut cut = cut_of(x.len, n, p.group);
+    const Cut cut = p.cut(x.len, n);
     x.nseg = cut.count;
     int local = at.item - q.item, rb = 0;
     if (local >= x.nseg) {
@@ -356,7 +380,7 @@ __global__ void __launch_bounds__(kThreads, FORM == kRows8 ? (D == 64 ? 4 : 3) :
     x.end = p.mask || n == 1 ? x.len : x.ctx + token_of(p, min(x.row0 + RB, x.rows) - 1) + 1;
     x.seen = x.ctx + (p.mask ? 0 : token_of(p, x.row0) + 1);
     const int last = (x.end + kStep - 1) / kStep;
-    static_assert(kMinSegment % kStep == 0, "segments are cut into steps");
+    static_assert((1 << kFewSegLog2) % kStep == 0 && kFewSegLog2 <= kSegLog2, "segments are cut into steps");
     x.step0 = x.seg * (cut.len / kStep);
     x.step1 = min(x.step0 + cut.len / kStep, last);
     return x;
@@ -878,7 +902,7 @@ __global__ void __launch_bounds__(kCombThreads) attn_kv8_combine_kernel(const At
   const int n_q = p.n_kv * p.group, total = req[p.B].item;
   for (int it = blockIdx.x; it < total; it += gridDim.x) {
     const int r = find_request(req, p.B, it), local = it - req[r].item, tok0 = req[r].tok;
-    const int n = req[r + 1].tok - tok0, nseg = cut_of(req[r].ctx + n, n, p.group).count;
+    const int n = req[r + 1].tok - tok0, nseg = p.cut(req[r].ctx + n, n).count;
     if (req[r].part + (long long)nseg * n * p.group > p.part_rows) continue;
     const int k = combine_warps(nseg), sub = w & (k - 1);
     const int task = (local * W + w) / k;  // (token, query head) of the request
@@ -983,10 +1007,10 @@ int launch_all(const AttnKV8Params& p, int num_sms, cudaStream_t s, std::string*
   const bool rows8 = (long long)p.max_new * p.group <= 8;
   if ((rows8 ? launch_form<D, kRows8, WIDE>(p, num_sms, s, err) : launch_form<D, kRows16, WIDE>(p, num_sms, s, err)) != 0) return -1;
   if (p.max_new > kSplitTokens && launch_form<D, kPrompt, WIDE>(p, num_sms, s, err) != 0) return -1;
-  if (p.max_len <= kMinSegment) return 0;  // no request can have two segments
+  if (p.max_len <= 1 << kSegLog2) return 0;  // no request can have two segments
   const long long tasks = (long long)p.T * p.n_kv * p.group;
   // no more CTAs than the longest request's rows would need: each forms the prefix sums
-  const long long want = (tasks * combine_warps(cut_of(p.max_len, 1, 1).count) + kCombThreads / 32 - 1) / (kCombThreads / 32);
+  const long long want = (tasks * combine_warps(p.cut(p.max_len, 1).count) + kCombThreads / 32 - 1) / (kCombThreads / 32);
   const int grid = (int)(want < (long long)num_sms * 8 ? want : (long long)num_sms * 8);
   return launch_pdl(attn_kv8_combine_kernel<D>, dim3(grid), dim3(kCombThreads), (size_t)(p.B + 1) * sizeof(Request), s, p,
                     "attention_kv8 combine", err);
@@ -998,11 +1022,15 @@ int launch_dim(const AttnKV8Params& p, int num_sms, cudaStream_t s, std::string*
 }
 
 // Partial rows at most: windows of up to 32 tokens have len / 512 + 1 segments, larger ones segments x rows
-// <= 32 blocks of 64, where their context is long.
-size_t part_rows(int B, long long total_len, int max_new, int group) {
-  const size_t small = (size_t)group * (max_new < kSplitTokens ? max_new : kSplitTokens) * ((size_t)(total_len / kMinSegment) + B);
+// <= items of 64 rows, where their context is long.
+size_t part_rows(const Cutter& cut, int B, long long total_len, int max_new) {
+  const int window = max_new < kSplitTokens ? max_new : kSplitTokens;
+  const size_t rows = (size_t)cut.group * window * ((size_t)(total_len >> cut.seg_log2) + B);
+  if (max_new <= kSplitTokens) return rows;
   const long long many = total_len / kLongContext < B ? total_len / kLongContext : B;
-  return small + (max_new > kSplitTokens ? (size_t)many * kItems * kPromptRows : 0);
+  const size_t by_items = (size_t)many * (kWaves * cut.wave / cut.n_kv) * kPromptRows;
+  const size_t by_length = (size_t)(total_len / kShortest) * cut.group * max_new;
+  return rows + (by_items < by_length ? by_items : by_length);
 }
 
 }  // namespace
@@ -1015,7 +1043,7 @@ unsigned int take_kv8_errors() {
 }
 
 size_t attention_kv8_workspace(int B, long long total_len, int max_new, int n_q, int n_kv, int D) {
-  return part_rows(B, total_len, max_new, n_q / n_kv) * n_kv * (D + 2) * sizeof(float);
+  return part_rows(cutter_of(n_kv, n_q / n_kv, D), B, total_len, max_new) * n_kv * (D + 2) * sizeof(float);
 }
 
 int launch_attention_kv8(const KV8Args& c, const AttnKV8Args& a, int num_sms, cudaStream_t s, std::string* err) {
@@ -1043,9 +1071,10 @@ int launch_attention_kv8(const KV8Args& c, const AttnKV8Args& a, int num_sms, cu
   p.log2p = c.log2p;
   p.n_kv = c.n_kv;
   p.group = a.n_q / c.n_kv;
+  p.cut = cutter_of(c.n_kv, p.group, c.D);
   p.group_inv = p.group == 1 ? 0u : (unsigned)(((1ull << 32) + p.group - 1) / p.group);
   p.scale_log2e = a.scale * 1.4426950408889634f;
-  p.part_rows = (long long)part_rows(a.B, a.total_len, a.max_new, p.group);
+  p.part_rows = (long long)part_rows(p.cut, a.B, a.total_len, a.max_new);
   p.part = static_cast<float*>(a.ws);
   p.part_ml = reinterpret_cast<float2*>(p.part + (size_t)p.part_rows * c.n_kv * c.D);
   return c.D == 64 ? launch_dim<64>(p, num_sms, s, err) : launch_dim<128>(p, num_sms, s, err);

@@ -457,3 +457,17 @@ def test_memory_of_calls_on_a_given_stream(handle, monkeypatch):
     check(o, q, parts, table, ctx, new, P, n_kv, D ** -0.5)
     assert plan.pos.tolist() == [1300, 50] and plan.status.item() == 0
     assert torch.equal(turned, q)
+
+
+@pytest.mark.parametrize("x,y", [("bf16", "bf16"), ("f32", "f32")])
+@pytest.mark.parametrize("D", [64, 128])
+def test_few_heads_are_cut_finer(x, y, D):
+    """Segments of 256 positions up to 16384, twice as long beyond; more than 64 segments for windows of over 32 tokens."""
+    attn_case([(255, 1), (256, 1), (511, 2), (513, 5), (16383, 1), (16384, 2), (16640, 20)], 16, D, 4, 2, x, y)
+    attn_case([(40000, 40), (5, 2), (4063, 33), (4062, 33), (9000, 100)], 128, D, 2, 1, x, y)
+
+
+def test_segments_of_a_prompt_end_inside_pages_and_windows_of_page_ids():
+    """Lengths whose shares are odd multiples of 128 positions."""
+    attn_case([(4100, 33), (6700, 47), (7300, 64), (11111, 130)], 64, 64, 6, 3, "bf16", "f32")
+    attn_case([(5003, 60), (8200, 35)], 32, 128, 24, 12, "bf16", "bf16")
