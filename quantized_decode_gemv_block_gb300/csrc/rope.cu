@@ -12,11 +12,14 @@
 // quarter turn and a rest in [-1/8, 1/8] turn, whose sine and cosine come from sincospif.
 //
 // Bound by DRAM: q and k are read and written once. A CTA forms the angles of its tokens once, in
-// shared memory, and turns eight pairs per thread and turn (16-byte accesses for bf16) of all of its
+// shared memory, and turns up to eight pairs per thread and turn (16-byte accesses for bf16) of all of its
 // heads. A prompt of 32768 tokens, 32 + 8 heads of 128 in bf16, takes 110 us, 6.1 TB/s read and written
 // (115 us with five CTAs per SM, 123 with eight, whose registers spill). With the angles formed by each
 // thread for eight heads, in registers, it took 116.5 us, and 1999 tokens of 20 heads of 64, which leave a
 // thread one head, 8.8 us in place of 4.5.
+//   Heads or halves that do not divide into 16-byte parts take 4 or 2 pairs at a time: 8192 tokens of 64 heads
+// of 80, bf16, 20 dims turned, 59 us by twos and 90 by ones (25 us of DRAM traffic); 4203 tokens of 18 heads of 96,
+// 24 dims turned, 11.1 us by fours, 14.8 by twos, 20.3 by ones.
 #include <cuda_bf16.h>
 
 #include <cstdint>
@@ -93,6 +96,10 @@ __device__ __forceinline__ void load(float (&v)[V], const float* p) {
       v[4 * i + 2] = x.z;
       v[4 * i + 3] = x.w;
     }
+  } else if (V == 2) {
+    const float2 x = *reinterpret_cast<const float2*>(p);
+    v[0] = x.x;
+    v[V - 1] = x.y;
   } else {
 #pragma unroll
     for (int i = 0; i < V; ++i) v[i] = p[i];
@@ -111,6 +118,20 @@ __device__ __forceinline__ void load(float (&v)[V], const uint16_t* p) {
         v[8 * i + 2 * j + 1] = __uint_as_float(w[j] & 0xFFFF0000u);
       }
     }
+  } else if (V % 2 == 0) {
+    uint32_t w[2];
+    if (V == 4) {
+      const uint2 x = __ldcs(reinterpret_cast<const uint2*>(p));
+      w[0] = x.x;
+      w[1] = x.y;
+    } else {
+      w[0] = __ldcs(reinterpret_cast<const uint32_t*>(p));
+    }
+#pragma unroll
+    for (int j = 0; j < V / 2; ++j) {
+      v[2 * j] = __uint_as_float(w[j % 2] << 16);
+      v[(2 * j + 1) % V] = __uint_as_float(w[j % 2] & 0xFFFF0000u);
+    }
   } else {
 #pragma unroll
     for (int i = 0; i < V; ++i) v[i] = __uint_as_float((uint32_t)p[i] << 16);
@@ -122,6 +143,8 @@ __device__ __forceinline__ void store(float* p, const float (&v)[V]) {
 #pragma unroll
     for (int i = 0; i < V / 4; ++i)
       reinterpret_cast<float4*>(p)[i] = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+  } else if (V == 2) {
+    *reinterpret_cast<float2*>(p) = make_float2(v[0], v[V - 1]);
   } else {
 #pragma unroll
     for (int i = 0; i < V; ++i) p[i] = v[i];
@@ -138,13 +161,17 @@ __device__ __forceinline__ void store(uint16_t* p, const float (&v)[V]) {
         w[j] = f32x2_to_bf16x2(v[8 * i + 2 * j], v[8 * i + 2 * j + 1]);
       reinterpret_cast<uint4*>(p)[i] = make_uint4(w[0], w[1], w[2], w[3]);
     }
+  } else if (V == 4) {
+    *reinterpret_cast<uint2*>(p) = make_uint2(f32x2_to_bf16x2(v[0], v[1 % V]), f32x2_to_bf16x2(v[2 % V], v[3 % V]));
+  } else if (V == 2) {
+    *reinterpret_cast<uint32_t*>(p) = f32x2_to_bf16x2(v[0], v[V - 1]);
   } else {
 #pragma unroll
     for (int i = 0; i < V; ++i) p[i] = f32_to_bf16_rn(v[i]);
   }
 }
 
-// V pairs per thread and turn: 8 where every row, head and half starts on 16 bytes, else 1.
+// V pairs per thread and turn: 8, 4 or 2 where every row, head and half starts on as many elements, else 1.
 template <typename X, typename Y, int V, bool ADJ>
 __global__ void __launch_bounds__(kThreads, sizeof(X) == 2 ? 6 : 5) rope_kernel(const RopeParams p) {
   __shared__ __align__(16) float sm_c[kTable], sm_s[kTable];  // [token][pair]
@@ -217,25 +244,33 @@ __global__ void __launch_bounds__(kThreads, sizeof(X) == 2 ? 6 : 5) rope_kernel(
 }
 
 template <typename X, typename Y>
-int launch_typed(const RopeParams& p, bool vec, bool adj, dim3 g, cudaStream_t s, std::string* err) {
+int launch_typed(const RopeParams& p, int V, bool adj, dim3 g, cudaStream_t s, std::string* err) {
   const dim3 b(kThreads);
-  if (vec) return adj ? launch_pdl(rope_kernel<X, Y, 8, true>, g, b, 0, s, p, "rope", err)
-                      : launch_pdl(rope_kernel<X, Y, 8, false>, g, b, 0, s, p, "rope", err);
+  if (V == 8) return adj ? launch_pdl(rope_kernel<X, Y, 8, true>, g, b, 0, s, p, "rope", err)
+                         : launch_pdl(rope_kernel<X, Y, 8, false>, g, b, 0, s, p, "rope", err);
+  if (V == 4) return adj ? launch_pdl(rope_kernel<X, Y, 4, true>, g, b, 0, s, p, "rope", err)
+                         : launch_pdl(rope_kernel<X, Y, 4, false>, g, b, 0, s, p, "rope", err);
+  if (V == 2) return adj ? launch_pdl(rope_kernel<X, Y, 2, true>, g, b, 0, s, p, "rope", err)
+                         : launch_pdl(rope_kernel<X, Y, 2, false>, g, b, 0, s, p, "rope", err);
   return adj ? launch_pdl(rope_kernel<X, Y, 1, true>, g, b, 0, s, p, "rope", err)
              : launch_pdl(rope_kernel<X, Y, 1, false>, g, b, 0, s, p, "rope", err);
 }
 
-bool on16(const void* p, long long stride, int elem) {
-  return reinterpret_cast<uintptr_t>(p) % 16 == 0 && stride * elem % 16 == 0;
+bool starts_on(int bytes, const void* p, long long stride, int elem) {
+  return reinterpret_cast<uintptr_t>(p) % bytes == 0 && stride * elem % bytes == 0;
 }
 
 }  // namespace
 
 int launch_rope(const RopeArgs& a, int num_sms, cudaStream_t s, std::string* err) {
   const int xe = a.x_dtype == KQ_F32 ? 4 : 2, ye = a.y_dtype == KQ_F32 ? 4 : 2;
-  const bool vec = a.D % 16 == 0 && a.rot_dim % 16 == 0 && on16(a.x0, a.xs0, xe) && on16(a.x1, a.xs1, xe) &&
-                   on16(a.y0, a.ys0, ye) && on16(a.y1, a.ys1, ye);
-  const int V = vec ? 8 : 1;
+  // rows, heads and halves of heads start on V elements, or on 16 bytes
+  auto fits_v = [&](int v) {
+    auto on = [&](const void* x, long long stride, int e) { return starts_on(e * v < 16 ? e * v : 16, x, stride, e); };
+    return a.D % (2 * v) == 0 && a.rot_dim % (2 * v) == 0 && on(a.x0, a.xs0, xe) && on(a.x1, a.xs1, xe) &&
+           on(a.y0, a.ys0, ye) && on(a.y1, a.ys1, ye);
+  };
+  const int V = fits_v(8) ? 8 : fits_v(4) ? 4 : fits_v(2) ? 2 : 1;
   RopeParams p = {a.x0, a.x1, a.y0, a.y1, a.xs0, a.xs1, a.ys0, a.ys1, a.h0, a.h1, a.T, a.D, a.rot_dim / 2,
                   a.freq, a.axis, a.pos, a.n_axes, a.inverse ? 1 : 0, 0, 0};
   p.chunks = p.pairs / V + (a.D - a.rot_dim + 2 * V - 1) / (2 * V);
@@ -259,10 +294,10 @@ int launch_rope(const RopeArgs& a, int num_sms, cudaStream_t s, std::string* err
     return -1;
   }
   if (a.x_dtype == KQ_F32)
-    return a.y_dtype == KQ_F32 ? launch_typed<float, float>(p, vec, a.adjacent, g, s, err)
-                               : launch_typed<float, uint16_t>(p, vec, a.adjacent, g, s, err);
-  return a.y_dtype == KQ_F32 ? launch_typed<uint16_t, float>(p, vec, a.adjacent, g, s, err)
-                             : launch_typed<uint16_t, uint16_t>(p, vec, a.adjacent, g, s, err);
+    return a.y_dtype == KQ_F32 ? launch_typed<float, float>(p, V, a.adjacent, g, s, err)
+                               : launch_typed<float, uint16_t>(p, V, a.adjacent, g, s, err);
+  return a.y_dtype == KQ_F32 ? launch_typed<uint16_t, float>(p, V, a.adjacent, g, s, err)
+                             : launch_typed<uint16_t, uint16_t>(p, V, a.adjacent, g, s, err);
 }
 
 }  // namespace kq

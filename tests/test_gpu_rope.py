@@ -88,6 +88,15 @@ def test_rows_that_start_off_16_bytes():
     check(o, *plain(q, pos, freqs(32), np.zeros(32, int), False, False), "off 16 bytes")
 
 
+@pytest.mark.parametrize("x,y", [("f32", "f32"), ("bf16", "bf16"), ("f32", "bf16"), ("bf16", "f32")])
+@pytest.mark.parametrize("adjacent", [False, True])
+@pytest.mark.parametrize("T,nq,nk,D,rot,view", [(40, 3, 1, 64, 64, 2), (700, 6, 2, 80, 20, 0), (65, 2, 2, 96, 24, 6), (9, 1, 1, 12, 8, 0),
+                                                (5, 2, 1, 132, 132, 0), (300, 3, 2, 80, 40, 0), (40, 3, 1, 64, 64, 4),
+                                                (21, 1, 2, 72, 72, 12), (4, 1, 1, 88, 0, 0)])
+def test_rows_and_halves_that_start_on_two_or_four_elements(x, y, adjacent, T, nq, nk, D, rot, view):
+    case(T, nq, nk, D, rot, 2, x, y, adjacent, True, view=view)
+
+
 @pytest.mark.parametrize("far", [2 ** 24, 2 ** 31 - 1])
 def test_far_positions(far):
     case(40, 2, 1, 64, 64, 2, "f32", "f32", False, False, far=far)
