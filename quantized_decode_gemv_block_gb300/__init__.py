@@ -350,8 +350,8 @@ class PagesPlan:
     __slots__ = ("cu", "pos", "slot", "n_free", "status")
 
     def __init__(self, B: int, T: int, device="cuda", stream=None):
-        buf = _empty(B + 1 + 2 * T + 2, torch.int32, device, stream)
-        self.cu, self.pos, self.slot, self.n_free, self.status = buf.split_with_sizes((B + 1, T, T, 1, 1))
+        self.cu, self.pos, self.slot, self.n_free, self.status = (
+            _empty(n, torch.int32, device, stream) for n in (B + 1, T, T, 1, 1))
 
 
 def pages_plan(ctx_len: torch.Tensor, new_len: torch.Tensor, block_table: torch.Tensor, free_pages: torch.Tensor,
@@ -361,9 +361,8 @@ def pages_plan(ctx_len: torch.Tensor, new_len: torch.Tensor, block_table: torch.
     B, width = block_table.shape
     if out is None:
         out = PagesPlan(B, T, block_table.device, stream)
-        base = out.cu.data_ptr()
-        outs = (base + 4 * (B + 1 + 2 * T), base, base + 4 * (B + 1), base + 4 * (B + 1 + T))
-        status = base + 4 * (B + 2 + 2 * T)
+        outs = (out.n_free.data_ptr(), out.cu.data_ptr(), out.pos.data_ptr(), out.slot.data_ptr())
+        status = out.status.data_ptr()
     else:
         outs = (_i32("out.n_free", out.n_free, 1), _i32("out.cu", out.cu, B + 1), _i32("out.pos", out.pos, T),
                 _i32("out.slot", out.slot, T))
@@ -403,6 +402,8 @@ def rope(q: torch.Tensor | None, k: torch.Tensor | None, pos: torch.Tensor, inv_
         raise ValueError("one of q and k is needed")
     T, D = ref.shape[0], ref.shape[2]
     axes = pos.shape[0] if pos.dim() == 2 else 1
+    if axes > 1 and pos.shape[1] != T:
+        raise ValueError("pos of several axes must be (axes, tokens)")
     pairs = inv_freq.numel()
     if pairs and (inv_freq.dtype != torch.float32 or not inv_freq.is_contiguous()):
         raise ValueError("inv_freq must be contiguous fp32")

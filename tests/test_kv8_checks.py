@@ -170,3 +170,9 @@ def test_calls_of_more_tokens_than_the_kernels_count(kq):
     assert L.kq_pages_release(FAKE, FAKE, 4, 32, FAKE, 8, FAKE, big, FAKE, FAKE + 4, FAKE, None) == kq.KQ_ERR_ARG
     assert L.kq_rope(kq.BF16, kq.BF16, FAKE, 1, FAKE, 1, 1, None, 0, None, 0, 0, big, 1, 0, None, None, None, 1, 0, None) == kq.KQ_ERR_ARG
     assert L.kq_kv8_append(ctypes.addressof(c), kq.BF16, FAKE, 128, FAKE, 128, FAKE, big, None) == kq.KQ_ERR_ARG
+
+
+def test_rope_positions_of_several_axes_have_a_row_of_tokens_each(kq):
+    x = torch.zeros((3, 2, 64), dtype=torch.bfloat16)
+    with pytest.raises(ValueError, match="axes, tokens"):
+        kq.rope(x, None, torch.zeros((2, 4), dtype=torch.int32), torch.zeros(32), stream=0)
