@@ -397,46 +397,57 @@ def rope(q: torch.Tensor | None, k: torch.Tensor | None, pos: torch.Tensor, inv_
     """Rotary positions on q and k (T, heads, head_dim; either may be None), through kq_rope. pos: int32 [T]
     or [axes, T]; inv_freq: fp32, one per pair (rot_dim = 2 * its length); pair_axis: uint8, one per pair.
     inverse=True is the gradient of the call without it. Returns (q_out, k_out)."""
-    ref = q if q is not None else k
+    ref = k if q is None else q
     if ref is None:
         raise ValueError("one of q and k is needed")
-    T, D = ref.shape[0], ref.shape[2]
+    T, _, D = ref.shape
+    dtype = ref.dtype
     axes = pos.shape[0] if pos.dim() == 2 else 1
     if axes > 1 and pos.shape[1] != T:
         raise ValueError("pos of several axes must be (axes, tokens)")
     pairs = inv_freq.numel()
-    if pairs and (inv_freq.dtype != torch.float32 or not inv_freq.is_contiguous()):
+    if pairs and (inv_freq.dtype is not torch.float32 or not inv_freq.is_contiguous()):
         raise ValueError("inv_freq must be contiguous fp32")
-    if pair_axis is not None and (pair_axis.dtype != torch.uint8 or not pair_axis.is_contiguous() or pair_axis.numel() != pairs):
-        raise ValueError("pair_axis must be contiguous uint8, one per pair")
-    if not inv_freq.is_cuda or (pair_axis is not None and not pair_axis.is_cuda):
-        _not_on_gpu("inv_freq and pair_axis")
+    if not inv_freq.is_cuda:
+        _not_on_gpu("inv_freq")
+    axis = None
+    if pair_axis is not None:
+        if pair_axis.dtype is not torch.uint8 or not pair_axis.is_contiguous() or pair_axis.numel() != pairs:
+            raise ValueError("pair_axis must be contiguous uint8, one per pair")
+        if not pair_axis.is_cuda:
+            _not_on_gpu("pair_axis")
+        axis = pair_axis.data_ptr()
     y_dtype = out_dtype or (q_out if q_out is not None else k_out if k_out is not None else ref).dtype
-    none = (None, 0, None, 0, 0)
-    qa = ka = none
+    qp = qs = qop = qos = kp = ks = kop = kos = n_q = n_k = 0
     if q is not None:
-        q_out, qa = _rope_side("q", q, q_out, ref, y_dtype, stream)
+        qs = _heads("q", q, None, D)
+        n_q, qp = q.shape[1], q.data_ptr()
+        if q_out is None:
+            q_out, qos = _empty(q.shape, y_dtype, q.device, stream), n_q * D
+        else:
+            qos = _rope_out("q", q, q_out, y_dtype)
+        qop = q_out.data_ptr()
     if k is not None:
-        k_out, ka = _rope_side("k", k, k_out, ref, y_dtype, stream)
+        if k.dtype is not dtype or k.shape[0] != T:
+            raise ValueError("q and k must agree in type and tokens")
+        ks = _heads("k", k, None, D)
+        n_k, kp = k.shape[1], k.data_ptr()
+        if k_out is None:
+            k_out, kos = _empty(k.shape, y_dtype, k.device, stream), n_k * D
+        else:
+            kos = _rope_out("k", k, k_out, y_dtype)
+        kop = k_out.data_ptr()
     flags = (KQ_ROPE_ADJACENT if adjacent else 0) | (KQ_ROPE_INVERSE if inverse else 0)
-    _check(lib().kq_rope(_dtype(ref.dtype), _dtype(y_dtype), *qa, *ka, T, D, 2 * pairs, inv_freq.data_ptr(),
-                         pair_axis.data_ptr() if pair_axis is not None else None, _i32("pos", pos, axes * T), axes,
-                         flags, _stream(stream)))
+    _check(lib().kq_rope(_dtype(dtype), _dtype(y_dtype), qp, qs, qop, qos, n_q, kp, ks, kop, kos, n_k, T, D, 2 * pairs,
+                         inv_freq.data_ptr(), axis, _i32("pos", pos, axes * T), axes, flags, _stream(stream)))
     return q_out if q is not None else None, k_out if k is not None else None
 
 
-def _rope_side(name, x, y, ref, y_dtype, stream):
-    """The output of one of rope's tensors, and its five arguments."""
-    if x is not ref and (x.dtype is not ref.dtype or x.shape[0] != ref.shape[0] or x.shape[2] != ref.shape[2]):
-        raise ValueError("q and k must agree in type, tokens and head_dim")
-    xs = _heads(name, x)
-    H, D = x.shape[1], x.shape[2]
-    if y is None:
-        y = _empty(x.shape, y_dtype, x.device, stream)
-        return y, (x.data_ptr(), xs, y.data_ptr(), H * D, H)
+def _rope_out(name, x, y, y_dtype) -> int:
+    """The token stride of a given output."""
     if y.shape != x.shape or y.dtype is not y_dtype:
         raise ValueError(f"{name}_out must have {name}'s shape, and both outputs one type")
-    return y, (x.data_ptr(), xs, y.data_ptr(), _heads(name + "_out", y), H)
+    return _heads(name + "_out", y)
 
 
 class KV8CacheC(ctypes.Structure):
