@@ -456,10 +456,8 @@ int kq_kv8_append(const kq_kv8_cache* cache, int x_dtype, const void* k, long lo
  *              kq_device_errors(), as do page ids outside the cache (those rows come out NaN)
  * Sums and softmax statistics are fp32; codes enter the tensor cores exactly. With fp32 output q
  * and the weights are carried in 22 bits; with bf16 output in fp16 (11 bits). A row's bits depend
- * on its own request alone: not on the other requests, nor, in windows of up to 32 tokens, on how many
- * tokens follow it, unless they take the request past a length at which it is cut or joined otherwise
- * (4096 and its multiples by powers of two; with one or two kv heads 512 and those from 2048 on). For the
- * same pages: appending a token may coarsen its page's codes.
+ * on its own request alone: not on the other requests, nor, in windows of up to 32 tokens, on the other
+ * tokens of its window (for the same pages: appending a token may coarsen its page's codes).
  * T <= 2^20, B <= KQ_KV8_MAX_REQUESTS, n_q / n_kv <= 64, max_len <= 2^28.
  * workspace: kq_attention_kv8_workspace_size() bytes, 256-byte aligned. At most two launches, three where
  * max_new > 32.

@@ -26,15 +26,15 @@
 // With 16 rows in the first form (two blocks of 8) a batch of windows of 32 rows of 64 took 48.7 us
 // in place of 41, and 32 rows at a time 79.
 //
-// Work. The positions of a request, from 513 on, are cut into segments of 512, or 256 for one or two kv heads
-// (longer ones where 64 do not suffice): a function of its own length, so that a row's bits depend on its own request alone. An
-// item is (request, block of rows, segment, kv head). A persistent grid walks the items; each CTA finds
-// them in prefix sums that it forms itself from the lengths on the device, so the host plans nothing and
-// the call can be captured. In a CTA four warps multiply and a fifth copies: it reads page ids and
-// scales 512 positions at a time and fills a ring of slots, each a step of 128 positions of K or of V, by
-// bulk copies of whole pages, across items. Each of the four takes 32 positions of a step through both
-// products alone, and they meet in shared memory once per item. A request of one segment writes its
-// output there; others write partials that a second kernel joins.
+// Work. The positions of a request are cut into segments, where they end being a matter of the position alone: 64 of
+// 512 (256 for one or two kv heads), then 32 of each doubled size; and they are joined in an order that their number
+// does not change. So a row's bits depend on its own request alone, and not on the tokens behind it. An item is
+// (request, block of rows, segment, kv head). A persistent grid walks the items; each CTA finds them in prefix sums
+// that it forms itself from the lengths on the device, so the host plans nothing and the call can be captured. In a
+// CTA four warps multiply and a fifth copies: it reads page ids and scales 512 positions at a time and fills a ring
+// of slots, each a step of 128 positions of K or of V, by bulk copies of whole pages, across items. Each of the four
+// takes 32 positions of a step through both products alone, and they meet in shared memory once per item. A request
+// of one segment writes its output there; others write partials that a second kernel joins.
 //   Windows of more than 32 tokens (prompts) run in a launch of their own, where max_new allows them: blocks of 64
 // rows, 16 for each warp, which takes its rows over all positions and writes them alone. Over contexts from 4096
 // positions on a request is cut so that it alone gives every CTA one item, or two where that comes out more even.
@@ -50,13 +50,12 @@
 // its own 112 to 132 us (its copies' and its items' bookkeeping weighed as much as its products); the fifth warp 100
 // us. Segments of 256 positions 115 us and of 1024 100 us; one token over 4096 positions 9.6, 10.4 and 14.4 us with
 // segments of 256, 512 and 1024. Few heads leave CTAs idle, so that short segments win: one token over 4096
-// positions, 16 / 2 heads, 9.5 us with segments of 256 and 11.4 with 512; 63 tokens over 1030 to 2060, 2 / 1 heads of
-// 64, 15.6 and 19.9; the other side, 64 tokens over 1 to 8191, 8 / 2 heads, 37.4 and 35.4, and with four heads 62 and
-// 57.
+// positions, 16 / 2 heads, 8.7 us with segments of 256 (11.4 with 512); 63 tokens over 1030 to 2060, 2 / 1 heads of
+// 64, 12 us (20); the other side, 64 tokens over 1 to 8191, 8 / 2 heads, 36.7 (35.4), and with four heads 62 (57).
 //
 // Bound by DRAM for single tokens: 64 requests of 1 to 8191 positions, 32 / 8 heads of 128, 543 MB in
-// 99.6 us, 5.45 TB/s, of which 5 us are the join and about 10 the start and the end; four contexts of 128k
-// positions 166 us, 6.3 TB/s (of 6.79 copied). Windows and prompts are bound by the multiplying warps'
+// 98.4 us, 5.5 TB/s, of which 5 us are the join and about 10 the start and the end; four contexts of 128k
+// positions 167 us, 6.3 TB/s (of 6.79 copied). Windows and prompts are bound by the multiplying warps'
 // latency (two or three of them per scheduler): the conversions, the softmax and the products follow one
 // another in each, 92 us for 16 requests x 8 tokens x 4 heads per kv head of 128 over 1000 to 9000
 // positions, 178 MB, and 175 to 210 TFLOP/s for prompts.
@@ -79,7 +78,6 @@ constexpr int kWarps = 4;                          // warps that multiply; one m
 constexpr int kMath = 32 * kWarps, kThreads = kMath + 32;
 constexpr int kWarpPos = 32, kStep = kWarps * kWarpPos;  // positions of a step, 32 per warp
 constexpr int kSegLog2 = 9, kFewSegLog2 = 8;             // positions of a segment at least; for few kv heads
-constexpr int kMaxSegments = 64;                         // segments of a request at most
 constexpr int kWindow = 32 * 16 / kStep;                 // steps whose page ids are read at once, a group of 16 tokens per lane
 constexpr int kSplitTokens = 32;                         // windows up to this many tokens are cut as above
 constexpr int kPromptRows = 64;                          // query rows of an item of larger windows (prompts)
@@ -94,22 +92,21 @@ __device__ unsigned int g_kv8_errors = 0;  // bit 0: a bounded wait gave up; bit
 
 // How a request's positions are cut: a function of its own lengths and the heads.
 struct Cut {
-  int len, count;  // positions of a segment (a multiple of a step), segments
+  int len, count;  // positions of a segment (multiples of a step; 0: those of a window), segments
 };
 struct Cutter {
   int group, n_kv, seg_log2, wave;  // query heads per kv head; kv heads; windows' shortest segments; prompts' CTAs at once
   __host__ __device__ Cut operator()(int len, int n) const {
-    if (n <= kSplitTokens) {  // segments doubled until kMaxSegments hold the request
-      static_assert(kMaxSegments == 64, "a power of two");
-      if (len <= 1 << kSegLog2) return {1 << kSegLog2, 1};  // nothing to join
-      int log2 = seg_log2;
-      const int over = (len - 1) >> (seg_log2 + 6);
+    if (n <= kSplitTokens) {
+      const int u = len - 1, over = u >> (seg_log2 + 6);
+      if (over == 0) return {0, (u >> seg_log2) + 1};
+      int j = 0;  // floor(log2(over))
 #ifdef __CUDA_ARCH__
-      log2 += 32 - __clz(over);
+      j = 31 - __clz(over);
 #else
-      for (int v = over; v > 0; v >>= 1) ++log2;
+      while (over >> (j + 1)) ++j;
 #endif
-      return {1 << log2, (len + (1 << log2) - 1) >> log2};
+      return {0, 64 + 32 * j + (((u >> (seg_log2 + j)) - 64) >> 1) + 1};
     }
     // as many segments as give all CTAs one item, or two where that shares the work out better by 5 %
     const Cut whole = {1 << 29, 1};
@@ -122,6 +119,14 @@ struct Cutter {
     if (count <= 1) return whole;
     const int size = ((len + count - 1) / count + kStep - 1) / kStep * kStep;
     return {size, (len + size - 1) / size};
+  }
+  // Where a segment begins: in windows at a position of its own, whatever the length: 64 segments of the shortest, then
+  // 32 of each doubled size.
+  __host__ __device__ int begin(const Cut& c, int seg) const {
+    if (c.len) return seg * c.len;
+    if (seg < 64) return seg << seg_log2;
+    const int t = seg - 64;
+    return (64 + ((t & 31) << 1)) << (seg_log2 + (t >> 5));
   }
 };
 Cutter cutter_of(int n_kv, int group, int D) {
@@ -381,8 +386,8 @@ __global__ void __launch_bounds__(kThreads, FORM == kRows8 ? (D == 64 ? 4 : 3) :
     x.seen = x.ctx + (p.mask ? 0 : token_of(p, x.row0) + 1);
     const int last = (x.end + kStep - 1) / kStep;
     static_assert((1 << kFewSegLog2) % kStep == 0 && kFewSegLog2 <= kSegLog2, "segments are cut into steps");
-    x.step0 = x.seg * (cut.len / kStep);
-    x.step1 = min(x.step0 + cut.len / kStep, last);
+    x.step0 = p.cut.begin(cut, x.seg) / kStep;
+    x.step1 = min(p.cut.begin(cut, x.seg + 1) / kStep, last);
     return x;
   };
 
@@ -885,14 +890,88 @@ __global__ void __launch_bounds__(kThreads, FORM == kRows8 ? (D == 64 ? 4 : 3) :
   if (dead && lane == 0) atomicOr(&g_kv8_errors, 1u);
 }
 
-// The segments of a request added up: 1 to 8 warps of a CTA per (token, query head), each taking every
-// k-th segment in order, lane j holding the weight of its j-th; then the warps' sums in warp order.
+// Sums 4, 2 and 1 apart of `COUNT` sums.
+template <int COUNT, int N>
+__device__ __forceinline__ void fold_sums(float (&acc)[COUNT][N]) {
+#pragma unroll
+  for (int h = COUNT / 2; h; h >>= 1)
+#pragma unroll
+    for (int q = 0; q < h; ++q)
+#pragma unroll
+      for (int e = 0; e < N; ++e) acc[q][e] += acc[q + h][e];
+}
+
+// The segments of a request added up in an order that does not depend on how many there are: eight sums, each of
+// every eighth segment in order, then sums 4, 2 and 1 apart. K warps of a CTA share them: warp `sub` takes sums
+// sub, sub + K, ... and joins its own. sum: D / 32 dims of this lane, and the weights'.
+template <int K, int E>
+__device__ __forceinline__ void join_segments(float (&sum)[E + 1], const AttnKV8Params& p, long long first, long long step, int nseg, int sub, float mb) {
+  constexpr int SUMS = 8 / K;
+  float acc[SUMS][E + 1];
+#pragma unroll
+  for (int q = 0; q < SUMS; ++q)
+#pragma unroll
+    for (int e = 0; e <= E; ++e) acc[q][e] = 0.f;
+  for (int s0 = sub; s0 < nseg; s0 += 8 * K) {
+    float2 ml[8];
+    float v[8][E];
+#pragma unroll
+    for (int u = 0; u < 8; ++u) {
+      const int s = s0 + u * K;
+      const long long at = first + s * step;
+      const float* src = p.part + at * 32 * E + (threadIdx.x & 31) * E;
+      ml[u] = make_float2(0.f, 0.f);
+#pragma unroll
+      for (int e = 0; e < E; ++e) v[u][e] = 0.f;
+      if (s < nseg) {
+        ml[u] = p.part_ml[at];
+        if (E == 4) {
+          const float4 x = *reinterpret_cast<const float4*>(src);
+          v[u][0] = x.x, v[u][1] = x.y, v[u][E - 2] = x.z, v[u][E - 1] = x.w;
+        } else {
+          const float2 x = *reinterpret_cast<const float2*>(src);
+          v[u][0] = x.x, v[u][1] = x.y;
+        }
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < 8; ++u) {
+      const float f = ml[u].y == 0.f ? 0.f : fast_exp2(ml[u].x - mb);
+      float(&to)[E + 1] = acc[u % SUMS];
+#pragma unroll
+      for (int e = 0; e < E; ++e) to[e] = __fmaf_rn(f, v[u][e], to[e]);
+      to[E] = __fmaf_rn(f, ml[u].y, to[E]);
+    }
+  }
+  fold_sums(acc);
+#pragma unroll
+  for (int e = 0; e <= E; ++e) sum[e] = acc[0][e];
+}
+
+// The other warps' sums, in shared memory behind this one's, joined with it.
+template <int K, int D>
+__device__ __forceinline__ void join_warps(float (&sum)[D / 32 + 1], const float (*sm_o)[D], const float* sm_sum) {
+  constexpr int E = D / 32;
+  const int lane = threadIdx.x & 31;
+  float acc[K][E + 1];
+#pragma unroll
+  for (int q = 0; q < K; ++q) {
+#pragma unroll
+    for (int e = 0; e < E; ++e) acc[q][e] = sm_o[q][lane * E + e];
+    acc[q][E] = sm_sum[q];
+  }
+  fold_sums(acc);
+#pragma unroll
+  for (int e = 0; e <= E; ++e) sum[e] = acc[0][e];
+}
+
 template <int D>
-__global__ void __launch_bounds__(kCombThreads) attn_kv8_combine_kernel(const AttnKV8Params p) {
+__global__ void __launch_bounds__(kCombThreads, D == 64 ? 3 : 1) attn_kv8_combine_kernel(const AttnKV8Params p) {
   constexpr int W = kCombThreads / 32, E = D / 32;
   extern __shared__ __align__(16) int sm_req[];
   __shared__ long long sm_scan[3 * W];
-  __shared__ float sm_o[W][D], sm_sum[W];
+  __shared__ __align__(16) float sm_o[W][D];
+  __shared__ float sm_sum[W];
   Request* req = reinterpret_cast<Request*>(sm_req);
   const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
   // the lengths were written before the attention kernel passed its own wait, after which alone this
@@ -909,64 +988,39 @@ __global__ void __launch_bounds__(kCombThreads) attn_kv8_combine_kernel(const At
     const bool live = task < n * n_q;
     const int i = task / n_q, hq = task - i * n_q, h = hq / p.group, row = i * p.group + hq - h * p.group;
     const long long step = (long long)n * p.group, first = req[r].part * p.n_kv + h * nseg * step + row;
-    float acc[E], den = 0.f;
+    float sum[E + 1];  // the last: of the weights
 #pragma unroll
-    for (int e = 0; e < E; ++e) acc[e] = 0.f;
+    for (int e = 0; e <= E; ++e) sum[e] = 0.f;
     if (live) {
       float mx = -INFINITY;
       for (int s = lane; s < nseg; s += 32) mx = fmaxf(mx, p.part_ml[first + s * step].x);
 #pragma unroll
       for (int x = 1; x < 32; x <<= 1) mx = fmaxf(mx, __shfl_xor_sync(~0u, mx, x));
       const float mb = mx == -INFINITY ? 0.f : mx;
-      const int mine = (nseg - sub + k - 1) / k;  // segments sub + j k
-      for (int j0 = 0; j0 < mine; j0 += 32) {
-        float wt = 0.f;
-        if (j0 + lane < mine) {
-          const float2 ml = p.part_ml[first + (sub + (j0 + lane) * k) * step];
-          wt = ml.y == 0.f ? 0.f : fast_exp2(ml.x - mb);
-          den += wt * ml.y;
-        }
-        const int jn = min(32, mine - j0);
-#pragma unroll 8
-        for (int j = 0; j < jn; ++j) {
-          const float f = __shfl_sync(~0u, wt, j);
-          const float* src = p.part + (first + (sub + (j0 + j) * k) * step) * D + lane * E;
-          if (E == 4) {
-            const float4 v = *reinterpret_cast<const float4*>(src);
-            acc[0] += f * v.x;
-            acc[1] += f * v.y;
-            acc[E - 2] += f * v.z;
-            acc[E - 1] += f * v.w;
-          } else {
-            const float2 v = *reinterpret_cast<const float2*>(src);
-            acc[0] += f * v.x;
-            acc[1] += f * v.y;
-          }
-        }
-      }
-#pragma unroll
-      for (int x = 1; x < 32; x <<= 1) den += __shfl_xor_sync(~0u, den, x);
+      if (k == 1) join_segments<1, E>(sum, p, first, step, nseg, sub, mb);
+      else if (k == 2) join_segments<2, E>(sum, p, first, step, nseg, sub, mb);
+      else if (k == 4) join_segments<4, E>(sum, p, first, step, nseg, sub, mb);
+      else join_segments<8, E>(sum, p, first, step, nseg, sub, mb);
     }
     if (k > 1) {  // uniform in the CTA
 #pragma unroll
-      for (int e = 0; e < E; ++e) sm_o[w][lane * E + e] = acc[e];
-      if (lane == 0) sm_sum[w] = den;
+      for (int e = 0; e < E; ++e) sm_o[w][lane * E + e] = sum[e];
+      if (lane == 0) sm_sum[w] = sum[E];
       __syncthreads();
       if (sub == 0) {
-        for (int j = 1; j < k; ++j) {
-          den += sm_sum[w + j];
-#pragma unroll
-          for (int e = 0; e < E; ++e) acc[e] += sm_o[w + j][lane * E + e];
-        }
+        if (k == 2) join_warps<2, D>(sum, sm_o + w, sm_sum + w);
+        else if (k == 4) join_warps<4, D>(sum, sm_o + w, sm_sum + w);
+        else join_warps<8, D>(sum, sm_o + w, sm_sum + w);
       }
       __syncthreads();
     }
+    const float den = sum[E];
     if (live && sub == 0) {
       const float inv = den == 0.f ? 0.f : 1.f / den;  // as a request of one segment
       const long long at = (tok0 + i) * p.os + (long long)hq * D + lane * E;
 #pragma unroll
       for (int e = 0; e < E; e += 2) {
-        const float v0 = acc[e] * inv, v1 = acc[e + 1] * inv;
+        const float v0 = sum[e] * inv, v1 = sum[e + 1] * inv;
         if (p.o_f32) *reinterpret_cast<float2*>(static_cast<float*>(p.o) + at + e) = make_float2(v0, v1);
         else *reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(p.o) + at + e) = (uint32_t)f32_to_bf16_rn(v0) | (uint32_t)f32_to_bf16_rn(v1) << 16;
       }
@@ -1007,7 +1061,7 @@ int launch_all(const AttnKV8Params& p, int num_sms, cudaStream_t s, std::string*
   const bool rows8 = (long long)p.max_new * p.group <= 8;
   if ((rows8 ? launch_form<D, kRows8, WIDE>(p, num_sms, s, err) : launch_form<D, kRows16, WIDE>(p, num_sms, s, err)) != 0) return -1;
   if (p.max_new > kSplitTokens && launch_form<D, kPrompt, WIDE>(p, num_sms, s, err) != 0) return -1;
-  if (p.max_len <= 1 << kSegLog2) return 0;  // no request can have two segments
+  if (p.max_len <= 1 << p.cut.seg_log2) return 0;  // no request can have two segments
   const long long tasks = (long long)p.T * p.n_kv * p.group;
   // no more CTAs than the longest request's rows would need: each forms the prefix sums
   const long long want = (tasks * combine_warps(p.cut(p.max_len, 1).count) + kCombThreads / 32 - 1) / (kCombThreads / 32);

@@ -471,3 +471,19 @@ def test_segments_of_a_prompt_end_inside_pages_and_windows_of_page_ids():
     """Lengths whose shares are odd multiples of 128 positions."""
     attn_case([(4100, 33), (6700, 47), (7300, 64), (11111, 130)], 64, 64, 6, 3, "bf16", "f32")
     attn_case([(5003, 60), (8200, 35)], 32, 128, 24, 12, "bf16", "bf16")
+
+
+@pytest.mark.parametrize("n_q,n_kv,D", [(4, 1, 64), (8, 2, 128), (3, 3, 64)])
+def test_windows_over_every_cut_give_the_bits_of_single_tokens(n_q, n_kv, D):
+    """Windows whose tokens stand before and after the positions where segments, their size or the warps that join
+    them change."""
+    P, n = 16, 4
+    ends = [256, 512, 1024, 2048, 4096, 8192, 16384, 32768, 65536]
+    lens = [(e - 2, n) for e in ends]
+    cache, parts, table, ctx, new, q = make(lens, P, D, n_q, n_kv, "f32", 21)
+    for y in ("f32", "bf16"):
+        o = run(cache, table, ctx, new, q, y)
+        for i in range(n):
+            a = run(cache, table, ctx + i, np.ones_like(new), q.view(len(ends), n, n_q, D)[:, i].contiguous(), y)
+            same = (a == o.view(len(ends), n, n_q, D)[:, i]).flatten(1).all(1)
+            assert same.all(), (i, [e for e, s in zip(ends, same.tolist()) if not s])
