@@ -454,10 +454,10 @@ int kq_kv8_append(const kq_kv8_cache* cache, int x_dtype, const void* k, long lo
  *              ctx + new, and of the sum of ctx + new over the requests: they size the launches and
  *              the workspace only. A request beyond them is not computed and sets bit 1 of
  *              kq_device_errors(), as do page ids outside the cache (those rows come out NaN)
- * Sums and softmax statistics are fp32; codes enter the tensor cores exactly. With fp32 output q
- * and the weights are carried in 22 bits; with bf16 output in fp16 (11 bits). A row's bits depend
- * on its own request alone: not on the other requests, nor, in windows of up to 32 tokens, on the other
- * tokens of its window (for the same pages: appending a token may coarsen its page's codes).
+ * Sums and softmax statistics are fp32; codes enter the tensor cores exactly. fp32 queries are
+ * carried in 22 bits; bf16 ones need 8 of fp16's 11. Weights are carried in 22 bits with fp32 output,
+ * in fp16 (11 bits) with bf16 output. A row's bits depend on its own request alone: not on the other
+ * requests, nor, in windows of up to 32 tokens, on the other tokens of its window (for the same pages: appending a token may coarsen its page's codes).
  * T <= 2^20, B <= KQ_KV8_MAX_REQUESTS, n_q / n_kv <= 64, max_len <= 2^28.
  * workspace: kq_attention_kv8_workspace_size() bytes, 256-byte aligned. At most two launches, three where
  * max_new > 32.

@@ -9,9 +9,12 @@
 // the MMA operands, see kv8.cuh).
 //
 // Precision. q is scaled per row by the power of two that puts its largest value in [2^14, 2^15)
-// and rounded to fp16: exact for bf16 values within 2^-28 of the row's largest; for fp32 queries a
-// relative 2^-12, below the rounding of a bf16 output. For fp32 outputs (WIDE) q and w are split into
-// fp16 hi + lo parts (22 bits). The weights that enter a product are those against the largest score of
+// and rounded to fp16: exact for bf16 values within 2^-28 of the row's largest. fp32 queries, and all of them where
+// the output is fp32, are split into fp16 hi + lo parts (QP = 2, 22 bits): rounded to one they would move a score by
+// 2^-12 of sum_d |scale q_d k_d|, and the weights by as much, which passes a bf16 output's 2^-9 from scores of 8 on. The
+// second part costs, with bf16 outputs, 84 -> 92 us for 16 requests x 8 tokens over 1000 to 9000 positions, 94 -> 105 for 64
+// tokens over 1 to 8191, 374 -> 435 for 2 x 2048 (32 / 8 heads of 128), 10.2 -> 11.2 for one token over 4096 (16 / 4 heads).
+// Weights are one fp16 part (2^-12 of themselves) for bf16 outputs, two (WP = 2) for fp32 ones. The weights that enter a product are those against the largest score of
 // their page (of up to 32 positions of it), up by 2^15: fp16 then holds weights down to 2^-29 of that in
 // full, and an absolute 2^-40 below. The accumulators take the page's share of the softmax and its v scale
 // in fp32, so pages whose scales lie far apart lose nothing to one another. Weight sums are products with
@@ -292,16 +295,16 @@ __device__ __forceinline__ void math_barrier() { asm volatile("bar.sync 1, %0;" 
 // Shared memory of a CTA: a ring of slots (a step's K or its V), the warps' outputs of an item, for 16
 // query rows the item's query operands, the requests.
 enum Form { kRows8, kRows16, kPrompt };
-template <int D, Form FORM, bool WIDE>
+template <int D, Form FORM, int QP>
 struct AttnSmem {
-  static constexpr int RB = FORM == kPrompt ? kPromptRows : FORM == kRows16 ? 16 : 8, PARTS = WIDE ? 2 : 1;
+  static constexpr int RB = FORM == kPrompt ? kPromptRows : FORM == kRows16 ? 16 : 8;
   static constexpr int kDepth = D == 64 ? 6 : FORM == kPrompt ? 4 : 3;
   static constexpr int kSlot = kStep * D;
   static constexpr int kOut = kDepth * kSlot;                                            // [warp][RB][D + 4] floats
   static constexpr int kOutWarp = FORM == kPrompt ? 0 : RB * (D + 4);
   static constexpr int kQ = kOut + kWarps * kOutWarp * 4;                                // [part][D / 16][32 lanes][4 words]
   static constexpr int kQPart = FORM == kRows8 ? 0 : D / 16 * 512;
-  static constexpr int kReq = kQ + (FORM == kPrompt ? kWarps : 1) * PARTS * kQPart;      // prompts: for each warp
+  static constexpr int kReq = kQ + (FORM == kPrompt ? kWarps : 1) * QP * kQPart;         // prompts: for each warp
   static constexpr size_t bytes(int B) { return kReq + (size_t)(B + 1) * sizeof(Request); }
 };
 
@@ -314,13 +317,12 @@ struct Item {  // (request, kv head, block of query rows, segment)
 // kRows8: 8 query rows as the B operand (rows 2 t4, 2 t4 + 1 in a lane); the others: 16 as the A operand (rows
 // g, g + 8). kRows8 and kRows16 give a row the same bits: every sum over dims, positions or lanes is the
 // tensor cores' own, in the same order of k. kPrompt: windows of more than 32 tokens, 64 rows an item, 16 for
-// each warp over all positions of a step, so that nothing is joined at the end.
-template <int D, Form FORM, bool WIDE>
+// each warp over all positions of a step, so that nothing is joined at the end. QP, WP: fp16 parts of queries and weights.
+template <int D, Form FORM, int QP, int WP>
 __global__ void __launch_bounds__(kThreads, FORM == kRows8 ? (D == 64 ? 4 : 3) : D == 64 ? 3 : 2) attn_kv8_kernel(const AttnKV8Params p) {
   constexpr bool R16 = FORM != kRows8, PR = FORM == kPrompt;
-  using S = AttnSmem<D, FORM, WIDE>;
+  using S = AttnSmem<D, FORM, QP>;
   constexpr int RB = S::RB, C32 = D / 32, K16 = D / 16, DEPTH = S::kDepth;
-  constexpr int PARTS = S::PARTS;              // fp16 parts of queries and weights
   constexpr int NV = R16 ? 4 : 2;              // scores of a row per lane and group of 16 tokens
   constexpr int NO = R16 ? 2 * K16 : K16;      // output tiles: 8 dims by 16 rows, or 16 dims by 8 rows
   extern __shared__ __align__(128) uint8_t smem[];
@@ -335,7 +337,7 @@ __global__ void __launch_bounds__(kThreads, FORM == kRows8 ? (D == 64 ? 4 : 3) :
   Request* req = reinterpret_cast<Request*>(smem + S::kReq);
   const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5, g = lane >> 2, t4 = lane & 3;
   const int wrow = PR ? 16 * w : 0;  // the warp's first row of the item
-  uint32_t* sm_q = reinterpret_cast<uint32_t*>(smem + S::kQ) + (PR ? w * S::PARTS * (S::kQPart / 4) : 0);
+  uint32_t* sm_q = reinterpret_cast<uint32_t*>(smem + S::kQ) + (PR ? w * QP * (S::kQPart / 4) : 0);
   if (tid == 0) {
     for (int k = 0; k < DEPTH; ++k) {
       mbar_init(&sm_full[k], 1);
@@ -467,7 +469,7 @@ __global__ void __launch_bounds__(kThreads, FORM == kRows8 ? (D == 64 ? 4 : 3) :
     // ---- query operands: lane (g, t4) takes row g of a block of 8 at dims 16 s + 4 t4 .. + 3; rows past
     // the last are zeros that see nothing. 8 rows: each warp for itself, in registers; 16: warps 0 and 1
     // for all, in shared memory
-    uint2 qh[R16 ? 1 : K16], ql[!R16 && WIDE ? K16 : 1];
+    uint2 qh[R16 ? 1 : K16], ql[!R16 && QP == 2 ? K16 : 1];
     float hq[2], rf[2];
     int lim[2];
     uint32_t see[2];
@@ -525,7 +527,7 @@ __global__ void __launch_bounds__(kThreads, FORM == kRows8 ? (D == 64 ? 4 : 3) :
         } else {
           qh[R16 ? 0 : s] = hi;
         }
-        if (WIDE) {
+        if (QP == 2) {
           const uint2 lo = make_uint2(f2_to_h2(f[0] - h_lo_to_f(hi.x), f[2] - h_lo_to_f(hi.x >> 16)),
                                       f2_to_h2(f[1] - h_lo_to_f(hi.y), f[3] - h_lo_to_f(hi.y >> 16)));
           mma_f16_16816(half, halves, lo.x, lo.y, half);
@@ -533,7 +535,7 @@ __global__ void __launch_bounds__(kThreads, FORM == kRows8 ? (D == 64 ? 4 : 3) :
             q16[S::kQPart / 4] = lo.x;
             q16[S::kQPart / 4 + 2] = lo.y;
           } else {
-            ql[!R16 && WIDE ? s : 0] = lo;
+            ql[!R16 && QP == 2 ? s : 0] = lo;
           }
         }
       }
@@ -606,10 +608,10 @@ __global__ void __launch_bounds__(kThreads, FORM == kRows8 ? (D == 64 ? 4 : 3) :
       const float kf[2] = {kf2.x, kf2.y}, vf[2] = {vf2.x, vf2.y};
 #pragma unroll
       for (int cc = 0; cc < C32; ++cc) {
-        uint32_t qa[PARTS][2][4];
+        uint32_t qa[QP][2][4];
         if (R16) {
 #pragma unroll
-          for (int part = 0; part < PARTS; ++part)
+          for (int part = 0; part < QP; ++part)
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
               const uint4 q = lds128(sm_q + part * (S::kQPart / 4) + ((2 * cc + i) * 32 + lane) * 4);
@@ -631,14 +633,14 @@ __global__ void __launch_bounds__(kThreads, FORM == kRows8 ? (D == 64 ? 4 : 3) :
           for (int i = 0; i < 2; ++i) {
             if (R16) {
 #pragma unroll
-              for (int part = 0; part < PARTS; ++part) {
+              for (int part = 0; part < QP; ++part) {
                 mma_f16_16816(sc[st][0], qa[part][i], a[i][0], a[i][2], sc[st][0]);
                 mma_f16_16816(sc[st][R16 ? 1 : 0], qa[part][i], a[i][1], a[i][3], sc[st][R16 ? 1 : 0]);
               }
             } else {
               const int s = R16 ? 0 : 2 * cc + i;
               mma_f16_16816(sc[st][0], a[i], qh[s].x, qh[s].y, sc[st][0]);
-              if (WIDE) mma_f16_16816(sc[st][0], a[i], ql[WIDE ? s : 0].x, ql[WIDE ? s : 0].y, sc[st][0]);
+              if (QP == 2) mma_f16_16816(sc[st][0], a[i], ql[QP == 2 ? s : 0].x, ql[QP == 2 ? s : 0].y, sc[st][0]);
             }
           }
         }
@@ -708,7 +710,7 @@ __global__ void __launch_bounds__(kThreads, FORM == kRows8 ? (D == 64 ? 4 : 3) :
         }
       }
       // the weights as operands: pairs of tokens (4 t, 4 t + 2) and (4 t + 1, 4 t + 3), as codes_to_h2 makes them
-      uint32_t wt[2][PARTS][4];  // 8 rows: two of the four
+      uint32_t wt[2][WP][4];  // 8 rows: two of the four
 #pragma unroll
       for (int st = 0; st < 2; ++st) {
         if (R16) {
@@ -717,13 +719,13 @@ __global__ void __launch_bounds__(kThreads, FORM == kRows8 ? (D == 64 ? 4 : 3) :
             const float a = sv[st][i & 1][i >> 1], b = sv[st][i & 1][R16 ? 2 + (i >> 1) : 0];
             const uint32_t hi = f2_to_h2(a, b);
             wt[st][0][i] = hi;
-            if (WIDE) wt[st][WIDE ? 1 : 0][i] = f2_to_h2(a - h_lo_to_f(hi), b - h_lo_to_f(hi >> 16));
+            if (WP == 2) wt[st][WP - 1][i] = f2_to_h2(a - h_lo_to_f(hi), b - h_lo_to_f(hi >> 16));
           }
         } else {
           const uint32_t e0 = f2_to_h2(sv[st][0][0], sv[st][1][0]), e1 = f2_to_h2(sv[st][0][1], sv[st][1][1]);
           weight_operand(wt[st][0], movmatrix(e0), movmatrix(e1));
-          if (WIDE)
-            weight_operand(wt[st][WIDE ? 1 : 0], movmatrix(f2_to_h2(sv[st][0][0] - h_lo_to_f(e0), sv[st][1][0] - h_lo_to_f(e0 >> 16))),
+          if (WP == 2)
+            weight_operand(wt[st][WP - 1], movmatrix(f2_to_h2(sv[st][0][0] - h_lo_to_f(e0), sv[st][1][0] - h_lo_to_f(e0 >> 16))),
                            movmatrix(f2_to_h2(sv[st][0][1] - h_lo_to_f(e1), sv[st][1][1] - h_lo_to_f(e1 >> 16))));
         }
       }
@@ -746,7 +748,7 @@ __global__ void __launch_bounds__(kThreads, FORM == kRows8 ? (D == 64 ? 4 : 3) :
 #pragma unroll
       for (int st = 0; st < 2; ++st) {
 #pragma unroll
-        for (int part = 0; part < PARTS; ++part) {
+        for (int part = 0; part < WP; ++part) {
           if (R16) mma_f16_16816(acc, wt[st][part], kOnes, kOnes, acc);
           else mma_f16_16816(acc, ones, wt[st][part][0], wt[st][part][1], acc);
         }
@@ -776,7 +778,7 @@ __global__ void __launch_bounds__(kThreads, FORM == kRows8 ? (D == 64 ? 4 : 3) :
           codes_to_h2(v.z, a[1][0], a[1][2]);
           codes_to_h2(v.w, a[1][1], a[1][3]);
 #pragma unroll
-          for (int part = 0; part < PARTS; ++part)
+          for (int part = 0; part < WP; ++part)
 #pragma unroll
             for (int s = 0; s < NA; ++s) {
               if (R16) mma_f16_16816(av[s], wt[st][part], a[s >> 1][s & 1], a[s >> 1][2 + (s & 1)], av[s]);
@@ -1028,10 +1030,10 @@ __global__ void __launch_bounds__(kCombThreads, D == 64 ? 3 : 1) attn_kv8_combin
   }
 }
 
-template <int D, Form FORM, bool WIDE>
+template <int D, Form FORM, int QP, int WP>
 int launch_form(const AttnKV8Params& p, int num_sms, cudaStream_t s, std::string* err) {
-  const size_t smem = AttnSmem<D, FORM, WIDE>::bytes(p.B);
-  auto* kernel = attn_kv8_kernel<D, FORM, WIDE>;
+  const size_t smem = AttnSmem<D, FORM, QP>::bytes(p.B);
+  auto* kernel = attn_kv8_kernel<D, FORM, QP, WP>;
   // CTAs per SM at this shared-memory size, asked for once per host thread, device and size
   static thread_local int known_dev = -1, per_sm = 0;
   static thread_local size_t known_smem = 0;
@@ -1056,11 +1058,11 @@ int launch_form(const AttnKV8Params& p, int num_sms, cudaStream_t s, std::string
 
 // Windows of up to 32 tokens, and, where max_new allows larger ones, those in a launch of their own: which
 // form a request takes, and its bits, do not depend on the others.
-template <int D, bool WIDE>
+template <int D, int QP, int WP>
 int launch_all(const AttnKV8Params& p, int num_sms, cudaStream_t s, std::string* err) {
   const bool rows8 = (long long)p.max_new * p.group <= 8;
-  if ((rows8 ? launch_form<D, kRows8, WIDE>(p, num_sms, s, err) : launch_form<D, kRows16, WIDE>(p, num_sms, s, err)) != 0) return -1;
-  if (p.max_new > kSplitTokens && launch_form<D, kPrompt, WIDE>(p, num_sms, s, err) != 0) return -1;
+  if ((rows8 ? launch_form<D, kRows8, QP, WP>(p, num_sms, s, err) : launch_form<D, kRows16, QP, WP>(p, num_sms, s, err)) != 0) return -1;
+  if (p.max_new > kSplitTokens && launch_form<D, kPrompt, QP, WP>(p, num_sms, s, err) != 0) return -1;
   if (p.max_len <= 1 << p.cut.seg_log2) return 0;  // no request can have two segments
   const long long tasks = (long long)p.T * p.n_kv * p.group;
   // no more CTAs than the longest request's rows would need: each forms the prefix sums
@@ -1072,7 +1074,8 @@ int launch_all(const AttnKV8Params& p, int num_sms, cudaStream_t s, std::string*
 
 template <int D>
 int launch_dim(const AttnKV8Params& p, int num_sms, cudaStream_t s, std::string* err) {
-  return p.o_f32 ? launch_all<D, true>(p, num_sms, s, err) : launch_all<D, false>(p, num_sms, s, err);
+  if (p.o_f32) return launch_all<D, 2, 2>(p, num_sms, s, err);
+  return p.q_f32 ? launch_all<D, 2, 1>(p, num_sms, s, err) : launch_all<D, 1, 1>(p, num_sms, s, err);
 }
 
 // Partial rows at most: windows of up to 32 tokens have len / 512 + 1 segments, larger ones segments x rows
