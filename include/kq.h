@@ -436,9 +436,11 @@ size_t kq_kv8_bytes(int n_pages, int page_size, int n_kv, int head_dim);
  * coding all of its tokens in one call gives: the cache does not depend on how tokens were
  * grouped into calls. A page with a value that is not finite gets scale NaN (until offset 0 is
  * written again). Scales do not shrink: overwriting a token (a rejected guess) keeps the page's.
- * The tokens of one call that go to one page stand next to each other at ascending slots, as
- * kq_pages_plan gives them; slots beyond the pages are skipped and set bit 1 of
- * kq_device_errors(). T <= 2^30. Errors: KQ_ERR_ARG, KQ_ERR_UNSUPPORTED, KQ_ERR_CUDA. */
+ * The rows of one call that go to one page stand behind one another at ascending slots, as
+ * kq_pages_plan gives them: skipped rows may stand between them and slots may be left out (they hold what
+ * they held), but no rows of other pages (such a page's codes and scale would be undefined). Slots beyond
+ * the pages are skipped too and set bit 1 of kq_device_errors(). T <= 2^30.
+ * Errors: KQ_ERR_ARG, KQ_ERR_UNSUPPORTED, KQ_ERR_CUDA. */
 int kq_kv8_append(const kq_kv8_cache* cache, int x_dtype, const void* k, long long k_stride, const void* v,
                   long long v_stride, const int* slot, int T, void* stream);
 
