@@ -1053,7 +1053,7 @@ int launch_form(const AttnKV8Params& p, int num_sms, cudaStream_t s, std::string
     *err = std::string("attention_kv8: ") + (e != cudaSuccess ? cudaGetErrorString(e) : "the kernel does not fit an SM");
     return -1;
   }
-  return launch_pdl(kernel, dim3(num_sms * per_sm), dim3(kThreads), smem, s, p, "attention_kv8", err, true);
+  return launch_pdl(kernel, dim3(num_sms * per_sm), dim3(kThreads), smem, s, p, "attention_kv8", err);
 }
 
 // Windows of up to 32 tokens, and, where max_new allows larger ones, those in a launch of their own: which
@@ -1068,6 +1068,8 @@ int launch_all(const AttnKV8Params& p, int num_sms, cudaStream_t s, std::string*
   // no more CTAs than the longest request's rows would need: each forms the prefix sums
   const long long want = (tasks * combine_warps(p.cut(p.max_len, 1).count) + kCombThreads / 32 - 1) / (kCombThreads / 32);
   const int grid = (int)(want < (long long)num_sms * 8 ? want : (long long)num_sms * 8);
+  static SmemAllowed allowed;
+  if (allow_smem(allowed, attn_kv8_combine_kernel<D>, (KQ_KV8_MAX_REQUESTS + 1) * sizeof(Request), "attention_kv8 combine", err) != 0) return -1;
   return launch_pdl(attn_kv8_combine_kernel<D>, dim3(grid), dim3(kCombThreads), (size_t)(p.B + 1) * sizeof(Request), s, p,
                     "attention_kv8 combine", err);
 }

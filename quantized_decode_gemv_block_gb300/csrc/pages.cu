@@ -240,6 +240,8 @@ int launch_pages_plan(const PagesArgs& a, int num_sms, cudaStream_t s, std::stri
   p.T = a.T;
   p.status = a.status;
   const size_t smem = (size_t)3 * (a.B + 1) * sizeof(int);
+  static SmemAllowed allowed;
+  if (allow_smem(allowed, pages_plan_kernel, (size_t)3 * (KQ_PAGES_MAX_REQUESTS + 1) * sizeof(int), "pages_plan", err) != 0) return -1;
   // one token per thread up to one CTA per SM; beyond it a CTA's share grows, as each CTA scans all requests
   const int threads = a.B > 256 || a.T > 256 * num_sms ? kMaxThreads : 256;
   const long long want = ((long long)a.T + threads - 1) / threads;
