@@ -1033,7 +1033,11 @@ __global__ void __launch_bounds__(kCombThreads, D == 64 ? 3 : 1) attn_kv8_combin
 template <int D, Form FORM, int QP, int WP>
 int launch_form(const AttnKV8Params& p, int num_sms, cudaStream_t s, std::string* err) {
   const size_t smem = AttnSmem<D, FORM, QP>::bytes(p.B);
+  constexpr size_t kMost = AttnSmem<D, FORM, QP>::bytes(KQ_KV8_MAX_REQUESTS);
+  static_assert(kMost + 2048 <= 227 * 1024, "with the kernel's static memory it fits an SM");
   auto* kernel = attn_kv8_kernel<D, FORM, QP, WP>;
+  static SmemAllowed allowed;
+  if (allow_smem(allowed, kernel, kMost, "attention_kv8", err) != 0) return -1;
   // CTAs per SM at this shared-memory size, asked for once per host thread, device and size
   static thread_local int known_dev = -1, per_sm = 0;
   static thread_local size_t known_smem = 0;
@@ -1042,8 +1046,7 @@ int launch_form(const AttnKV8Params& p, int num_sms, cudaStream_t s, std::string
   if (e == cudaSuccess && (dev != known_dev || smem != known_smem)) {
     per_sm = 0;
     known_dev = -1;
-    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-    if (e == cudaSuccess) e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kernel, kThreads, smem);
+    e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kernel, kThreads, smem);
     if (e == cudaSuccess && per_sm > 0) {
       known_dev = dev;
       known_smem = smem;
