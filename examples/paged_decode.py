@@ -75,7 +75,8 @@ class PagedDecoder:
         return kq.gemm("q4_k", lay[name], x.contiguous(), n, k)
 
     def step(self, new: dict[int, list[int]], logits: bool = False):
-        """Runs the new tokens of the slots given; returns {slot: next token}, or {slot: logits} if asked."""
+        """Runs the new tokens of the slots given; returns {slot: next token}, or {slot: logits} if asked. A step for which
+        there are no pages raises RuntimeError and changes nothing."""
         d, B = self.d, self.table.shape[0]
         counts = [len(new.get(s, ())) for s in range(B)]
         tokens = [t for s in range(B) for t in new.get(s, ())]
@@ -83,6 +84,8 @@ class PagedDecoder:
         assert 0 < T <= self.max_tokens
         new_len = torch.tensor(counts, dtype=torch.int32, device="cuda")
         plan = kq.pages_plan(self.length, new_len, self.table, self.free, self.n_free, self.page_size, T)
+        if plan.status.item():  # nothing was handed out: the decoder is as it was
+            raise RuntimeError(f"pages_plan refused the step: status {plan.status.item()}")
         self.n_free = plan.n_free.clone()
         max_len = max(a + b for a, b in zip(self.lens, counts))
         x = self.embed[torch.tensor(tokens, device="cuda")]
@@ -109,8 +112,6 @@ class PagedDecoder:
         got = []
         for i in range(0, len(live), 16):
             got += kq.head_argmax(self.head, None, hidden[i:i + 16].contiguous(), d["vocab"], d["hidden"], all_rows=True)[0].tolist()
-        if plan.status.item():
-            raise RuntimeError(f"pages_plan refused the step: status {plan.status.item()}")
         return dict(zip(live, got))
 
     def release(self, slots):
