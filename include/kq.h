@@ -396,7 +396,8 @@ int kq_pages_release(const int* len, const unsigned char* done, int B, int page_
 /* Rotary positions of one or more axes, on q and k in one launch. Pair i < rot_dim/2 of a head
  * turns by angle = pos[axis_i][t] * inv_freq[i]: (a, b) -> (a cos - b sin, b cos + a sin); pair i is
  * elements (i, i + rot_dim/2), or (2i, 2i+1) with KQ_ROPE_ADJACENT. Elements from rot_dim on are
- * copied. Angles are formed modulo a turn in 64-bit integers: no position is too large; the
+ * copied. Angles are formed modulo a turn in 64-bit integers, off by under 2^-24 rad for
+ * |pos * inv_freq| < 2^38, so no position is too large; an inv_freq that is not finite gives NaN. The
  * products and sums are fp32, rounded once to y_dtype.
  *   q, k, q_out, k_out  T rows of n heads of head_dim, token strides in elements (views into a
  *             fused qkv row are fine). A tensor with n = 0 heads may be NULL. In place: same

@@ -7,8 +7,8 @@
 //
 // The angle is formed as a binary fraction of a turn in 64-bit integers, so that positions of any
 // size lose nothing: freq = m 2^e (24-bit m) gives F = m C 2^(e-2), C = round(2^64 * 2/pi), the
-// turn fraction per position in units of 2^-64 (error below one unit for freq <= 1); pos * F
-// modulo 2^64 is the phase, exact but for pos units. Its top 32 bits are cut into the nearest
+// turn fraction per position in units of 2^-64 (error below 1 + freq / 8 units); pos * F
+// modulo 2^64 is the phase, exact but for pos times that. A frequency that is not finite gives NaN. Its top 32 bits are cut into the nearest
 // quarter turn and a rest in [-1/8, 1/8] turn, whose sine and cosine come from sincospif.
 //
 // Bound by DRAM: q and k are read and written once. A CTA forms the angles of its tokens once, in
@@ -183,7 +183,9 @@ __global__ void __launch_bounds__(kThreads, sizeof(X) == 2 ? 6 : 5) rope_kernel(
     const int ax = p.axis ? p.axis[pr] : 0;
     // an axis beyond the positions' rows turns nothing
     const int pos = ax < p.n_axes ? p.pos[(long long)ax * p.T + t0 + t] : 0;
-    const float2 cs = cos_sin_turn(turn_per_position(p.freq[pr]), pos);
+    const float f = p.freq[pr];
+    float2 cs = cos_sin_turn(turn_per_position(f), pos);
+    if (ax < p.n_axes && (__float_as_uint(f) & 0x7F800000u) == 0x7F800000u) cs.x = cs.y = __uint_as_float(0x7FC00000u);
     sm_c[i] = cs.x;
     sm_s[i] = p.inverse ? -cs.y : cs.y;
   }
