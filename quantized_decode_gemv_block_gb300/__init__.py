@@ -403,8 +403,8 @@ def rope(q: torch.Tensor | None, k: torch.Tensor | None, pos: torch.Tensor, inv_
     T, _, D = ref.shape
     dtype = ref.dtype
     axes = pos.shape[0] if pos.dim() == 2 else 1
-    if axes > 1 and pos.shape[1] != T:
-        raise ValueError("pos of several axes must be (axes, tokens)")
+    if pos.dim() > 2 or (axes > 1 and pos.shape[1] != T):
+        raise ValueError("pos must be (tokens) or, of several axes, (axes, tokens)")
     pairs = inv_freq.numel()
     if pairs and (inv_freq.dtype is not torch.float32 or not inv_freq.is_contiguous()):
         raise ValueError("inv_freq must be contiguous fp32")
