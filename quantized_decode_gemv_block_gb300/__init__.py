@@ -396,10 +396,15 @@ def rope(q: torch.Tensor | None, k: torch.Tensor | None, pos: torch.Tensor, inv_
          q_out: torch.Tensor | None = None, k_out: torch.Tensor | None = None, stream=None):
     """Rotary positions on q and k (T, heads, head_dim; either may be None), through kq_rope. pos: int32 [T]
     or [axes, T]; inv_freq: fp32, one per pair (rot_dim = 2 * its length); pair_axis: uint8, one per pair.
-    inverse=True is the gradient of the call without it. Returns (q_out, k_out)."""
+    inverse=True is the gradient of the call without it, and what autograd calls for a q or k that requires one.
+    Returns (q_out, k_out)."""
     ref = k if q is None else q
     if ref is None:
         raise ValueError("one of q and k is needed")
+    if torch.is_grad_enabled() and (ref.requires_grad or (k is not None and k.requires_grad)):
+        if q_out is not None or k_out is not None:
+            raise ValueError("q_out and k_out take no q or k that requires a gradient")
+        return _Rope.apply(q, k, pos, inv_freq, pair_axis, adjacent, inverse, out_dtype, stream)
     T, _, D = ref.shape
     dtype = ref.dtype
     axes = pos.shape[0] if pos.dim() == 2 else 1
@@ -441,6 +446,29 @@ def rope(q: torch.Tensor | None, k: torch.Tensor | None, pos: torch.Tensor, inv_
     _check(lib().kq_rope(_dtype(dtype), _dtype(y_dtype), qp, qs, qop, qos, n_q, kp, ks, kop, kos, n_k, T, D, 2 * pairs,
                          inv_freq.data_ptr(), axis, _i32("pos", pos, axes * T), axes, flags, _stream(stream)))
     return q_out if q is not None else None, k_out if k is not None else None
+
+
+class _Rope(torch.autograd.Function):
+    """rope of tensors that require a gradient: the rotation back by the same angles, on the current stream."""
+
+    @staticmethod
+    def forward(ctx, q, k, pos, inv_freq, pair_axis, adjacent, inverse, out_dtype, stream):
+        ctx.set_materialize_grads(False)
+        ctx.save_for_backward(pos, inv_freq, pair_axis)
+        ctx.how = adjacent, not inverse, (k if q is None else q).dtype
+        outs = rope(q, k, pos, inv_freq, pair_axis, adjacent, inverse, out_dtype, stream=stream)
+        ctx.mark_non_differentiable(*(o for o, need in zip(outs, ctx.needs_input_grad) if o is not None and not need))
+        return outs
+
+    @staticmethod
+    def backward(ctx, gq, gk):
+        pos, inv_freq, pair_axis = ctx.saved_tensors
+        adjacent, inverse, dtype = ctx.how
+        # a gradient may be a view of any strides, an expanded one among them
+        gq, gk = (g.contiguous() if g is not None and need else None for g, need in zip((gq, gk), ctx.needs_input_grad))
+        if gq is not None or gk is not None:
+            gq, gk = rope(gq, gk, pos, inv_freq, pair_axis, adjacent, inverse, dtype)
+        return gq, gk, None, None, None, None, None, None, None
 
 
 def _rope_out(name, x, y, y_dtype) -> int:

@@ -18,3 +18,12 @@ def test_positions_of_more_than_two_dimensions_are_refused(kq, shape):
     x = torch.zeros((5, 2, 64), dtype=torch.bfloat16)
     with pytest.raises(ValueError, match="axes, tokens"):
         kq.rope(x, None, torch.zeros(shape, dtype=torch.int32), torch.zeros(32), pair_axis=torch.zeros(32, dtype=torch.uint8), stream=0)
+
+
+def test_given_outputs_and_gradients_do_not_go_together(kq):
+    x = torch.zeros((5, 2, 64), requires_grad=True)
+    pos, f = torch.zeros(5, dtype=torch.int32), torch.zeros(32)
+    with pytest.raises(ValueError, match="gradient"):
+        kq.rope(x, None, pos, f, q_out=torch.zeros_like(x), stream=0)
+    with pytest.raises(ValueError, match="gradient"):
+        kq.rope(x.detach(), x, pos, f, k_out=torch.zeros_like(x), stream=0)
