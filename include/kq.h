@@ -25,7 +25,8 @@
  * is overwritten, never accumulated. All pointers are DEVICE pointers unless a
  * function says otherwise. The caller owns every buffer; the library allocates
  * nothing per call. Its only state: a thread-local error string, per-device caches of
- * the SM count and of kernel attributes, the device error words read by
+ * the SM count and of kernel attributes (of none that a call's size changes, so host threads may
+ * call at once), thread-local caches of a kernel's occupancy, the device error words read by
  * kq_device_errors(), and the fixed scratch array of kq_decode_step_static.
  * Every call is asynchronous on `stream` (a cudaStream_t passed as void*, NULL =
  * the legacy default stream) and never synchronises. There is no CPU fallback:

@@ -510,7 +510,8 @@ class KV8Cache:
 
 
 def kv8_append(cache: KV8Cache, k: torch.Tensor, v: torch.Tensor, slot: torch.Tensor, stream=None) -> None:
-    """Quantize k and v (T, n_kv, head_dim) into their slots (int32 [T], -1 skips) through kq_kv8_append."""
+    """Quantize k and v (T, n_kv, head_dim) into their slots (int32 [T], -1 skips) through kq_kv8_append. Rows of one page
+    stand behind one another, with skipped rows between them at most."""
     if k.dtype != v.dtype or k.shape[0] != v.shape[0]:
         raise ValueError("k and v must agree in type and tokens")
     T, x_dtype = k.shape[0], _dtype(k.dtype)
@@ -531,7 +532,8 @@ def attention_kv8(q: torch.Tensor, cache: KV8Cache, block_table: torch.Tensor, c
                   out_dtype=None, workspace: torch.Tensor | None = None, stream=None) -> torch.Tensor:
     """Attention of the packed new tokens' q (T, n_q, head_dim) over the requests' pages (kq_attention_kv8).
     max_new, max_len, total_len (default B * max_len): bounds of new_len, of ctx_len + new_len and of its sum.
-    scale: default 1/sqrt(head_dim); mask: int32 [T] tree masks or None (causal). Returns (T, n_q, head_dim)."""
+    scale: default 1/sqrt(head_dim); mask: int32 [T] tree masks or None (causal). Returns (T, n_q, head_dim), which
+    carries no gradient."""
     T, n_q, D = q.shape
     B, width = block_table.shape
     if total_len is None:

@@ -12,8 +12,8 @@
 // and rounded to fp16: exact for bf16 values within 2^-28 of the row's largest. fp32 queries, and all of them where
 // the output is fp32, are split into fp16 hi + lo parts (QP = 2, 22 bits): rounded to one they would move a score by
 // 2^-12 of sum_d |scale q_d k_d|, and the weights by as much, which passes a bf16 output's 2^-9 from scores of 8 on. The
-// second part costs, with bf16 outputs, 84 -> 92 us for 16 requests x 8 tokens over 1000 to 9000 positions, 94 -> 105 for 64
-// tokens over 1 to 8191, 374 -> 435 for 2 x 2048 (32 / 8 heads of 128), 10.2 -> 11.2 for one token over 4096 (16 / 4 heads).
+// second part costs, with bf16 outputs, 84 -> 92 us for 16 requests x 8 tokens over 1000 to 9000 positions in pages of 32, 94 -> 105
+// for 64 tokens over 1 to 8191, 374 -> 435 for 2 x 2048 (32 / 8 heads of 128), 10.2 -> 11.2 for one token over 4096 (16 / 4 heads).
 // Weights are one fp16 part (2^-12 of themselves) for bf16 outputs, two (WP = 2) for fp32 ones. The weights that enter a product are those against the largest score of
 // their page (of up to 32 positions of it), up by 2^15: fp16 then holds weights down to 2^-29 of that in
 // full, and an absolute 2^-40 below. The accumulators take the page's share of the softmax and its v scale
@@ -52,13 +52,13 @@
 // warps that share the second product by dims, with a barrier per step, 177 us; each warp with items and a ring of
 // its own 112 to 132 us (its copies' and its items' bookkeeping weighed as much as its products); the fifth warp 100
 // us. Segments of 256 positions 115 us and of 1024 100 us; one token over 4096 positions 9.6, 10.4 and 14.4 us with
-// segments of 256, 512 and 1024. Few heads leave CTAs idle, so that short segments win: one token over 4096
+// segments of 256, 512 and 1024 (queries of one part). Few heads leave CTAs idle, so that short segments win: one token over 4096
 // positions, 16 / 2 heads, 8.7 us with segments of 256 (11.4 with 512); 63 tokens over 1030 to 2060, 2 / 1 heads of
 // 64, 12 us (20); the other side, 64 tokens over 1 to 8191, 8 / 2 heads, 36.7 (35.4), and with four heads 62 (57).
 //
 // Bound by DRAM for single tokens: 64 requests of 1 to 8191 positions, 32 / 8 heads of 128, 543 MB in
 // 98.4 us, 5.5 TB/s, of which 5 us are the join and about 10 the start and the end; four contexts of 128k
-// positions 167 us, 6.3 TB/s (of 6.79 copied). Windows and prompts are bound by the multiplying warps'
+// positions 168 us, 6.2 TB/s (of 6.79 copied). Windows and prompts are bound by the multiplying warps'
 // latency (two or three of them per scheduler): the conversions, the softmax and the products follow one
 // another in each, 92 us for 16 requests x 8 tokens x 4 heads per kv head of 128 over 1000 to 9000
 // positions, 178 MB, and 175 to 210 TFLOP/s for prompts.
