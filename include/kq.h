@@ -89,7 +89,8 @@ const char* kq_version(void);
 /* Reads and clears the device error word of the current device; synchronises the device.
  * Every wait inside a kernel is bounded: if one gives up, the kernel records bit 0 here,
  * skips the rest of its work (its output is then invalid) and returns instead of hanging.
- * Bit 1: a paged-cache kernel met lengths, slots or page ids outside the bounds it was given.
+ * Bit 1: a paged-cache kernel met lengths, slots or page ids outside the bounds it was given, or an
+ * experts' product a plan outside them.
  * Returns the bits (0 = nothing recorded) or KQ_ERR_CUDA if the word cannot be read. */
 int kq_device_errors(void);
 
@@ -472,6 +473,82 @@ int kq_attention_kv8(const kq_kv8_cache* cache, int q_dtype, const void* q, long
                      long long o_stride, int n_q, const int* ctx_len, const int* new_len, int B, int T, int max_new,
                      int max_len, long long total_len, const int* block_table, int max_blocks, const unsigned int* mask,
                      float scale, void* workspace, size_t ws_bytes, void* stream);
+
+/* ---- Norms around a residual sum ----
+ * What stands between two blocks of a decoder layer, in one pass over its rows:
+ *   z  = y, or with KQ_NORM_POST rms(y) * post         rms(v) = v / sqrt(mean v^2 + eps)
+ *   h' = h + scale * gate * z                          x = rms(h') * pre
+ *   y, gate    T rows of H (y_dtype), token strides in elements. gate NULL: ones; gate_stride 0: one row for all
+ *              tokens. y NULL: h' = h
+ *   h, h_out   T rows of H (h_dtype). h NULL: h' = scale * gate * z; h_out NULL: h' is not written
+ *   post, pre  H weights (w_dtype), NULL: ones; with KQ_NORM_UNIT_OFFSET a stored w stands for 1 + w
+ *   x          T rows of H (x_dtype); NULL: no second norm
+ * Sums and products are fp32; h' and x are rounded once each, x from the unrounded h'. A row's bits depend
+ * on that row alone. h_out may be h (same stride);
+ * h_out or x may be y (same type and stride). Outputs must not overlap inputs or each other otherwise.
+ * T <= 2^30, H in 1..32768. Errors: KQ_ERR_ARG, KQ_ERR_UNSUPPORTED, KQ_ERR_CUDA. */
+enum kq_norm_flags { KQ_NORM_POST = 1u, KQ_NORM_UNIT_OFFSET = 2u };
+int kq_residual_norm(int y_dtype, const void* y, long long y_stride, int h_dtype, const void* h, long long h_stride, void* h_out,
+                     long long h_out_stride, const void* gate, long long gate_stride, float scale, int w_dtype,
+                     const void* post, const void* pre, float eps, int x_dtype, void* x, long long x_stride, int T, int H,
+                     unsigned flags, void* stream);
+
+/* ---- Mixture of experts over block-quantized weights ----
+ * A layer whose feed-forward is E experts of which each token takes k: kq_moe_route chooses them from the
+ * router's logits, kq_moe_plan sorts the T * k pairs (token, choice) by expert, kq_moe_gate_up and
+ * kq_moe_down multiply each pair's row by its expert's matrices. Pair t * k + j is choice j of token t.
+ * Ids, the plan and the weights live in device memory and are read there, so a captured step can be
+ * replayed with other logits. Nothing here uses atomics on results. A padded batch gives its padding
+ * rows logits of -inf (or NaN): they get id -1, and no product touches them. */
+enum { KQ_MOE_MAX_EXPERTS = 1024, KQ_MOE_MAX_CHOICES = 32, KQ_MOE_MAX_K = 20480, KQ_MOE_MAX_PAIRS = 8388608 };
+
+/* The k experts of each token: s = softmax(logits), or with KQ_ROUTE_SIGMOID 1 / (1 + exp(-logit)); choices
+ * c = s + bias. With n_group > 1 the experts stand in n_group groups of consecutive ones, and only the
+ * top_group groups of the largest c (KQ_ROUTE_GROUP_TOP2: of the largest sum of the two largest c) stay.
+ * The k largest c are taken in falling order, ties to the lowest expert (or group).
+ *   logits   T rows of E, fp32 or bf16, `stride` elements apart. A logit of -inf or NaN, or a bias of -inf or
+ *            NaN, is an expert that cannot be chosen; +inf counts as the largest number
+ *   bias     E fp32 (device) or NULL; it takes part in the choice only
+ *   ids      T x k ints: the experts, or -1 where no more can be chosen
+ *   weights  T x k fp32: s of each choice, with KQ_ROUTE_RENORM divided by the sum over the token's choices
+ *            (0 where that is 0), times `scale`; 0 for id -1
+ * Choices are those of 64-bit scores; without a bias they follow the logits. k <= top_group * (E / n_group),
+ * n_group <= 32. One launch. Errors: KQ_ERR_ARG, KQ_ERR_UNSUPPORTED, KQ_ERR_CUDA. */
+enum kq_route_flags { KQ_ROUTE_SIGMOID = 1u, KQ_ROUTE_RENORM = 2u, KQ_ROUTE_GROUP_TOP2 = 4u };
+int kq_moe_route(int x_dtype, const void* logits, long long stride, int T, int E, int k, const float* bias, int n_group,
+                 int top_group, float scale, unsigned flags, int* ids, float* weights, void* stream);
+
+/* Pairs by expert: order[offsets[e] .. offsets[e+1]-1] are the pairs of expert e, in rising order; pairs whose
+ * id is outside 0..E-1 stand in none, and order is -1 from offsets[E] on.
+ *   ids T x k ints; offsets E+1 ints, order T * k ints (outputs). One launch. Errors: KQ_ERR_ARG, KQ_ERR_CUDA. */
+int kq_moe_plan(const int* ids, int T, int k, int E, int* offsets, int* order, void* stream);
+
+/* act[t k + j] = silu(g) * u for every pair of the plan, [g u] = W_e x[t] with its expert's matrix.
+ *   w        E matrices of 2 F x K weights, rows gate then up, one behind another, as for kq_gemv (16-byte aligned)
+ *   x        T rows of K bf16, x_stride elements apart (a multiple of 8), 16-byte aligned
+ *   offsets, order  from kq_moe_plan
+ *   act      T * k rows of F bf16, 16-byte aligned (output); rows of pairs outside the plan stay as they are
+ *   workspace  kq_moe_gate_up_workspace_size() bytes, 256-byte aligned (NULL where that is 0)
+ * Products and sums as kq_gemv's (fp32, exact products), g and u are not rounded before silu.
+ * A pair's bits depend on its row and expert alone. K is a multiple of 256 up to 20480. Q6_K needs
+ * E * 2F * row bytes to be a multiple of 16. A plan outside its bounds (offsets that fall or pass T * k, pairs outside
+ * 0..T*k-1) sets bit 1 of kq_device_errors(), and the experts or pairs concerned are not computed.
+ * Errors: KQ_ERR_ARG, KQ_ERR_UNSUPPORTED, KQ_ERR_WORKSPACE, KQ_ERR_CUDA. */
+size_t kq_moe_gate_up_workspace_size(int fmt, int T, int k, int E, int F, int K);
+int kq_moe_gate_up(int fmt, const void* w, const void* x, long long x_stride, const int* offsets, const int* order, int T,
+                   int k, int E, int F, int K, void* act, void* workspace, size_t ws_bytes, void* stream);
+
+/* y[t] = add[t] + sum_j weights[t][j] * W_e act[t k + j] over the token's choices with an id in 0..E-1, j in order.
+ *   w        E matrices of H x K weights, one behind another; act: T * k rows of K bf16, 16-byte aligned
+ *   ids, weights  T x k, as kq_moe_route gives them, and the plan made of these ids
+ *   add      T rows of H fp32, add_stride elements apart (a shared expert's output, the residual), or NULL
+ *   y        T rows of H (y_dtype), y_stride elements apart; may be add (same stride, fp32)
+ *   workspace  kq_moe_down_workspace_size() bytes, 256-byte aligned
+ * The sum over choices is fp32, in order. Otherwise as kq_moe_gate_up. */
+size_t kq_moe_down_workspace_size(int fmt, int T, int k, int E, int H, int K);
+int kq_moe_down(int fmt, const void* w, const void* act, const int* offsets, const int* order, const int* ids,
+                const float* weights, int T, int k, int E, int H, int K, const float* add, long long add_stride, int y_dtype,
+                void* y, long long y_stride, void* workspace, size_t ws_bytes, void* stream);
 
 #ifdef __cplusplus
 }

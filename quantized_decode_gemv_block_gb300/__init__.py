@@ -112,6 +112,19 @@ def load_library(path: str = LIB_PATH):
     L.kq_attention_kv8_workspace_size.restype = SZ
     L.kq_attention_kv8.argtypes = [P, I, P, LL, I, P, LL, I, P, P, I, I, I, I, LL, P, I, P, F, P, SZ, P]
     L.kq_attention_kv8.restype = I
+    L.kq_residual_norm.argtypes = [I, P, LL, I, P, LL, P, LL, P, LL, F, I, P, P, F, I, P, LL, I, I, U, P]
+    L.kq_residual_norm.restype = I
+    L.kq_moe_route.argtypes = [I, P, LL, I, I, I, P, I, I, F, U, P, P, P]
+    L.kq_moe_route.restype = I
+    L.kq_moe_plan.argtypes = [P, I, I, I, P, P, P]
+    L.kq_moe_plan.restype = I
+    for name in ("kq_moe_gate_up_workspace_size", "kq_moe_down_workspace_size"):
+        getattr(L, name).argtypes = [I, I, I, I, I, I]
+        getattr(L, name).restype = SZ
+    L.kq_moe_gate_up.argtypes = [I, P, P, LL, P, P, I, I, I, I, I, P, P, SZ, P]
+    L.kq_moe_gate_up.restype = I
+    L.kq_moe_down.argtypes = [I, P, P, P, P, P, P, I, I, I, I, I, P, LL, I, P, LL, P, SZ, P]
+    L.kq_moe_down.restype = I
     _lib = L
     return L
 
@@ -559,6 +572,245 @@ def attention_kv8(q: torch.Tensor, cache: KV8Cache, block_table: torch.Tensor, c
                                   D ** -0.5 if scale is None else scale, workspace.data_ptr(),
                                   workspace.nbytes, _stream(stream)))
     return out
+
+
+# ---- Norms around a residual sum, and mixture of experts ----
+
+KQ_NORM_POST, KQ_NORM_UNIT_OFFSET = 1, 2
+KQ_ROUTE_SIGMOID, KQ_ROUTE_RENORM, KQ_ROUTE_GROUP_TOP2 = 1, 2, 4
+_SCORES = {"softmax": 0, "sigmoid": KQ_ROUTE_SIGMOID}
+_GROUP_SCORES = {"max": 0, "top2": KQ_ROUTE_GROUP_TOP2}
+
+
+def _here(name: str, t: torch.Tensor) -> int:
+    """The address of a tensor that a kernel of the current device reads or writes and that takes no gradient."""
+    if not t.is_cuda:
+        _not_on_gpu(name)
+    elif t.device.index != torch._C._cuda_getDevice():
+        raise ValueError(f"{name} must be on the current device")
+    if t.requires_grad and torch.is_grad_enabled():
+        raise ValueError(f"{name} requires a gradient, which this operator does not give")
+    return t.data_ptr()
+
+
+def _rows(name: str, t: torch.Tensor, T: int, H: int) -> int:
+    """The token stride of a (T, H) tensor of contiguous rows."""
+    if t.dim() != 2 or t.shape[0] != T or t.shape[1] != H or (H > 1 and t.stride(1) != 1):
+        raise ValueError(f"{name} must be ({T}, {H}) with contiguous rows")
+    s = t.stride(0)
+    return s if T > 1 and s > 0 else H if T <= 1 else _overlap(name)
+
+
+def _overlap(name: str):
+    raise ValueError(f"{name} must have a row of its own for every token")
+
+
+def _flat(name: str, t: torch.Tensor, dtype, shape) -> int:
+    """The address of a contiguous tensor of this type and shape."""
+    if t.dtype is not dtype or tuple(t.shape) != tuple(shape) or not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous {dtype} of shape {tuple(shape)}")
+    return _here(name, t)
+
+
+def residual_norm(h: torch.Tensor | None, y: torch.Tensor | None, post=None, gate: torch.Tensor | None = None, scale: float = 1.0,
+                  pre=None, eps: float = 1e-6, unit_offset: bool = False, x_dtype=None, h_out: torch.Tensor | None = None,
+                  x_out: torch.Tensor | None = None, stream=None):
+    """h' = h + scale * gate * rms(y) * post and x = rms(h') * pre in one pass (kq_residual_norm). h, y: (T, H), either may be
+    None; post, pre: H weights, True for a norm without weights, None for no norm; gate: (H) or (T, H) of y's type or None.
+    unit_offset: a stored weight stands for 1 + w. h_out and x_out are made where they are not given (h' in h's type, x in
+    x_dtype, bf16 by default); h_out may be h. Returns (h', x), x None without pre. Carries no gradient."""
+    ref = h if y is None else y
+    if ref is None:
+        raise ValueError("one of h and y is needed")
+    if ref.dim() != 2:
+        raise ValueError("h and y must be (tokens, H)")
+    T, H = ref.shape
+    h_dtype = (ref if h is None else h).dtype
+    y_dtype = ref.dtype
+    flags = KQ_NORM_UNIT_OFFSET if unit_offset else 0
+    yp = ys = hp = hs = gp = gs = xp = xs = 0
+    if y is not None:
+        yp, ys = _here("y", y), _rows("y", y, T, H)
+    if h is not None:
+        hp, hs = _here("h", h), _rows("h", h, T, H)
+    if gate is not None:
+        if gate.dtype is not y_dtype:
+            raise ValueError("gate must have y's type")
+        gp = _here("gate", gate)
+        if gate.dim() == 1:
+            if gate.shape[0] != H or (H > 1 and gate.stride(0) != 1):
+                raise ValueError("gate must be (H) or (T, H) with contiguous rows")
+        else:
+            gs = _rows("gate", gate, T, H)
+    w, w_dtype = [0, 0], F32
+    for i, (name, t) in enumerate((("post", post), ("pre", pre))):
+        if isinstance(t, torch.Tensor):
+            if t.dim() != 1 or t.shape[0] != H or not t.is_contiguous():
+                raise ValueError(f"{name} must be {H} contiguous weights")
+            if w[0] and t.dtype is not post.dtype:
+                raise ValueError("post and pre must agree in type")
+            w[i], w_dtype = _here(name, t), _dtype(t.dtype)
+    if post is not None and post is not False:
+        flags |= KQ_NORM_POST
+    if h_out is None:
+        h_out, hos = _empty((T, H), h_dtype, ref.device, stream), H
+        hop = h_out.data_ptr()
+    else:
+        if h_out.dtype is not h_dtype and h is not None:
+            raise ValueError("h_out must have h's type")
+        h_dtype = h_out.dtype
+        hop, hos = _here("h_out", h_out), _rows("h_out", h_out, T, H)
+    if pre is not None and pre is not False:
+        if x_out is None:
+            x_out, xs = _empty((T, H), x_dtype or torch.bfloat16, ref.device, stream), H
+            xp = x_out.data_ptr()
+        else:
+            if x_dtype is not None and x_out.dtype is not x_dtype:
+                raise ValueError("x_out must have x_dtype")
+            xp, xs = _here("x_out", x_out), _rows("x_out", x_out, T, H)
+    elif x_out is not None:
+        raise ValueError("x_out without pre")
+    _check(lib().kq_residual_norm(_dtype(y_dtype), yp, ys, _dtype(h_dtype), hp, hs, hop, hos, gp, gs, scale, w_dtype, w[0], w[1],
+                                  eps, _dtype(x_out.dtype) if xp else F32, xp, xs, T, H, flags, _stream(stream)))
+    return h_out, x_out
+
+
+def moe_route(logits: torch.Tensor, k: int, score: str = "softmax", bias: torch.Tensor | None = None, n_group: int = 1,
+              top_group: int = 1, group_score: str = "max", renorm: bool = True, scale: float = 1.0, ids: torch.Tensor | None = None,
+              weights: torch.Tensor | None = None, stream=None):
+    """The k experts of each token from the router's logits (T, E), fp32 or bf16 (kq_moe_route). score: "softmax" or
+    "sigmoid"; bias: E fp32, for the choice only; group_score: "max" or "top2". Returns (ids int32 [T, k], -1 where no expert
+    can be chosen, weights fp32 [T, k]). Carries no gradient."""
+    if logits.dim() != 2:
+        raise ValueError("logits must be (tokens, experts)")
+    T, E = logits.shape
+    if score not in _SCORES or group_score not in _GROUP_SCORES:
+        raise ValueError("score must be softmax or sigmoid, group_score max or top2")
+    xp, xs = _here("logits", logits), _rows("logits", logits, T, E)
+    bp = 0 if bias is None else _flat("bias", bias, torch.float32, (E,))
+    n = (T, max(k, 0))
+    if ids is None:
+        ids = _empty(n, torch.int32, logits.device, stream)
+        ip = ids.data_ptr()
+    else:
+        ip = _flat("ids", ids, _I32, n)
+    if weights is None:
+        weights = _empty(n, torch.float32, logits.device, stream)
+        wp = weights.data_ptr()
+    else:
+        wp = _flat("weights", weights, torch.float32, n)
+    flags = _SCORES[score] | _GROUP_SCORES[group_score] | (KQ_ROUTE_RENORM if renorm else 0)
+    _check(lib().kq_moe_route(_dtype(logits.dtype), xp, xs, T, E, k, bp, n_group, top_group, scale, flags, ip, wp, _stream(stream)))
+    return ids, weights
+
+
+class MoePlan:
+    """The pairs (token, choice) by expert: offsets [E+1] and order [T*k], int32 device tensors."""
+    __slots__ = ("offsets", "order")
+
+    def __init__(self, offsets: torch.Tensor, order: torch.Tensor):
+        for name, t in (("offsets", offsets), ("order", order)):
+            if t.dtype is not _I32 or t.dim() != 1 or not t.is_contiguous():
+                raise ValueError(f"{name} must be contiguous int32 of one dimension")
+        if offsets.shape[0] < 2:
+            raise ValueError("offsets must hold one expert more than there are")
+        self.offsets, self.order = offsets, order
+
+
+def moe_plan(ids: torch.Tensor, n_experts: int, out: MoePlan | None = None, stream=None) -> MoePlan:
+    """The plan of the experts' products from the ids (T, k) that moe_route gives (kq_moe_plan)."""
+    if ids.dim() != 2:
+        raise ValueError("ids must be (tokens, choices)")
+    T, k = ids.shape
+    ip = _flat("ids", ids, _I32, (T, k))
+    if out is None:
+        out = MoePlan(_empty(max(n_experts, 1) + 1, _I32, ids.device, stream), _empty(T * k, _I32, ids.device, stream))
+        fp, op = out.offsets.data_ptr(), out.order.data_ptr()
+    else:
+        fp, op = _flat("out.offsets", out.offsets, _I32, (n_experts + 1,)), _flat("out.order", out.order, _I32, (T * k,))
+    _check(lib().kq_moe_plan(ip, T, k, n_experts, fp, op, _stream(stream)))
+    return out
+
+
+def moe_gate_up_workspace_size(fmt, T: int, k: int, E: int, F: int, K: int) -> int:
+    return lib().kq_moe_gate_up_workspace_size(_fmt(fmt), T, k, E, F, K)
+
+
+def moe_down_workspace_size(fmt, T: int, k: int, E: int, H: int, K: int) -> int:
+    return lib().kq_moe_down_workspace_size(_fmt(fmt), T, k, E, H, K)
+
+
+def _experts(w: torch.Tensor, plan: MoePlan, rows: int, fmt: int, K: int):
+    """The address of the experts' blocks, their number, and the addresses of the plan."""
+    E = plan.offsets.shape[0] - 1
+    if w.dtype is not torch.uint8 or not w.is_contiguous() or w.numel() != E * rows * lib().kq_row_bytes(fmt, K):
+        raise ValueError(f"w must be the contiguous uint8 blocks of {E} matrices of {rows} x {K} weights")
+    return _here("w", w), E, _here("plan.offsets", plan.offsets), _here("plan.order", plan.order)
+
+
+def _workspace(workspace: torch.Tensor | None, need: int, device, stream):
+    if workspace is None:
+        workspace = _empty(need, torch.uint8, device, stream) if need else None
+    elif not workspace.is_contiguous():
+        raise ValueError("workspace must be contiguous")
+    return (workspace, _here("workspace", workspace), workspace.nbytes) if workspace is not None else (None, 0, 0)
+
+
+def moe_gate_up(fmt, w: torch.Tensor, x: torch.Tensor, plan: MoePlan, F: int, K: int, act: torch.Tensor | None = None,
+                workspace: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """act[t*k+j] = silu(g) * u with [g u] = W_e x[t] for every pair of the plan (kq_moe_gate_up). w: uint8 blocks of E matrices
+    of 2F x K, x: (T, K) bf16, act: (T*k, F) bf16, whose rows of pairs without an expert stay as they are (where it is made here:
+    undefined). Carries no gradient."""
+    fmt = _fmt(fmt)
+    if x.dim() != 2 or x.dtype is not torch.bfloat16:
+        raise ValueError("x must be (tokens, K) bf16")
+    T = x.shape[0]
+    wp, E, fp, op = _experts(w, plan, 2 * F, fmt, K)
+    xp, xs = _here("x", x), _rows("x", x, T, K)
+    n = plan.order.shape[0]
+    if n % T if T else n:
+        raise ValueError("the plan must hold a number of choices for each of x's tokens")
+    k = n // T if T else 1
+    if act is None:
+        act = _empty((n, F), torch.bfloat16, x.device, stream)
+        ap = act.data_ptr()
+    else:
+        ap = _flat("act", act, torch.bfloat16, (n, F))
+    ws, wsp, wsn = _workspace(workspace, moe_gate_up_workspace_size(fmt, T, k, E, F, K) if workspace is None else 0, x.device, stream)
+    _check(lib().kq_moe_gate_up(fmt, wp, xp, xs, fp, op, T, k, E, F, K, ap, wsp, wsn, _stream(stream)))
+    return act
+
+
+def moe_down(fmt, w: torch.Tensor, act: torch.Tensor, plan: MoePlan, ids: torch.Tensor, weights: torch.Tensor, H: int, K: int,
+             add: torch.Tensor | None = None, out_dtype=None, y: torch.Tensor | None = None, workspace: torch.Tensor | None = None,
+             stream=None) -> torch.Tensor:
+    """y[t] = add[t] + sum_j weights[t, j] * W_e act[t*k+j] over the token's choices (kq_moe_down). w: uint8 blocks of E matrices
+    of H x K, act: (T*k, K) bf16, ids and weights (T, k) as moe_route gives them, add: (T, H) fp32 or None, y: (T, H) in out_dtype
+    (fp32 by default), may be add. Carries no gradient."""
+    fmt = _fmt(fmt)
+    if ids.dim() != 2:
+        raise ValueError("ids must be (tokens, choices)")
+    T, k = ids.shape
+    wp, E, fp, op = _experts(w, plan, H, fmt, K)
+    if plan.order.shape[0] != T * k:
+        raise ValueError("the plan must be that of the ids")
+    ap = _flat("act", act, torch.bfloat16, (T * k, K))
+    ip, tp = _flat("ids", ids, _I32, (T, k)), _flat("weights", weights, torch.float32, (T, k))
+    dp = ds = 0
+    if add is not None:
+        if add.dtype is not torch.float32:
+            raise ValueError("add must be fp32")
+        dp, ds = _here("add", add), _rows("add", add, T, H)
+    if y is None:
+        y, ys = _empty((T, H), out_dtype or torch.float32, act.device, stream), H
+        yp = y.data_ptr()
+    else:
+        if out_dtype is not None and y.dtype is not out_dtype:
+            raise ValueError("y must have out_dtype")
+        yp, ys = _here("y", y), _rows("y", y, T, H)
+    ws, wsp, wsn = _workspace(workspace, moe_down_workspace_size(fmt, T, k, E, H, K) if workspace is None else 0, act.device, stream)
+    _check(lib().kq_moe_down(fmt, wp, ap, fp, op, ip, tp, T, k, E, H, K, dp, ds, _dtype(y.dtype), yp, ys, wsp, wsn, _stream(stream)))
+    return y
 
 
 class KVCacheC(ctypes.Structure):

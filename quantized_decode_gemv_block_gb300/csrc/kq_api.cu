@@ -151,7 +151,9 @@ int kq_device_errors(void) {
   if (vt == 0xFFFFFFFFu) return fail(KQ_ERR_CUDA, "reading the prefill error word");
   const unsigned int vk = kq::take_kv8_errors(), va = kq::take_kv8_append_errors();
   if (vk == 0xFFFFFFFFu || va == 0xFFFFFFFFu) return fail(KQ_ERR_CUDA, "reading the paged cache's error words");
-  v |= vt | vk | va;
+  const unsigned int vm = kq::take_moe_errors();
+  if (vm == 0xFFFFFFFFu) return fail(KQ_ERR_CUDA, "reading the experts' error word");
+  v |= vt | vk | va | vm;
   ok();
   return static_cast<int>(v & 0x7FFFFFFFu);
 }
@@ -704,6 +706,180 @@ int kq_attention_kv8(const kq_kv8_cache* cache, int q_dtype, const void* q, long
     kq::AttnKV8Args a = {q_dtype, o_dtype, q, q_stride, o, o_stride, B, T, max_new, max_len, total_len, ctx_len, new_len,
                          block_table, max_blocks, n_q, reinterpret_cast<const uint32_t*>(mask), scale, workspace};
     if (kq::launch_attention_kv8(c, a, sms, static_cast<cudaStream_t>(stream), &err) != 0) return fail(KQ_ERR_CUDA, err);
+    return ok();
+  });
+}
+
+// ---- Norms around a residual sum ----
+
+int kq_residual_norm(int y_dtype, const void* y, long long y_stride, int h_dtype, const void* h, long long h_stride, void* h_out,
+                     long long h_out_stride, const void* gate, long long gate_stride, float scale, int w_dtype,
+                     const void* post, const void* pre, float eps, int x_dtype, void* x, long long x_stride, int T, int H,
+                     unsigned flags, void* stream) {
+  return guarded([&] {
+    if (!dtype_known(y_dtype) || !dtype_known(h_dtype) || !dtype_known(w_dtype) || !dtype_known(x_dtype))
+      return fail(KQ_ERR_UNSUPPORTED, "y_dtype, h_dtype, w_dtype and x_dtype must be KQ_F32 or KQ_BF16");
+    if (flags & ~(unsigned)(KQ_NORM_POST | KQ_NORM_UNIT_OFFSET)) return fail(KQ_ERR_ARG, "unknown flag bits " + std::to_string(flags));
+    if (T < 0 || T > kMaxItems) return fail(KQ_ERR_ARG, "T must be in 0..2^30");
+    if (H < 1 || H > 32768) return fail(KQ_ERR_ARG, "H must be in 1..32768");
+    if (T == 0) return ok();
+    if (!y && !h) return fail(KQ_ERR_ARG, "y and h are both NULL");
+    if (!y && (gate || post || (flags & KQ_NORM_POST))) return fail(KQ_ERR_ARG, "gate and post belong to y, which is NULL");
+    if (post && !(flags & KQ_NORM_POST)) return fail(KQ_ERR_ARG, "post without KQ_NORM_POST");
+    if (pre && !x) return fail(KQ_ERR_ARG, "pre without x");
+    if (!h_out && !x) return fail(KQ_ERR_ARG, "h_out and x are both NULL");
+    if ((y && y_stride < H) || (h && h_stride < H) || (h_out && h_out_stride < H) || (x && x_stride < H) ||
+        (gate && gate_stride != 0 && gate_stride < H))
+      return fail(KQ_ERR_ARG, "a token stride is shorter than a row");
+    const uintptr_t ya = y_dtype == KQ_F32 ? 4 : 2, ha = h_dtype == KQ_F32 ? 4 : 2, wa = w_dtype == KQ_F32 ? 4 : 2;
+    if (!aligned(y, ya) || !aligned(gate, ya) || !aligned(h, ha) || !aligned(h_out, ha) || !aligned(post, wa) || !aligned(pre, wa) ||
+        !aligned(x, x_dtype == KQ_F32 ? 4 : 2))
+      return fail(KQ_ERR_ARG, "a pointer is not aligned to its element");
+    if (h && h == h_out && h_stride != h_out_stride) return fail(KQ_ERR_ARG, "in place needs the same stride on both sides");
+    if ((x && x == h) || (h_out && h_out == y && (h_dtype != y_dtype || h_out_stride != y_stride)) || (x && x == h_out) ||
+        (x && x == y && (x_dtype != y_dtype || x_stride != y_stride)))
+      return fail(KQ_ERR_ARG, "x and h_out may take y's place at its type and stride, and h_out h's; x not h's or h_out's");
+    const kq::ResidualNormArgs a = {y_dtype, h_dtype, w_dtype, x_dtype, y, y_stride, h, h_stride, h_out, h_out_stride, x, x_stride,
+                                    gate, gate_stride, post, pre, scale, eps, T, H,
+                                    (flags & KQ_NORM_POST) != 0, (flags & KQ_NORM_UNIT_OFFSET) != 0};
+    std::string err;
+    if (kq::launch_residual_norm(a, static_cast<cudaStream_t>(stream), &err) != 0) return fail(KQ_ERR_CUDA, err);
+    return ok();
+  });
+}
+
+// ---- Mixture of experts ----
+
+static bool moe_sizes_ok(int T, int k, int E) {
+  return T >= 0 && E >= 1 && E <= KQ_MOE_MAX_EXPERTS && k >= 1 && k <= KQ_MOE_MAX_CHOICES && (long long)T * k <= KQ_MOE_MAX_PAIRS;
+}
+static const char* const kMoeSizes = "E must be in 1..1024, k in 1..32 and T * k up to 2^23";
+
+int kq_moe_route(int x_dtype, const void* logits, long long stride, int T, int E, int k, const float* bias, int n_group, int top_group,
+                 float scale, unsigned flags, int* ids, float* weights, void* stream) {
+  return guarded([&] {
+    if (!dtype_known(x_dtype)) return fail(KQ_ERR_UNSUPPORTED, "x_dtype must be KQ_F32 or KQ_BF16");
+    if (flags & ~(unsigned)(KQ_ROUTE_SIGMOID | KQ_ROUTE_RENORM | KQ_ROUTE_GROUP_TOP2))
+      return fail(KQ_ERR_ARG, "unknown flag bits " + std::to_string(flags));
+    if (!moe_sizes_ok(T, k, E)) return fail(KQ_ERR_ARG, kMoeSizes);
+    if (n_group < 1 || n_group > 32 || E % n_group || top_group < 1 || top_group > n_group)
+      return fail(KQ_ERR_ARG, "n_group must be in 1..32 and divide E, and top_group be in 1..n_group");
+    if (k > E / n_group * top_group) return fail(KQ_ERR_ARG, "k is more than the experts of top_group groups");
+    if (stride < E) return fail(KQ_ERR_ARG, "stride is shorter than a token's logits");
+    if (T == 0) return ok();
+    if (!logits || !ids || !weights) return fail(KQ_ERR_ARG, "logits, ids or weights is NULL");
+    if (!aligned(logits, x_dtype == KQ_F32 ? 4 : 2) || !aligned(bias, 4) || !aligned(ids, 4) || !aligned(weights, 4))
+      return fail(KQ_ERR_ARG, "a pointer is not aligned to its element");
+    const kq::MoeRouteArgs a = {x_dtype, logits, stride, T, E, k, bias, n_group, top_group, !(flags & KQ_ROUTE_SIGMOID),
+                                (flags & KQ_ROUTE_GROUP_TOP2) != 0, (flags & KQ_ROUTE_RENORM) != 0, scale, ids, weights};
+    std::string err;
+    if (kq::launch_moe_route(a, static_cast<cudaStream_t>(stream), &err) != 0) return fail(KQ_ERR_CUDA, err);
+    return ok();
+  });
+}
+
+int kq_moe_plan(const int* ids, int T, int k, int E, int* offsets, int* order, void* stream) {
+  return guarded([&] {
+    if (!moe_sizes_ok(T, k, E)) return fail(KQ_ERR_ARG, kMoeSizes);
+    if (!offsets || (T > 0 && (!ids || !order))) return fail(KQ_ERR_ARG, "ids, offsets or order is NULL");
+    if (!aligned(ids, 4) || !aligned(offsets, 4) || !aligned(order, 4)) return fail(KQ_ERR_ARG, "arrays must be 4-byte aligned");
+    std::string err;
+    if (kq::launch_moe_plan(ids, (long long)T * k, E, offsets, order, static_cast<cudaStream_t>(stream), &err) != 0)
+      return fail(KQ_ERR_CUDA, err);
+    return ok();
+  });
+}
+
+// Sizes of both products: N is F of a gate | up matrix (2 F rows), H of a down matrix.
+static bool moe_gemm_ok(int fmt, int T, int k, int E, int N, int K, bool gate_up) {
+  return fmt_known(fmt) && moe_sizes_ok(T, k, E) && N >= 1 && N <= (1 << 20) && K >= 256 && K % 256 == 0 && K <= KQ_MOE_MAX_K &&
+         (long long)E * N * (gate_up ? 2 : 1) <= 0x7FFFFFFFLL;
+}
+
+size_t kq_moe_gate_up_workspace_size(int fmt, int T, int k, int E, int F, int K) {
+  return moe_gemm_ok(fmt, T, k, E, F, K, true) ? kq::moe_gate_up_workspace(fmt, T, k, E, F, K) : 0;
+}
+size_t kq_moe_down_workspace_size(int fmt, int T, int k, int E, int H, int K) {
+  return moe_gemm_ok(fmt, T, k, E, H, K, false) ? kq::moe_down_workspace(fmt, T, k, E, H, K) : 0;
+}
+
+// Checks shared by the products; *a gets what they share.
+static int moe_gemm_check(int fmt, const void* w, const void* x, long long xs, const int* offsets, const int* order, int T, int k,
+                          int E, int N, int K, bool gate_up, const void* ws, size_t ws_bytes, size_t need, kq::MoeGemmArgs* a) {
+  if (!fmt_known(fmt)) return fail(KQ_ERR_UNSUPPORTED, "unknown block format " + std::to_string(fmt));
+  if (!moe_gemm_ok(fmt, T, k, E, N, K, gate_up))
+    return fail(KQ_ERR_ARG, std::string(kMoeSizes) + "; K a multiple of 256 up to 20480; an expert's rows 1..2^20, all rows below 2^31");
+  if (xs < K || xs % 8) return fail(KQ_ERR_ARG, "a row stride must be a multiple of 8 that holds K values");
+  if (T == 0) return KQ_OK;
+  if (!w || !x || !offsets || !order) return fail(KQ_ERR_ARG, "w, the activations, offsets or order is NULL");
+  if (!aligned(w, 16) || !aligned(x, 16) || !aligned(offsets, 4) || !aligned(order, 4))
+    return fail(KQ_ERR_ARG, "w and the activations must be 16-byte, offsets and order 4-byte aligned");
+  if (fmt == KQ_Q6_K && (long long)E * N * (gate_up ? 2 : 1) * (long long)kq_row_bytes(fmt, K) % 16)
+    return fail(KQ_ERR_UNSUPPORTED, "Q6_K experts whose bytes are no multiple of 16");
+  if (need && (!ws || ws_bytes < need || !aligned(ws, 256)))
+    return fail(KQ_ERR_WORKSPACE, "workspace must be >= " + std::to_string(need) + " bytes, 256-byte aligned");
+  *a = {};
+  a->fmt = fmt;
+  a->w = w;
+  a->x = x;
+  a->xs = xs;
+  a->offsets = offsets;
+  a->order = order;
+  a->T = T;
+  a->k = k;
+  a->E = E;
+  a->N = N;
+  a->K = K;
+  return KQ_OK;
+}
+
+int kq_moe_gate_up(int fmt, const void* w, const void* x, long long x_stride, const int* offsets, const int* order, int T, int k, int E,
+                   int F, int K, void* act, void* workspace, size_t ws_bytes, void* stream) {
+  return guarded([&] {
+    kq::MoeGemmArgs a;
+    const int rc = moe_gemm_check(fmt, w, x, x_stride, offsets, order, T, k, E, F, K, true, workspace, ws_bytes,
+                                  kq_moe_gate_up_workspace_size(fmt, T, k, E, F, K), &a);
+    if (rc != KQ_OK) return rc;
+    if (T == 0) return ok();
+    if (!act || !aligned(act, 16)) return fail(KQ_ERR_ARG, "act is NULL or not 16-byte aligned");
+    a.act = act;
+    a.ws = workspace;
+    std::string err;
+    const int sms = sm_count(&err);
+    if (sms < 0) return fail(KQ_ERR_CUDA, err);
+    if (kq::launch_moe_gate_up(a, sms, static_cast<cudaStream_t>(stream), &err) != 0) return fail(KQ_ERR_CUDA, err);
+    return ok();
+  });
+}
+
+int kq_moe_down(int fmt, const void* w, const void* act, const int* offsets, const int* order, const int* ids, const float* weights,
+                int T, int k, int E, int H, int K, const float* add, long long add_stride, int y_dtype, void* y, long long y_stride,
+                void* workspace, size_t ws_bytes, void* stream) {
+  return guarded([&] {
+    if (!dtype_known(y_dtype)) return fail(KQ_ERR_UNSUPPORTED, "y_dtype must be KQ_F32 or KQ_BF16");
+    kq::MoeGemmArgs a;
+    const int rc = moe_gemm_check(fmt, w, act, K, offsets, order, T, k, E, H, K, false, workspace, ws_bytes,
+                                  kq_moe_down_workspace_size(fmt, T, k, E, H, K), &a);
+    if (rc != KQ_OK) return rc;
+    if (y_stride < H || (add && add_stride < H)) return fail(KQ_ERR_ARG, "a token stride is shorter than a row");
+    if (T == 0) return ok();
+    if (!y || !ids || !weights) return fail(KQ_ERR_ARG, "y, ids or weights is NULL");
+    if (!aligned(y, y_dtype == KQ_F32 ? 4 : 2) || !aligned(add, 4) || !aligned(ids, 4) || !aligned(weights, 4))
+      return fail(KQ_ERR_ARG, "a pointer is not aligned to its element");
+    if (add && (const void*)add == y && (y_dtype != KQ_F32 || add_stride != y_stride))
+      return fail(KQ_ERR_ARG, "in place needs an fp32 y of add's stride");
+    a.ids = ids;
+    a.weights = weights;
+    a.add = add;
+    a.add_stride = add_stride;
+    a.y_dtype = y_dtype;
+    a.y = y;
+    a.y_stride = y_stride;
+    a.ws = workspace;
+    std::string err;
+    const int sms = sm_count(&err);
+    if (sms < 0) return fail(KQ_ERR_CUDA, err);
+    if (kq::launch_moe_down(a, sms, static_cast<cudaStream_t>(stream), &err) != 0) return fail(KQ_ERR_CUDA, err);
     return ok();
   });
 }

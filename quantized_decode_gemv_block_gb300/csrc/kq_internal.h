@@ -170,6 +170,66 @@ size_t attention_kv8_workspace(int B, long long total_len, int max_new, int n_q,
 int launch_attention_kv8(const KV8Args& c, const AttnKV8Args& a, int num_sms, cudaStream_t s, std::string* err);
 unsigned int take_kv8_errors();
 
+// Norms around a residual sum (residual_norm.cu).
+struct ResidualNormArgs {
+  int y_dtype, h_dtype, w_dtype, x_dtype;
+  const void* y;
+  long long ys;
+  const void* h;
+  long long hs;
+  void* h_out;
+  long long hos;
+  void* x;
+  long long xs;
+  const void* gate;
+  long long gs;  // 0: one row for all tokens
+  const void *post, *pre;
+  float scale, eps;
+  int T, H;
+  bool norm_y, offset;
+};
+int launch_residual_norm(const ResidualNormArgs& a, cudaStream_t s, std::string* err);
+
+// Mixture of experts: routing and the plan (moe_route.cu), the experts' products (moe_gemm.cu).
+struct MoeRouteArgs {
+  int x_dtype;
+  const void* x;
+  long long xs;
+  int T, E, k;
+  const float* bias;
+  int n_group, top_group;
+  bool softmax, two, renorm;
+  float scale;
+  int* ids;
+  float* weights;
+};
+int launch_moe_route(const MoeRouteArgs& a, cudaStream_t s, std::string* err);
+int launch_moe_plan(const int* ids, long long n, int E, int* offsets, int* order, cudaStream_t s, std::string* err);
+
+struct MoeGemmArgs {
+  int fmt;
+  const void* w;
+  const void* x;  // bf16 rows
+  long long xs;
+  const int *offsets, *order;
+  int T, k, E, N, K;  // N: ffn of a gate | up matrix, hidden of a down matrix
+  void* act;          // gate_up: T k x N bf16
+  // down
+  const int* ids;
+  const float* weights;
+  const float* add;
+  long long add_stride;
+  int y_dtype;
+  void* y;
+  long long y_stride;
+  void* ws;
+};
+size_t moe_gate_up_workspace(int fmt, int T, int k, int E, int F, int K);
+size_t moe_down_workspace(int fmt, int T, int k, int E, int H, int K);
+int launch_moe_gate_up(const MoeGemmArgs& a, int num_sms, cudaStream_t s, std::string* err);
+int launch_moe_down(const MoeGemmArgs& a, int num_sms, cudaStream_t s, std::string* err);
+unsigned int take_moe_errors();
+
 // GPU quantizers (fp64 arithmetic).
 int launch_quantize(int fmt, const float* w, void* blocks, int N, int K, cudaStream_t stream,
                     std::string* err);

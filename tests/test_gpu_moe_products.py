@@ -1,0 +1,305 @@
+"""The experts' products (kq_moe_gate_up, kq_moe_down) against 64-bit forms on the oracle's weights.
+
+Tolerance of a product: the library's contract, d = 1e-4 sum_k |w_k x_k|. act = silu(g) u: |silu'| <= 1.1, so
+1.1 d_g |u| + (|silu(g)| + 1.1 d_g) d_u, expf, the division and the products 8 units of 2^-24, and the rounding to bf16 (8 significant
+bits: neighbours of 1 are 2^-7 apart, so at most 2^-8 of the value). y: the
+weights' sum of the products' d, one rounding per choice and one for add, and the rounding to y's type.
+"""
+import numpy as np
+import pytest
+import torch
+
+import quantized_decode_gemv_block_gb300 as kq
+from moe_plain import bf16, dev, experts, product
+
+pytestmark = pytest.mark.gpu
+TOL, U = 1e-4, 2.0 ** -24
+FORMATS = ["q4_k", "q8_0", "q5_k", "q6_k", "affine4"]
+
+
+@pytest.fixture(scope="module", autouse=True)
+def built():
+    from quantized_decode_gemv_block_gb300 import build
+    build.build()
+    import oracle
+    oracle.build()
+    assert torch.cuda.is_available()
+    yield
+    assert kq.device_errors() == 0
+
+
+def some_ids(T, k, E, seed=0, none=0.0, twice=False):
+    rng = np.random.default_rng(seed + T + E)
+    ids = np.stack([rng.integers(0, E, k) if twice else rng.permutation(E)[:k] for _ in range(T)]) if T else np.zeros((0, k))
+    ids = ids.astype(np.int32)
+    ids[rng.random((T, k)) < none] = -1
+    return ids
+
+
+def gate_up(fmt, w, wp, x, ids, F, **kw):
+    T, k = ids.shape
+    E, K = wp.shape[0], wp.shape[2]
+    plan = kq.moe_plan(dev(ids), E)
+    act = kw.pop("act", None)
+    if act is None:
+        act = torch.full((T * k, F), 77.0, dtype=torch.bfloat16, device="cuda")
+    out = kq.moe_gate_up(fmt, w, x, plan, F, K, act=act, **kw)
+    e = ids.reshape(-1)
+    y, b = product(wp, x.repeat_interleave(k, 0), e)
+    g, u, dg, du = y[:, :F], y[:, F:], TOL * b[:, :F], TOL * b[:, F:]
+    silu = g / (1 + np.exp(-g))
+    ref = silu * u
+    tol = 1.1 * dg * np.abs(u) + (np.abs(silu) + 1.1 * dg) * du + 8 * U * np.abs(ref)
+    tol += (np.abs(ref) + tol) * 2.0 ** -8 + 2.0 ** -126
+    got = out.double().cpu().numpy()
+    assert (np.abs(got - ref) <= tol)[e >= 0].all(), (np.abs(got - ref) - tol)[e >= 0].max()
+    assert (got[e < 0] == 77.0).all()  # left as they were
+    return out
+
+
+def down(fmt, w, wp, act, ids, weights, H, add=None, dtype=torch.float32, **kw):
+    T, k = ids.shape
+    E, K = wp.shape[0], wp.shape[2]
+    plan = kq.moe_plan(dev(ids), E)
+    a0 = None if add is None else add.double().cpu().numpy()
+    out = kq.moe_down(fmt, w, act, plan, dev(ids), weights, H, K, add=add, out_dtype=dtype, **kw)
+    e = ids.reshape(-1)
+    y, b = product(wp, act, e)
+    c = np.abs(weights.double().cpu().numpy())
+    y, b = y.reshape(T, k, H), b.reshape(T, k, H)
+    ref = (y * weights.double().cpu().numpy()[..., None]).sum(1)
+    size = (np.abs(y) * c[..., None]).sum(1)
+    if add is not None:
+        ref, size = ref + a0, size + np.abs(a0)
+    tol = TOL * (b * c[..., None]).sum(1) + (k + 1) * U * size + np.abs(ref) * torch.finfo(dtype).eps / 2 + 2.0 ** -126
+    got = out.double().cpu().numpy()
+    assert (np.abs(got - ref) <= tol).all(), (np.abs(got - ref) - tol).max()
+    return out
+
+
+def some_weights(T, k, seed=0):
+    return torch.rand((T, k), generator=torch.Generator(device="cuda").manual_seed(seed + T), device="cuda")
+
+
+def both(fmt, T, k, E, H, F, none=0.0, twice=False, seed=0):
+    ids = some_ids(T, k, E, seed, none, twice)
+    w1, p1 = experts(fmt, E, 2 * F, H, seed)
+    act = gate_up(fmt, w1, p1, bf16(T, H, seed=seed), ids, F)
+    w2, p2 = experts(fmt, E, H, F, seed + 1)
+    act = torch.where(torch.tensor(ids.reshape(-1) < 0, device="cuda")[:, None], float("nan"), act)  # read by nobody
+    down(fmt, w2, p2, act, ids, some_weights(T, k), H)
+    return ids
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("T", [1, 2, 7, 8, 9, 16, 17, 40])
+def test_formats_and_token_counts(fmt, T):
+    both(fmt, T, 2, 4, 512, 256)
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("K", [256, 768, 2304, 2560, 2816, 5120, 5376, 10496])
+def test_lengths(fmt, K):
+    """One, several and too many units for one CTA: two, four and eight CTAs share K."""
+    E, T, k, N = 2, 5, 1, 40
+    ids = some_ids(T, k, E)
+    w, p = experts(fmt, E, 2 * N, K)
+    gate_up(fmt, w, p, bf16(T, K), ids, N)
+    w, p = experts(fmt, E, N, K)
+    down(fmt, w, p, bf16(T * k, K), ids, some_weights(T, k), N)
+
+
+@pytest.mark.parametrize("fmt", ["q4_k", "q6_k", "affine4"])
+@pytest.mark.parametrize("N", [8, 24, 56, 136])
+def test_rows_that_end_inside_a_tile(fmt, N):
+    E, T, k, K = 8, 6, 3, 512
+    ids = some_ids(T, k, E)
+    w, p = experts(fmt, E, 2 * N, K)
+    gate_up(fmt, w, p, bf16(T, K), ids, N)
+    w, p = experts(fmt, E, N, K)
+    down(fmt, w, p, bf16(T * k, K), ids, some_weights(T, k), N)
+
+
+@pytest.mark.parametrize("N", [1, 3, 7, 17, 33])
+def test_odd_rows(N):
+    E, T, k, K = 3, 5, 2, 256
+    ids = some_ids(T, k, E)
+    w, p = experts("q4_k", E, 2 * N, K)
+    gate_up("q4_k", w, p, bf16(T, K), ids, N)
+    w, p = experts("q4_k", E, N, K)
+    down("q4_k", w, p, bf16(T * k, K), ids, some_weights(T, k), N)
+
+
+@pytest.mark.parametrize("kw", [dict(E=1, k=1), dict(E=60, k=4), dict(E=16, k=16), dict(E=8, k=2, none=0.3), dict(E=8, k=2, none=1.0),
+                                dict(E=5, k=4, twice=True), dict(E=1, k=6, twice=True)])
+def test_shares_of_experts(kw):
+    both("q4_k", 21, H=256, F=256, **kw)
+
+
+def test_one_expert_takes_all_and_others_none():
+    T, E, K, N = 90, 30, 512, 64
+    ids = np.full((T, 1), 11, np.int32)
+    w, p = experts("q4_k", E, 2 * N, K)
+    gate_up("q4_k", w, p, bf16(T, K), ids, N)
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+def test_a_pair_has_the_bits_it_has_alone(fmt):
+    """In windows of up to 32 tokens of an expert, whatever the others are."""
+    T, k, E, H, F = 30, 2, 4, 768, 256
+    ids = some_ids(T, k, E)
+    w1, p1 = experts(fmt, E, 2 * F, H)
+    w2, p2 = experts(fmt, E, H, F, 1)
+    x, weights = bf16(T, H), some_weights(T, k)
+    act = gate_up(fmt, w1, p1, x, ids, F)
+    y = down(fmt, w2, p2, act, ids, weights, H)
+    for t in (0, 13, 29):
+        a = gate_up(fmt, w1, p1, x[t:t + 1], ids[t:t + 1], F)
+        assert torch.equal(a, act[t * k:(t + 1) * k])
+        assert torch.equal(down(fmt, w2, p2, a, ids[t:t + 1], weights[t:t + 1], H)[0], y[t])
+    one = some_ids(T, k, E, seed=9)
+    one[4] = ids[4]
+    assert torch.equal(gate_up(fmt, w1, p1, x, one, F)[8:10], act[8:10])
+
+
+def test_products_agree_with_gemv():
+    E, H, K, T = 3, 520, 2560, 4
+    ids = np.array([[0], [2], [1], [2]], np.int32)
+    w, p = experts("q4_k", E, H, K)
+    x = bf16(T, K)
+    y = down("q4_k", w, p, x, ids, torch.ones((T, 1), device="cuda"), H)
+    size = kq.row_bytes("q4_k", K) * H
+    for t in range(T):
+        e = int(ids[t, 0])
+        g = kq.gemv("q4_k", w[e * size:(e + 1) * size], x[t:t + 1], H, K)
+        b = np.abs(x[t].double().cpu().numpy()) @ np.abs(p[e]).T
+        assert (np.abs((g[0] - y[t]).double().cpu().numpy()) <= 2 * TOL * b).all()
+
+
+def test_added_rows_types_strides_and_in_place():
+    T, k, E, H, K = 13, 2, 4, 264, 512
+    ids = some_ids(T, k, E, none=0.2)
+    w, p = experts("q4_k", E, H, K)
+    act, weights = bf16(T * k, K), some_weights(T, k)
+    wide = torch.randn((T, H + 9), device="cuda")
+    add = wide[:, 5:5 + H]
+    y = down("q4_k", w, p, act, ids, weights, H, add=add)
+    yb = down("q4_k", w, p, act, ids, weights, H, add=add, dtype=torch.bfloat16)
+    assert torch.equal(yb, y.to(torch.bfloat16))
+    out = torch.full((T, H + 3), 9.0, device="cuda")
+    down("q4_k", w, p, act, ids, weights, H, add=add, y=out[:, 1:1 + H])
+    assert torch.equal(out[:, 1:1 + H], y) and (out[:, 0] == 9.0).all() and (out[:, 1 + H:] == 9.0).all()
+    plan = kq.moe_plan(dev(ids), E)
+    kq.moe_down("q4_k", w, act, plan, dev(ids), weights, H, K, add=add, y=add)
+    assert torch.equal(add, y)
+    x = bf16(T, K + 24)[:, 8:8 + K]
+    w, p = experts("q4_k", E, 2 * 40, K)
+    gate_up("q4_k", w, p, x, ids, 40)
+
+
+def test_tokens_without_experts_get_what_is_added():
+    T, k, E, H, K = 4, 2, 3, 64, 256
+    ids = np.full((T, k), -1, np.int32)
+    w, p = experts("q4_k", E, H, K)
+    act = torch.full((T * k, K), float("nan"), dtype=torch.bfloat16, device="cuda")
+    add = torch.randn((T, H), device="cuda")
+    plan = kq.moe_plan(dev(ids), E)
+    y = kq.moe_down("q4_k", w, act, plan, dev(ids), torch.full((T, k), float("nan"), device="cuda"), H, K, add=add)
+    assert torch.equal(y, add)
+    assert not kq.moe_down("q4_k", w, act, plan, dev(ids), some_weights(T, k), H, K).any()
+
+
+def test_a_nan_stays_in_its_token():
+    T, k, E, H, K = 20, 1, 2, 96, 512
+    ids = np.zeros((T, k), np.int32)
+    w, p = experts("q4_k", E, 2 * H, K)
+    x = bf16(T, K)
+    clean = gate_up("q4_k", w, p, x, ids, H)
+    x[7, 100] = float("nan")
+    x[9, 3] = float("inf")
+    out = kq.moe_gate_up("q4_k", w, x, kq.moe_plan(dev(ids), E), H, K)
+    keep = [t for t in range(T) if t not in (7, 9)]
+    assert torch.equal(out[keep], clean[keep]) and out[7].isnan().all() and not out[9].isfinite().all()
+
+
+def test_plans_out_of_bounds_are_left_out_and_reported():
+    T, k, E, F, K = 6, 2, 4, 32, 256
+    ids = some_ids(T, k, E)
+    w, p = experts("q4_k", E, 2 * F, K)
+    x = bf16(T, K)
+    good = kq.moe_plan(dev(ids), E)
+    want = gate_up("q4_k", w, p, x, ids, F)
+    assert kq.device_errors() == 0
+    for change in ("order", "offsets", "falling", "negative"):
+        order, off = good.order.clone(), good.offsets.clone()
+        if change == "order":
+            order[0], order[3] = T * k, -5
+        elif change == "offsets":
+            off[E] = T * k + 1
+        elif change == "falling":
+            off[2] = 0 if off[1] > 0 else -1
+        else:
+            off[0] = -1
+        act = torch.full((T * k, F), 3.0, dtype=torch.bfloat16, device="cuda")
+        kq.moe_gate_up("q4_k", w, x, kq.MoePlan(off, order), F, K, act=act)
+        assert kq.device_errors() == 2, change
+        same = (act == want).all(1)
+        if change == "falling":  # expert 1 is left out; expert 2 has the pairs that its offsets name, the others' too
+            last = good.order[good.offsets[3]:good.offsets[4]].long()
+            assert same[last].all()
+        else:
+            assert (same | (act == 3.0).all(1)).all() and not same.all()
+
+
+def test_captured_and_replayed_with_other_choices():
+    T, k, E, H, F = 24, 2, 8, 512, 256
+    w1, p1 = experts("q4_k", E, 2 * F, H)
+    w2, p2 = experts("q6_k", E, H, F, 1)
+    x, ids, weights = bf16(T, H), dev(some_ids(T, k, E)), some_weights(T, k)
+
+    def step():
+        plan = kq.moe_plan(ids, E)
+        act = kq.moe_gate_up("q4_k", w1, x, plan, F, H)
+        return kq.moe_down("q6_k", w2, act, plan, ids, weights, H, F)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        step()
+    torch.cuda.current_stream().wait_stream(s)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        y = step()
+    for seed in (5, 6):
+        new = some_ids(T, k, E, seed=seed, none=0.1)
+        ids.copy_(dev(new))
+        x.copy_(bf16(T, H, seed=seed))
+        graph.replay()
+        a = gate_up("q4_k", w1, p1, x, new, F)
+        a = torch.where(ids.flatten()[:, None] < 0, 0, a)
+        assert torch.equal(down("q6_k", w2, p2, a, new, weights, H), y)
+
+
+def test_two_streams_at_once():
+    T, k, E, H, F = 40, 2, 8, 512, 256
+    w, p = experts("q4_k", E, 2 * F, H)
+    calls = [(bf16(T, H, seed=i), some_ids(T, k, E, seed=i)) for i in range(2)]
+    plans = [kq.moe_plan(dev(i), E) for _, i in calls]
+    want = [gate_up("q4_k", w, p, x, i, F) for x, i in calls]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in calls]
+    got = [[], []]
+    for _ in range(5):
+        for n, s in enumerate(streams):
+            got[n].append(kq.moe_gate_up("q4_k", w, calls[n][0], plans[n], F, H, stream=s))
+    torch.cuda.synchronize()
+    for n in range(2):
+        assert all(torch.equal(a, want[n]) for a in got[n])
+
+
+def test_no_tokens():
+    w, _ = experts("q4_k", 2, 32, 256)
+    plan = kq.moe_plan(torch.empty((0, 2), dtype=torch.int32, device="cuda"), 2)
+    assert kq.moe_gate_up("q4_k", w, torch.empty((0, 256), dtype=torch.bfloat16, device="cuda"), plan, 16, 256).shape == (0, 16)
+    y = kq.moe_down("q4_k", w, torch.empty((0, 256), dtype=torch.bfloat16, device="cuda"), plan,
+                    torch.empty((0, 2), dtype=torch.int32, device="cuda"), torch.empty((0, 2), device="cuda"), 32, 256)
+    assert y.shape == (0, 32)
