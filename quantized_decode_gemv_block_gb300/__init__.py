@@ -582,34 +582,52 @@ _SCORES = {"softmax": 0, "sigmoid": KQ_ROUTE_SIGMOID}
 _GROUP_SCORES = {"max": 0, "top2": KQ_ROUTE_GROUP_TOP2}
 
 
-def _here(name: str, t: torch.Tensor) -> int:
-    """The address of a tensor that a kernel of the current device reads or writes and that takes no gradient."""
-    if not t.is_cuda:
-        _not_on_gpu(name)
-    elif t.device.index != torch._C._cuda_getDevice():
-        raise ValueError(f"{name} must be on the current device")
-    if t.requires_grad and torch.is_grad_enabled():
-        raise ValueError(f"{name} requires a gradient, which this operator does not give")
+def _device() -> int:
+    """The current device's index, -1 where there is none: what get_device() says of a tensor that a kernel may take."""
+    if torch.cuda.is_initialized():
+        return torch._C._cuda_getDevice()
+    return torch.cuda.current_device() if torch.cuda.is_available() else -1
+
+
+def _here(name: str, t: torch.Tensor, dev: int) -> int:
+    """The address of a tensor that a kernel of device `dev` reads or writes and that takes no gradient."""
+    if t.get_device() != dev or t.requires_grad:
+        if not t.is_cuda:
+            _not_on_gpu(name)
+        elif t.get_device() != dev:
+            raise ValueError(f"{name} must be on the current device")
+        if t.requires_grad and torch.is_grad_enabled():
+            raise ValueError(f"{name} requires a gradient, which this operator does not give")
     return t.data_ptr()
 
 
-def _rows(name: str, t: torch.Tensor, T: int, H: int) -> int:
-    """The token stride of a (T, H) tensor of contiguous rows."""
-    if t.dim() != 2 or t.shape[0] != T or t.shape[1] != H or (H > 1 and t.stride(1) != 1):
-        raise ValueError(f"{name} must be ({T}, {H}) with contiguous rows")
-    s = t.stride(0)
-    return s if T > 1 and s > 0 else H if T <= 1 else _overlap(name)
+def _rows(name: str, t: torch.Tensor, shape) -> int:
+    """The token stride of a tensor of this shape (T, H) with contiguous rows."""
+    T, H = shape
+    if t.shape == shape:
+        s0, s1 = t.stride()
+        if s1 == 1 and s0 >= H:
+            return s0
+        if s1 == 1 or H <= 1:
+            if T <= 1:
+                return H
+            if s0 >= H:
+                return s0
+            raise ValueError(f"{name} must have a row of its own for every token")
+    raise ValueError(f"{name} must be {tuple(shape)} with contiguous rows")
 
 
-def _overlap(name: str):
-    raise ValueError(f"{name} must have a row of its own for every token")
-
-
-def _flat(name: str, t: torch.Tensor, dtype, shape) -> int:
+def _flat(name: str, t: torch.Tensor, dtype, shape, dev: int) -> int:
     """The address of a contiguous tensor of this type and shape."""
-    if t.dtype is not dtype or tuple(t.shape) != tuple(shape) or not t.is_contiguous():
+    if t.dtype is not dtype or t.shape != shape or not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous {dtype} of shape {tuple(shape)}")
-    return _here(name, t)
+    return _here(name, t, dev)
+
+
+def _weights(name: str, t: torch.Tensor, H: int, dev: int) -> int:
+    if t.shape != (H,) or not t.is_contiguous():
+        raise ValueError(f"{name} must be {H} contiguous weights")
+    return _here(name, t, dev)
 
 
 def residual_norm(h: torch.Tensor | None, y: torch.Tensor | None, post=None, gate: torch.Tensor | None = None, scale: float = 1.0,
@@ -622,56 +640,57 @@ def residual_norm(h: torch.Tensor | None, y: torch.Tensor | None, post=None, gat
     ref = h if y is None else y
     if ref is None:
         raise ValueError("one of h and y is needed")
-    if ref.dim() != 2:
+    shape = ref.shape
+    if len(shape) != 2:
         raise ValueError("h and y must be (tokens, H)")
-    T, H = ref.shape
+    T, H = shape
+    dev = _device()
     h_dtype = (ref if h is None else h).dtype
-    y_dtype = ref.dtype
     flags = KQ_NORM_UNIT_OFFSET if unit_offset else 0
-    yp = ys = hp = hs = gp = gs = xp = xs = 0
+    yp = ys = hp = hs = gp = gs = xp = xs = post_p = pre_p = 0
+    w_dtype, x_code = torch.float32, F32
     if y is not None:
-        yp, ys = _here("y", y), _rows("y", y, T, H)
+        yp, ys = _here("y", y, dev), _rows("y", y, shape)
     if h is not None:
-        hp, hs = _here("h", h), _rows("h", h, T, H)
+        hp, hs = _here("h", h, dev), _rows("h", h, shape)
     if gate is not None:
-        if gate.dtype is not y_dtype:
+        if gate.dtype is not ref.dtype:
             raise ValueError("gate must have y's type")
-        gp = _here("gate", gate)
+        gp = _here("gate", gate, dev)
         if gate.dim() == 1:
-            if gate.shape[0] != H or (H > 1 and gate.stride(0) != 1):
+            if gate.shape[0] != H or not gate.is_contiguous():
                 raise ValueError("gate must be (H) or (T, H) with contiguous rows")
         else:
-            gs = _rows("gate", gate, T, H)
-    w, w_dtype = [0, 0], F32
-    for i, (name, t) in enumerate((("post", post), ("pre", pre))):
-        if isinstance(t, torch.Tensor):
-            if t.dim() != 1 or t.shape[0] != H or not t.is_contiguous():
-                raise ValueError(f"{name} must be {H} contiguous weights")
-            if w[0] and t.dtype is not post.dtype:
-                raise ValueError("post and pre must agree in type")
-            w[i], w_dtype = _here(name, t), _dtype(t.dtype)
+            gs = _rows("gate", gate, shape)
     if post is not None and post is not False:
         flags |= KQ_NORM_POST
+        if post is not True:
+            post_p, w_dtype = _weights("post", post, H, dev), post.dtype
     if h_out is None:
-        h_out, hos = _empty((T, H), h_dtype, ref.device, stream), H
+        h_out, hos = _empty(shape, h_dtype, ref.device, stream), H
         hop = h_out.data_ptr()
     else:
         if h_out.dtype is not h_dtype and h is not None:
             raise ValueError("h_out must have h's type")
         h_dtype = h_out.dtype
-        hop, hos = _here("h_out", h_out), _rows("h_out", h_out, T, H)
+        hop, hos = _here("h_out", h_out, dev), _rows("h_out", h_out, shape)
     if pre is not None and pre is not False:
+        if pre is not True:
+            if post_p and pre.dtype is not w_dtype:
+                raise ValueError("post and pre must agree in type")
+            pre_p, w_dtype = _weights("pre", pre, H, dev), pre.dtype
         if x_out is None:
-            x_out, xs = _empty((T, H), x_dtype or torch.bfloat16, ref.device, stream), H
+            x_out, xs = _empty(shape, x_dtype or torch.bfloat16, ref.device, stream), H
             xp = x_out.data_ptr()
         else:
             if x_dtype is not None and x_out.dtype is not x_dtype:
                 raise ValueError("x_out must have x_dtype")
-            xp, xs = _here("x_out", x_out), _rows("x_out", x_out, T, H)
+            xp, xs = _here("x_out", x_out, dev), _rows("x_out", x_out, shape)
+        x_code = _dtype(x_out.dtype)
     elif x_out is not None:
         raise ValueError("x_out without pre")
-    _check(lib().kq_residual_norm(_dtype(y_dtype), yp, ys, _dtype(h_dtype), hp, hs, hop, hos, gp, gs, scale, w_dtype, w[0], w[1],
-                                  eps, _dtype(x_out.dtype) if xp else F32, xp, xs, T, H, flags, _stream(stream)))
+    _check(lib().kq_residual_norm(_dtype(ref.dtype), yp, ys, _dtype(h_dtype), hp, hs, hop, hos, gp, gs, scale, _dtype(w_dtype), post_p,
+                                  pre_p, eps, x_code, xp, xs, T, H, flags, _stream(stream)))
     return h_out, x_out
 
 
@@ -681,24 +700,26 @@ def moe_route(logits: torch.Tensor, k: int, score: str = "softmax", bias: torch.
     """The k experts of each token from the router's logits (T, E), fp32 or bf16 (kq_moe_route). score: "softmax" or
     "sigmoid"; bias: E fp32, for the choice only; group_score: "max" or "top2". Returns (ids int32 [T, k], -1 where no expert
     can be chosen, weights fp32 [T, k]). Carries no gradient."""
-    if logits.dim() != 2:
+    shape = logits.shape
+    if len(shape) != 2:
         raise ValueError("logits must be (tokens, experts)")
-    T, E = logits.shape
+    T, E = shape
     if score not in _SCORES or group_score not in _GROUP_SCORES:
         raise ValueError("score must be softmax or sigmoid, group_score max or top2")
-    xp, xs = _here("logits", logits), _rows("logits", logits, T, E)
-    bp = 0 if bias is None else _flat("bias", bias, torch.float32, (E,))
-    n = (T, max(k, 0))
+    dev = _device()
+    xp, xs = _here("logits", logits, dev), _rows("logits", logits, shape)
+    bp = 0 if bias is None else _flat("bias", bias, torch.float32, (E,), dev)
+    out = (T, max(k, 0))
     if ids is None:
-        ids = _empty(n, torch.int32, logits.device, stream)
+        ids = _empty(out, _I32, logits.device, stream)
         ip = ids.data_ptr()
     else:
-        ip = _flat("ids", ids, _I32, n)
+        ip = _flat("ids", ids, _I32, out, dev)
     if weights is None:
-        weights = _empty(n, torch.float32, logits.device, stream)
+        weights = _empty(out, torch.float32, logits.device, stream)
         wp = weights.data_ptr()
     else:
-        wp = _flat("weights", weights, torch.float32, n)
+        wp = _flat("weights", weights, torch.float32, out, dev)
     flags = _SCORES[score] | _GROUP_SCORES[group_score] | (KQ_ROUTE_RENORM if renorm else 0)
     _check(lib().kq_moe_route(_dtype(logits.dtype), xp, xs, T, E, k, bp, n_group, top_group, scale, flags, ip, wp, _stream(stream)))
     return ids, weights
@@ -713,7 +734,7 @@ class MoePlan:
             if t.dtype is not _I32 or t.dim() != 1 or not t.is_contiguous():
                 raise ValueError(f"{name} must be contiguous int32 of one dimension")
         if offsets.shape[0] < 2:
-            raise ValueError("offsets must hold one expert more than there are")
+            raise ValueError("offsets must hold one word more than there are experts")
         self.offsets, self.order = offsets, order
 
 
@@ -722,12 +743,16 @@ def moe_plan(ids: torch.Tensor, n_experts: int, out: MoePlan | None = None, stre
     if ids.dim() != 2:
         raise ValueError("ids must be (tokens, choices)")
     T, k = ids.shape
-    ip = _flat("ids", ids, _I32, (T, k))
+    dev = _device()
+    ip = _flat("ids", ids, _I32, (T, k), dev)
     if out is None:
-        out = MoePlan(_empty(max(n_experts, 1) + 1, _I32, ids.device, stream), _empty(T * k, _I32, ids.device, stream))
+        out = MoePlan.__new__(MoePlan)
+        out.offsets = _empty(max(n_experts, 1) + 1, _I32, ids.device, stream)
+        out.order = _empty(T * k, _I32, ids.device, stream)
         fp, op = out.offsets.data_ptr(), out.order.data_ptr()
     else:
-        fp, op = _flat("out.offsets", out.offsets, _I32, (n_experts + 1,)), _flat("out.order", out.order, _I32, (T * k,))
+        fp = _flat("out.offsets", out.offsets, _I32, (n_experts + 1,), dev)
+        op = _flat("out.order", out.order, _I32, (T * k,), dev)
     _check(lib().kq_moe_plan(ip, T, k, n_experts, fp, op, _stream(stream)))
     return out
 
@@ -740,20 +765,23 @@ def moe_down_workspace_size(fmt, T: int, k: int, E: int, H: int, K: int) -> int:
     return lib().kq_moe_down_workspace_size(_fmt(fmt), T, k, E, H, K)
 
 
-def _experts(w: torch.Tensor, plan: MoePlan, rows: int, fmt: int, K: int):
+_BLOCKS = {Q8_0: (32, 34), Q4_K: (256, 144), AFFINE4: (32, 20), Q5_K: (256, 176), Q6_K: (256, 210)}
+
+
+def _experts(w: torch.Tensor, plan: MoePlan, rows: int, fmt: int, K: int, dev: int):
     """The address of the experts' blocks, their number, and the addresses of the plan."""
     E = plan.offsets.shape[0] - 1
-    if w.dtype is not torch.uint8 or not w.is_contiguous() or w.numel() != E * rows * lib().kq_row_bytes(fmt, K):
+    n, size = _BLOCKS.get(fmt, (1, 0))
+    if w.dtype is not torch.uint8 or not w.is_contiguous() or (w.numel() != E * rows * (K // n) * size and size):
         raise ValueError(f"w must be the contiguous uint8 blocks of {E} matrices of {rows} x {K} weights")
-    return _here("w", w), E, _here("plan.offsets", plan.offsets), _here("plan.order", plan.order)
+    return _here("w", w, dev), E, _here("plan.offsets", plan.offsets, dev), _here("plan.order", plan.order, dev)
 
 
-def _workspace(workspace: torch.Tensor | None, need: int, device, stream):
-    if workspace is None:
-        workspace = _empty(need, torch.uint8, device, stream) if need else None
-    elif not workspace.is_contiguous():
+def _workspace(workspace: torch.Tensor, dev: int):
+    """The address and bytes of a given workspace."""
+    if not workspace.is_contiguous():
         raise ValueError("workspace must be contiguous")
-    return (workspace, _here("workspace", workspace), workspace.nbytes) if workspace is not None else (None, 0, 0)
+    return _here("workspace", workspace, dev), workspace.nbytes
 
 
 def moe_gate_up(fmt, w: torch.Tensor, x: torch.Tensor, plan: MoePlan, F: int, K: int, act: torch.Tensor | None = None,
@@ -765,8 +793,9 @@ def moe_gate_up(fmt, w: torch.Tensor, x: torch.Tensor, plan: MoePlan, F: int, K:
     if x.dim() != 2 or x.dtype is not torch.bfloat16:
         raise ValueError("x must be (tokens, K) bf16")
     T = x.shape[0]
-    wp, E, fp, op = _experts(w, plan, 2 * F, fmt, K)
-    xp, xs = _here("x", x), _rows("x", x, T, K)
+    dev = _device()
+    wp, E, fp, op = _experts(w, plan, 2 * F, fmt, K, dev)
+    xp, xs = _here("x", x, dev), _rows("x", x, (T, K))
     n = plan.order.shape[0]
     if n % T if T else n:
         raise ValueError("the plan must hold a number of choices for each of x's tokens")
@@ -775,8 +804,11 @@ def moe_gate_up(fmt, w: torch.Tensor, x: torch.Tensor, plan: MoePlan, F: int, K:
         act = _empty((n, F), torch.bfloat16, x.device, stream)
         ap = act.data_ptr()
     else:
-        ap = _flat("act", act, torch.bfloat16, (n, F))
-    ws, wsp, wsn = _workspace(workspace, moe_gate_up_workspace_size(fmt, T, k, E, F, K) if workspace is None else 0, x.device, stream)
+        ap = _flat("act", act, torch.bfloat16, (n, F), dev)
+    if workspace is None:
+        size = moe_gate_up_workspace_size(fmt, T, k, E, F, K)
+        workspace = _empty(max(size, 256), torch.uint8, x.device, stream)
+    wsp, wsn = _workspace(workspace, dev)
     _check(lib().kq_moe_gate_up(fmt, wp, xp, xs, fp, op, T, k, E, F, K, ap, wsp, wsn, _stream(stream)))
     return act
 
@@ -790,25 +822,29 @@ def moe_down(fmt, w: torch.Tensor, act: torch.Tensor, plan: MoePlan, ids: torch.
     fmt = _fmt(fmt)
     if ids.dim() != 2:
         raise ValueError("ids must be (tokens, choices)")
-    T, k = ids.shape
-    wp, E, fp, op = _experts(w, plan, H, fmt, K)
+    shape = T, k = ids.shape
+    dev = _device()
+    wp, E, fp, op = _experts(w, plan, H, fmt, K, dev)
     if plan.order.shape[0] != T * k:
         raise ValueError("the plan must be that of the ids")
-    ap = _flat("act", act, torch.bfloat16, (T * k, K))
-    ip, tp = _flat("ids", ids, _I32, (T, k)), _flat("weights", weights, torch.float32, (T, k))
+    ap = _flat("act", act, torch.bfloat16, (T * k, K), dev)
+    ip, tp = _flat("ids", ids, _I32, shape, dev), _flat("weights", weights, torch.float32, shape, dev)
     dp = ds = 0
     if add is not None:
         if add.dtype is not torch.float32:
             raise ValueError("add must be fp32")
-        dp, ds = _here("add", add), _rows("add", add, T, H)
+        dp, ds = _here("add", add, dev), _rows("add", add, (T, H))
     if y is None:
         y, ys = _empty((T, H), out_dtype or torch.float32, act.device, stream), H
         yp = y.data_ptr()
     else:
         if out_dtype is not None and y.dtype is not out_dtype:
             raise ValueError("y must have out_dtype")
-        yp, ys = _here("y", y), _rows("y", y, T, H)
-    ws, wsp, wsn = _workspace(workspace, moe_down_workspace_size(fmt, T, k, E, H, K) if workspace is None else 0, act.device, stream)
+        yp, ys = _here("y", y, dev), _rows("y", y, (T, H))
+    if workspace is None:
+        size = moe_down_workspace_size(fmt, T, k, E, H, K)
+        workspace = _empty(max(size, 256), torch.uint8, act.device, stream)
+    wsp, wsn = _workspace(workspace, dev)
     _check(lib().kq_moe_down(fmt, wp, ap, fp, op, ip, tp, T, k, E, H, K, dp, ds, _dtype(y.dtype), yp, ys, wsp, wsn, _stream(stream)))
     return y
 

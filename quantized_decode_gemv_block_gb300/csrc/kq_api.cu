@@ -741,7 +741,7 @@ int kq_residual_norm(int y_dtype, const void* y, long long y_stride, int h_dtype
       return fail(KQ_ERR_ARG, "x and h_out may take y's place at its type and stride, and h_out h's; x not h's or h_out's");
     const kq::ResidualNormArgs a = {y_dtype, h_dtype, w_dtype, x_dtype, y, y_stride, h, h_stride, h_out, h_out_stride, x, x_stride,
                                     gate, gate_stride, post, pre, scale, eps, T, H,
-                                    (flags & KQ_NORM_POST) != 0, (flags & KQ_NORM_UNIT_OFFSET) != 0};
+                                    (flags & KQ_NORM_POST) != 0, flags & KQ_NORM_UNIT_OFFSET ? 1.f : 0.f};
     std::string err;
     if (kq::launch_residual_norm(a, static_cast<cudaStream_t>(stream), &err) != 0) return fail(KQ_ERR_CUDA, err);
     return ok();

@@ -186,7 +186,8 @@ struct ResidualNormArgs {
   const void *post, *pre;
   float scale, eps;
   int T, H;
-  bool norm_y, offset;
+  bool norm_y;
+  float offset;  // 1: stored weights stand around zero
 };
 int launch_residual_norm(const ResidualNormArgs& a, cudaStream_t s, std::string* err);
 

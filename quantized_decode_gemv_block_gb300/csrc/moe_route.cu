@@ -6,13 +6,16 @@
 //
 // Choices are those of 64-bit scores. Without a bias the logits are in the same order as the scores, and they are compared
 // as they are. With one, a warp orders fp32 choices and looks at the gaps that decide: where one is within what fp32 can be
-// off, it does the token again in 64 bits (a few tokens in a thousand; all others need no 64-bit arithmetic, of which this
-// GPU has little). Two experts of the same logit and bias are equal in either, so that bf16 logits' ties stay in fp32.
+// off, it forms the choices that can be concerned in 64 bits, a lane for each (one token in a hundred needs that, but with
+// all 256 experts in 64 bits that token alone took 13 us of the call's 28: this GPU has little 64-bit arithmetic). Two
+// experts of the same logit and bias are equal in either, so that bf16 logits' ties stay in fp32.
 //
-// One warp per token, logits and choices in registers, the maxima by the warp's integer reduction on keys in the order of
-// the values. Plan: a stable counting sort; a warp takes its consecutive pairs 32 at a time and ranks those of one expert
-// among them by a match, once to count and once to place, with the sums over warps (and up to eight CTAs of a
-// cluster, through their shared memory) between.
+// One warp per token, logits and choices in registers. Bound by the instructions: up to 256 experts a lane sorts its own (a
+// network of 19 exchanges for eight) and a choice takes the largest of the lanes' heads by the warp's integer reduction, on
+// keys in the order of the values.
+// Plan: a stable counting sort. A warp holds up to 256 consecutive pairs and ranks those of one expert among 32 by ballots over
+// the ids' bits; counts go to the warp's own counters, and the sums over warps (and the eight CTAs of a cluster, through
+// their shared memory) give each pair its place. Bound by latency: loads, two turns of shared memory, two cluster barriers.
 #include <cooperative_groups.h>
 #include <cuda_bf16.h>
 
@@ -35,39 +38,106 @@ constexpr int kRouteWarps = 4;
 struct RouteParams {
   MoeRouteArgs a;
   int per_group;  // experts of a group
-  int row_bytes;  // shared memory of a warp: E logits, E choices in 64 bits
+  int magic;      // e / per_group = e * magic >> 20, for e < 1024
+  int row_bytes;  // shared memory of a warp: E times keys of 64-bit choices, logits, fp32 choices, a list
 };
 
-// Keys in the order of the values.
+// Keys in the order of the values (-0 as 0).
 __device__ __forceinline__ uint32_t key_of(float v) {
-  const uint32_t b = __float_as_uint(v == 0.f ? 0.f : v);
-  return b >> 31 ? ~b : b | 0x80000000u;
+  const int b = __float_as_int(v + 0.f);
+  return (uint32_t)b ^ ((uint32_t)(b >> 31) | 0x80000000u);
 }
-__device__ __forceinline__ float of_key(uint32_t k) { return __uint_as_float(k >> 31 ? k & 0x7FFFFFFFu : ~k); }
+__device__ __forceinline__ float of_key(uint32_t k) { return __uint_as_float(k ^ ((uint32_t)((int)~k >> 31) | 0x80000000u)); }
+constexpr uint32_t kNone = 0x007FFFFFu;  // the key of -inf
 
+// A lane's choices, largest first, equal ones by the lower expert. Up to eight are sorted once by exchanges of neighbours, which
+// keep equal keys in their order, and then move up; more of them are looked through for each choice (at 16 sorting
+// would take 120 exchanges).
+template <int N>
+struct Lane {
+  static constexpr bool kSorted = N <= 8;
+  uint32_t key[N];
+  int at[kSorted ? N : 1];
+
+  __device__ __forceinline__ void ready() {
+    if constexpr (kSorted) {
+#pragma unroll
+      for (int i = 0; i < N; ++i) at[i] = i;
+#pragma unroll
+      for (int r = 0; r < N; ++r) {
+#pragma unroll
+        for (int i = r & 1; i + 1 < N; i += 2) {
+          const bool swap = key[i + 1] > key[i];
+          const uint32_t k = key[i];
+          const int a = at[i];
+          key[i] = swap ? key[i + 1] : k, key[i + 1] = swap ? k : key[i + 1];
+          at[i] = swap ? at[i + 1] : a, at[i + 1] = swap ? a : at[i + 1];
+        }
+      }
+    }
+  }
+  __device__ __forceinline__ void head(uint32_t& k, int& i) const {
+    if constexpr (kSorted) {
+      k = key[0], i = at[0];
+    } else {
+      k = key[0];
+#pragma unroll
+      for (int n = 1; n < N; ++n) k = max(k, key[n]);
+      i = 0;
+#pragma unroll
+      for (int n = N - 1; n >= 0; --n) i = key[n] == k ? n : i;
+    }
+  }
+  __device__ __forceinline__ void pop(int i) {
+    if constexpr (kSorted) {
+#pragma unroll
+      for (int n = 0; n + 1 < N; ++n) key[n] = key[n + 1], at[n] = at[n + 1];
+      key[N - 1] = kNone;
+    } else {
+#pragma unroll
+      for (int n = 0; n < N; ++n) key[n] = n == i ? kNone : key[n];
+    }
+  }
+};
+
+// 64-bit values are compared as whole numbers in their order: this GPU's 64-bit unit takes 32 cycles for a warp.
+constexpr long long kLeast = (long long)0x8000000000000000ull;  // -inf
+__device__ __forceinline__ long long key64_of(double v) {
+  const long long b = __double_as_longlong(v + 0.0);
+  return v > -(double)INFINITY ? b ^ ((b >> 63) & 0x7FFFFFFFFFFFFFFFll) : kLeast;
+}
+__device__ __forceinline__ double of_key64(long long k) { return __longlong_as_double(k ^ ((k >> 63) & 0x7FFFFFFFFFFFFFFFll)); }
+
+__device__ __forceinline__ float least(float) { return -INFINITY; }
+__device__ __forceinline__ long long least(long long) { return kLeast; }
+__device__ __forceinline__ float plus(float a, float b) { return a + b; }
+__device__ __forceinline__ long long plus(long long a, long long b) { return key64_of(of_key64(a) + of_key64(b)); }
+
+// What a choice formed from fast fp32 scores can be off by: __expf is within (2 + 1.2 |d|) 2^-23 of its value e^-|d|, so
+// within 2.5 * 2^-23; the sum of up to 1024 of them (32 of a lane, 5 levels) within 21 * 2^-23 of itself, the division, the
+// product and the addition of the bias two roundings each: under 32 * 2^-23 for s <= 1, and a rounding of |c|.
+__device__ __forceinline__ float off_by(float c) { return 3.8146973e-6f * (1.f + 0.5f * fabsf(c)); }
+
+// The groups that stay, as a mask. choice: E values (float, or keys of 64-bit ones), the least where an expert cannot be
+// chosen. sure: NULL, or cleared where the border is too narrow for fp32; *edge is then what the lane's group (lane / lanes of a
+// group) scores by at least: its second largest choice or its largest.
 template <typename V>
-__device__ __forceinline__ V low() { return -(V)INFINITY; }
-
-// What fp32 scores and choices can be off by, with room: s is within a dozen roundings of 2^-24 (s |ln s| <= 0.37 covers
-// the difference of logits), and adding the bias rounds once more.
-__device__ __forceinline__ float off_by(float c) { return 1.9073486e-6f * (2.f + fabsf(c)); }
-
-// The groups that stay, as a mask. choice: E values, -inf where an expert cannot be chosen. sure: cleared where the border
-// is too narrow for fp32 (V = float, `exact` false).
-template <typename V>
-__device__ unsigned keep_groups(const V* choice, int G, int keep, int per_group, bool two, bool exact, bool* sure) {
+__device__ unsigned keep_groups(const V* choice, int G, int keep, int per_group, bool two, bool* sure, V* edge) {
   const int lane = threadIdx.x & 31;
   int lanes = 32;
   while (lanes * G > 32) lanes /= 2;  // lanes of a group
   const int mine = lane / lanes;
-  V a = low<V>(), b = low<V>();
+  const V none = least(V());
+  V a = none, b = none;
   if (mine < G) {
+#pragma unroll 1
     for (int i = lane % lanes; i < per_group; i += lanes) {
-      const V c = choice[mine * per_group + i];
-      if (c > a) b = a, a = c;
-      else if (c > b) b = c;
+      const V c = choice[mine * per_group + i], lo = a < c ? a : c;
+      a = a > c ? a : c;
+      b = b > lo ? b : lo;
     }
   }
+#pragma unroll 1
   for (int d = 1; d < lanes; d *= 2) {
     const V a2 = __shfl_xor_sync(kAll, a, d), b2 = __shfl_xor_sync(kAll, b, d);
     const V lo = a < a2 ? a : a2;
@@ -75,167 +145,214 @@ __device__ unsigned keep_groups(const V* choice, int G, int keep, int per_group,
     b = b > lo ? b : lo;
     a = a > a2 ? a : a2;
   }
-  const V score = two && b != low<V>() ? a + b : a;
+  const V score = two && b != none ? plus(a, b) : a;
+  if (edge) *edge = two && b != none ? b : a;
   // lane g now takes group g
   const V s = __shfl_sync(kAll, score, (lane < G ? lane : 0) * lanes);
   int before = 0;
+#pragma unroll 1
   for (int g = 0; g < G; ++g) {
     const V o = __shfl_sync(kAll, s, g);
     before += o > s || (o == s && g < lane);
   }
   const unsigned kept = __ballot_sync(kAll, lane < G && before < keep);
-  if (!exact) {
-    const float in = lane < G && (kept >> lane & 1) ? (float)s : INFINITY, out = lane < G && !(kept >> lane & 1) ? (float)s : -INFINITY;
-    const float least = of_key(__reduce_min_sync(kAll, key_of(in))), most = of_key(__reduce_max_sync(kAll, key_of(out)));
-    if (least - most <= 2.f * off_by(least)) *sure = false;
+  if (sure) {
+    const bool in = lane < G && (kept >> lane & 1);
+    const float f = (float)s;
+    const float low = of_key(__reduce_min_sync(kAll, key_of(in ? f : INFINITY)));
+    const float high = of_key(__reduce_max_sync(kAll, key_of(lane < G && !in ? f : -INFINITY)));
+    if (low - high <= 4.f * off_by(low)) *sure = false;  // sums of two
   }
   return kept;
 }
 
-template <int VPL>
-__global__ void __launch_bounds__(kRouteWarps * 32) moe_route_kernel(const RouteParams p) {
+// The 64-bit choices of the experts whose fp32 one is within reach of `edge` (of lane (group * lanes)'s edge where lanes > 0), as
+// keys; the others' are the fp32 ones, which decide nothing. All lanes take part. Out of line, as most tokens pass by.
+__device__ __noinline__ void exact_choices(const RouteParams& p, long long* keys, float top, float edge, int lanes) {
+  const MoeRouteArgs& a = p.a;
+  const float* xs = reinterpret_cast<const float*>(keys + a.E);
+  const float* cs = xs + a.E;
+  int* list = reinterpret_cast<int*>(keys + 2 * a.E);
+  const int lane = threadIdx.x % 32;
+  int n = 0;
+  for (int b = 0; b < a.E; b += 32) {
+    const int e = b + lane;
+    const float at = __shfl_sync(kAll, edge, lanes && e < a.E ? (e * p.magic >> 20) * lanes : 0);
+    const float f = e < a.E ? cs[e] : -INFINITY;
+    const bool in = f > -INFINITY && f >= at - 2.f * off_by(at);
+    if (e < a.E) keys[e] = key64_of((double)f);
+    const unsigned ins = __ballot_sync(kAll, in);
+    if (in) list[n + __popc(ins & ((1u << lane) - 1))] = e;
+    n += __popc(ins);
+  }
+  double per_z = 1.0;
+  if (a.softmax) {
+    double z = 0.0;
+    for (int e = lane; e < a.E; e += 32) z += exp((double)xs[e] - (double)top);
+#pragma unroll
+    for (int d = 16; d > 0; d /= 2) z += __shfl_xor_sync(kAll, z, d);
+    per_z = 1.0 / z;
+  }
+  __syncwarp();
+  for (int j = lane; j < n; j += 32) {
+    const int e = list[j];
+    const double v = xs[e];
+    double s = exp(a.softmax ? v - (double)top : -fabs(v)) * per_z;
+    if (!a.softmax) {  // u / (1 + u) or 1 / (1 + u) of u = exp(-|v|) <= 1: a reciprocal in [1/2, 1] by two Newton steps
+      const double y = 1.0 + s;
+      double r = (double)__frcp_rn((float)y);
+      r = fma(r, fma(-y, r, 1.0), r);
+      r = fma(r, fma(-y, r, 1.0), r);
+      s = v < 0.0 ? s * r : r;
+    }
+    keys[e] = key64_of(s + (a.bias ? (double)a.bias[e] : 0.0));
+  }
+  __syncwarp();
+}
+
+// Lane j gets the expert of the j-th largest key, -1 where there is none; the keys are used up.
+__device__ __noinline__ int largest_keys(long long* keys, int E, int k) {
+  const int lane = threadIdx.x % 32;
+  int id = -1;
+  for (int j = 0; j < k; ++j) {
+    long long m = kLeast;
+    int best = E;
+#pragma unroll 4
+    for (int e = lane; e < E; e += 32)
+      if (keys[e] > m) m = keys[e], best = e;
+    const int hi = __reduce_max_sync(kAll, (int)(m >> 32));
+    const unsigned lo = __reduce_max_sync(kAll, (int)(m >> 32) == hi ? (unsigned)m : 0u);
+    const bool mine = (int)(m >> 32) == hi && (unsigned)m == lo;
+    best = (int)__reduce_min_sync(kAll, mine ? (unsigned)best : kAll);
+    if (best == E) break;
+    if (lane == j) id = best;
+    if (lane == (best & 31)) keys[best] = kLeast;
+    __syncwarp();
+  }
+  return id;
+}
+
+template <typename X, int VPL>
+__global__ void __launch_bounds__(kRouteWarps * 32, VPL <= 8 ? 10 : 1) moe_route_kernel(const __grid_constant__ RouteParams p) {
   extern __shared__ __align__(16) uint8_t smem[];
   const MoeRouteArgs& a = p.a;
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-  double* wide = reinterpret_cast<double*>(smem + warp * p.row_bytes);
-  float* xs = reinterpret_cast<float*>(wide + a.E);
+  long long* keys = reinterpret_cast<long long*>(smem + warp * p.row_bytes);
+  float* xs = reinterpret_cast<float*>(keys + a.E);
+  float* cs = xs + a.E;
   const long long t = (long long)blockIdx.x * kRouteWarps + warp;
   grid_launch_dependents();
   grid_dependency_wait();
   if (t >= a.T) return;
 
-  float x[VPL], c[VPL];  // expert 32 i + lane
-  float top = -INFINITY;
+  float x[VPL];  // expert 32 i + lane
+  const X* row = static_cast<const X*>(a.x) + t * a.xs + lane;
+  uint32_t most = kNone;
 #pragma unroll
   for (int i = 0; i < VPL; ++i) {
-    const int e = 32 * i + lane;
     float v = -INFINITY;
-    if (e < a.E) {
-      v = a.x_dtype == KQ_F32 ? static_cast<const float*>(a.x)[t * a.xs + e]
-                              : __uint_as_float((uint32_t)static_cast<const uint16_t*>(a.x)[t * a.xs + e] << 16);
-      v = v == v ? fminf(v, FLT_MAX) : -INFINITY;  // NaN: not to be chosen; +inf: the largest
-      xs[e] = v;
+    if (32 * i + lane < a.E) {
+      if constexpr (sizeof(X) == 4) v = row[32 * i];
+      else v = __uint_as_float((uint32_t)row[32 * i] << 16);
     }
     x[i] = v;
-    top = fmaxf(top, v);
   }
-  top = of_key(__reduce_max_sync(kAll, key_of(top)));
+#pragma unroll
+  for (int i = 0; i < VPL; ++i) {
+    x[i] = x[i] == x[i] ? fminf(x[i], FLT_MAX) : -INFINITY;  // NaN: not to be chosen; +inf: the largest
+    if (32 * i + lane < a.E) xs[32 * i + lane] = x[i];
+    most = max(most, key_of(x[i]));
+  }
+  const float top = of_key(__reduce_max_sync(kAll, most));
   __syncwarp();
 
   const bool by_score = a.bias || (a.n_group > 1 && a.two);  // else logits are in the scores' order
   float sum = 0.f;
   if (a.softmax && (by_score || !a.renorm) && top > -INFINITY) {
 #pragma unroll
-    for (int i = 0; i < VPL; ++i) sum += x[i] > -INFINITY ? expf(x[i] - top) : 0.f;
+    for (int i = 0; i < VPL; ++i) sum += expf(x[i] - top);
 #pragma unroll
     for (int d = 16; d > 0; d /= 2) sum += __shfl_xor_sync(kAll, sum, d);
   }
-  auto score = [&](float v) { return v == -INFINITY ? 0.f : a.softmax ? expf(v - top) / sum : 1.f / (1.f + expf(-v)); };
   auto bias = [&](int e) { return a.bias ? a.bias[e] : 0.f; };
-  // an expert that can be chosen has a logit, and a bias that is not -inf or NaN
-  auto choice_of = [&](float v, int e) {
-    const float s = score(v) + bias(e);
-    return v == -INFINITY || !(s > -INFINITY) ? -INFINITY : s;
-  };
 
-  // c: what is compared
-  bool sure = true;
-  unsigned groups = kAll;
-#pragma unroll
-  for (int i = 0; i < VPL; ++i) c[i] = by_score && 32 * i + lane < a.E ? choice_of(x[i], 32 * i + lane) : x[i];
-  if (a.n_group > 1) {
-    float* cs = reinterpret_cast<float*>(wide);
-#pragma unroll
-    for (int i = 0; i < VPL; ++i)
-      if (32 * i + lane < a.E) cs[32 * i + lane] = c[i];
-    __syncwarp();
-    groups = keep_groups<float>(cs, a.n_group, a.top_group, p.per_group, a.two, !by_score, &sure);
+  // c: what is compared; an expert that can be chosen has a logit, and a bias that is not -inf or NaN
+  Lane<VPL> c;
+  if (by_score) {
+    const float rest = a.softmax ? __fdividef(1.f, sum) : 1.f;
 #pragma unroll
     for (int i = 0; i < VPL; ++i) {
-      const int e = 32 * i + lane;
-      if (e < a.E && !(groups >> e / p.per_group & 1)) c[i] = x[i] = -INFINITY;
-      else if (!a.bias) c[i] = x[i];
+      const float s = a.softmax ? __expf(x[i] - top) * rest : __fdividef(1.f, 1.f + __expf(-x[i]));
+      const float b = 32 * i + lane < a.E ? s + bias(32 * i + lane) : -INFINITY;
+      c.key[i] = x[i] > -INFINITY && b > -INFINITY ? key_of(b) : kNone;
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) c.key[i] = key_of(x[i]);
+  }
+  if (by_score) {
+#pragma unroll
+    for (int i = 0; i < VPL; ++i)
+      if (32 * i + lane < a.E) cs[32 * i + lane] = of_key(c.key[i]);
+    __syncwarp();
+  }
+  if (a.n_group > 1) {
+    bool sure = true;
+    float edge = -INFINITY;
+    unsigned groups = keep_groups<float>(by_score ? cs : xs, a.n_group, a.top_group, p.per_group, a.two, by_score ? &sure : nullptr, &edge);
+    if (!sure) {
+      int lanes = 32;
+      while (lanes * a.n_group > 32) lanes /= 2;
+      exact_choices(p, keys, top, edge, lanes);
+      groups = keep_groups<long long>(keys, a.n_group, a.top_group, p.per_group, a.two, nullptr, nullptr);
+      __syncwarp();
+    }
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) {
+      const bool in = groups >> ((32 * i + lane) * p.magic >> 20 & 31) & 1;
+      if (!a.bias) c.key[i] = key_of(x[i]);
+      else if (!in && 32 * i + lane < a.E) cs[32 * i + lane] = -INFINITY;
+      if (!in) c.key[i] = kNone;
     }
   }
 
   int id = -1;  // lane j holds choice j
-  if (sure) {
-    float last = INFINITY;
-    int last_e = 0;
-    const int rounds = a.bias ? min(a.k + 1, a.E) : a.k;  // one more, for the last gap
-    for (int j = 0; j < rounds; ++j) {
-      float m = c[0];
-      int e = lane;
-#pragma unroll
-      for (int i = 1; i < VPL; ++i)
-        if (c[i] > m) m = c[i], e = 32 * i + lane;
-      const uint32_t key = __reduce_max_sync(kAll, key_of(m));
-      const float most = of_key(key);
-      if (most == -INFINITY) break;
-      e = (int)__reduce_min_sync(kAll, key_of(m) == key ? (unsigned)e : kAll);
-      if (a.bias && j > 0 && last - most <= 2.f * off_by(last) && !(xs[last_e] == xs[e] && a.bias[last_e] == a.bias[e])) {
-        sure = false;
-        break;
-      }
+  bool sure = true;
+  c.ready();
+  uint32_t last = 0;
+  int last_e = 0;
+  const int rounds = a.bias ? min(a.k + 1, a.E) : a.k;  // one more, for the last gap
+  for (int j = 0; j < rounds; ++j) {
+    uint32_t k;
+    int i;
+    c.head(k, i);
+    const uint32_t key = __reduce_max_sync(kAll, k);
+    if (key == kNone) break;
+    const int e = (int)__reduce_min_sync(kAll, k == key ? (unsigned)(32 * i + lane) : kAll);
+    if (a.bias && j > 0) {
+      const float before = of_key(last);
+      if (before - of_key(key) <= 2.f * off_by(before) && !(xs[last_e] == xs[e] && a.bias[last_e] == a.bias[e])) sure = false;
+    }
+    if (j < a.k) {
       if (lane == j) id = e;
-#pragma unroll
-      for (int i = 0; i < VPL; ++i)
-        if (32 * i + lane == e) c[i] = -INFINITY;
-      last = most;
+      last = key;
       last_e = e;
     }
-    if (a.bias && lane >= a.k) id = -1;
+    if (lane == (e & 31)) c.pop(i);
   }
-  if (!sure) {  // again in 64 bits
-    double z = 0.0;
-    id = -1;
-    if (a.softmax) {
-      for (int e = lane; e < a.E; e += 32) z += xs[e] > -INFINITY ? exp((double)xs[e] - (double)top) : 0.0;
-#pragma unroll
-      for (int d = 16; d > 0; d /= 2) z += __shfl_xor_sync(kAll, z, d);
-    }
+  if (!sure) {  // a.bias: again from the exact choices down to the last one's reach
     __syncwarp();
-    for (int e = lane; e < a.E; e += 32) {
-      const double v = xs[e], s = a.softmax ? exp(v - (double)top) / z : 1.0 / (1.0 + exp(-v));
-      const double w = s + (double)bias(e);
-      wide[e] = v == low<double>() || !(w > low<double>()) ? low<double>() : w;
-    }
-    __syncwarp();
-    if (a.n_group > 1) {
-      bool unused = true;
-      groups = keep_groups<double>(wide, a.n_group, a.top_group, p.per_group, a.two, true, &unused);
-      __syncwarp();
-      for (int e = lane; e < a.E; e += 32) {
-        if (!(groups >> e / p.per_group & 1)) wide[e] = low<double>();
-        else if (!a.bias) wide[e] = xs[e];
-      }
-      __syncwarp();
-    }
-    for (int j = 0; j < a.k; ++j) {
-      double m = low<double>();
-      int best = a.E;
-      for (int e = lane; e < a.E; e += 32)
-        if (wide[e] > m) m = wide[e], best = e;
-#pragma unroll
-      for (int d = 16; d > 0; d /= 2) {
-        const double m2 = __shfl_xor_sync(kAll, m, d);
-        const int e2 = __shfl_xor_sync(kAll, best, d);
-        if (m2 > m || (m2 == m && e2 < best)) m = m2, best = e2;
-      }
-      if (best == a.E) break;
-      if (lane == j) id = best;
-      if (lane == best % 32) wide[best] = low<double>();
-      __syncwarp();
-    }
+    exact_choices(p, keys, top, of_key(last), 0);
+    id = largest_keys(keys, a.E, a.k);
   }
 
   const float v = id >= 0 ? xs[id] : -INFINITY;
-  float w;
+  float w = 0.f;
   if (a.softmax && a.renorm) {  // softmax over the chosen: no sum over all experts to underflow against
     const float most = of_key(__reduce_max_sync(kAll, key_of(v)));
-    w = id >= 0 ? expf(v - most) : 0.f;
-  } else {
-    w = id >= 0 ? score(v) : 0.f;
+    if (id >= 0) w = expf(v - most);
+  } else if (id >= 0) {
+    w = a.softmax ? expf(v - top) / sum : 1.f / (1.f + expf(-v));
   }
   if (a.renorm) {
     float s = w;
@@ -253,15 +370,40 @@ __global__ void __launch_bounds__(kRouteWarps * 32) moe_route_kernel(const Route
 
 constexpr int kPlanWarps = 32;
 constexpr int kPlanCluster = 8;
+constexpr int kHold = 8;  // pairs of a lane at a time
 
 struct PlanParams {
   const int* ids;
   int n, E;
+  int bits;     // of an id, and of E, which stands for none
   int segment;  // pairs of a warp, a multiple of 32
   int warps;    // warps of a CTA that have pairs
   int ctas;
   int *offsets, *order;
 };
+
+// The next 32 * kHold pairs of a warp from b on: their ids (E: none), and for each the lanes that have the same one.
+__device__ __forceinline__ void take_pairs(const PlanParams& p, long long b, long long end, int (&id)[kHold], unsigned (&same)[kHold]) {
+  const int lane = threadIdx.x & 31;
+#pragma unroll
+  for (int i = 0; i < kHold; ++i) {
+    const long long q = b + 32 * i + lane;
+    id[i] = q < end ? p.ids[q] : -1;
+  }
+#pragma unroll
+  for (int i = 0; i < kHold; ++i) {
+    if ((unsigned)id[i] >= (unsigned)p.E) id[i] = p.E;
+    same[i] = kAll;
+  }
+  for (int bit = 0; bit < p.bits; ++bit) {
+#pragma unroll
+    for (int i = 0; i < kHold; ++i) {
+      const bool set = id[i] >> bit & 1;
+      const unsigned v = __ballot_sync(kAll, set);
+      same[i] &= set ? v : ~v;
+    }
+  }
+}
 
 __global__ void __launch_bounds__(kPlanWarps * 32) moe_plan_kernel(const PlanParams p) {
   extern __shared__ int counts[];  // [warps][E], then E totals
@@ -273,22 +415,27 @@ __global__ void __launch_bounds__(kPlanWarps * 32) moe_plan_kernel(const PlanPar
   for (int i = tid; i < p.warps * p.E; i += kPlanWarps * 32) counts[i] = 0;
   grid_launch_dependents();
   grid_dependency_wait();
-  __syncthreads();
 
   // pairs [p0, p1) are this warp's
   const long long p0 = ((long long)rank * p.warps + warp) * p.segment;
   const long long p1 = warp < p.warps ? min(p0 + p.segment, (long long)p.n) : p0;
   int* mine = counts + warp * p.E;
-  for (long long b = p0; b < p1; b += 32) {
-    const int id = b + lane < p1 ? p.ids[b + lane] : -1;
-    const unsigned same = __match_any_sync(kAll, id);
-    if (id >= 0 && id < p.E && (same & ((1u << lane) - 1)) == 0) mine[id] += __popc(same);
-    __syncwarp();
+  const unsigned below = (1u << lane) - 1;
+  int id[kHold];
+  unsigned same[kHold];
+  if (p0 < p1) take_pairs(p, p0, p1, id, same);
+  __syncthreads();
+  for (long long b = p0; b < p1; b += 32 * kHold) {
+    if (b > p0) take_pairs(p, b, p1, id, same);
+#pragma unroll
+    for (int i = 0; i < kHold; ++i)  // additions of whole numbers: their order does not matter
+      if (id[i] < p.E && !(same[i] & below)) atomicAdd(mine + id[i], __popc(same[i]));
   }
   __syncthreads();
   int all = 0, before = 0;
   if (tid < p.E) {  // E <= threads
     int run = 0;
+#pragma unroll 8
     for (int w = 0; w < p.warps; ++w) {
       const int c = counts[w * p.E + tid];
       counts[w * p.E + tid] = run;
@@ -301,11 +448,14 @@ __global__ void __launch_bounds__(kPlanWarps * 32) moe_plan_kernel(const PlanPar
     cg::cluster_group cluster = cg::this_cluster();
     cluster.sync();
     if (tid < p.E) {
+      int c[kPlanCluster];
+#pragma unroll
+      for (int r = 0; r < kPlanCluster; ++r) c[r] = cluster.map_shared_rank(total, r)[tid];
       all = 0;
-      for (int r = 0; r < p.ctas; ++r) {
-        const int c = cluster.map_shared_rank(total, r)[tid];
-        if (r < rank) before += c;
-        all += c;
+#pragma unroll
+      for (int r = 0; r < kPlanCluster; ++r) {
+        before += r < rank ? c[r] : 0;
+        all += c[r];
       }
     }
     cluster.sync();  // totals are read everywhere before they are overwritten
@@ -336,24 +486,40 @@ __global__ void __launch_bounds__(kPlanWarps * 32) moe_plan_kernel(const PlanPar
   }
   if (rank == 0 && tid == 0) p.offsets[p.E] = live;
   __syncthreads();
-  for (long long b = p0; b < p1; b += 32) {
-    const int id = b + lane < p1 ? p.ids[b + lane] : -1;
-    const unsigned same = __match_any_sync(kAll, id), lower = same & ((1u << lane) - 1);
-    const bool ok = id >= 0 && id < p.E;
-    if (ok) p.order[total[id] + mine[id] + __popc(lower)] = (int)(b + lane);
-    __syncwarp();
-    if (ok && lower == 0) mine[id] += __popc(same);
-    __syncwarp();
+  for (long long b = p0; b < p1; b += 32 * kHold) {
+    if (p.segment > 32 * kHold) take_pairs(p, b, p1, id, same);
+#pragma unroll
+    for (int i = 0; i < kHold; ++i) {
+      int place = 0;  // of the first lane with this id, which holds the counter's turn
+      const bool first = !(same[i] & below);
+      if (id[i] < p.E && first) {
+        place = total[id[i]] + mine[id[i]];
+        mine[id[i]] += __popc(same[i]);
+      }
+      place = __shfl_sync(kAll, place, __ffs(same[i]) - 1) + __popc(same[i] & below);
+      if (id[i] < p.E) p.order[place] = (int)(b + 32 * i + lane);
+      __syncwarp();
+    }
   }
   for (long long i = (long long)live + rank * (kPlanWarps * 32) + tid; i < p.n; i += p.ctas * (kPlanWarps * 32)) p.order[i] = -1;
 }
 
-template <int VPL>
+template <typename X, int VPL>
 int launch_route(const RouteParams& p, cudaStream_t s, std::string* err) {
   static SmemAllowed allowed;
-  if (allow_smem(allowed, moe_route_kernel<VPL>, (size_t)kRouteWarps * 12 * 32 * VPL, "moe_route", err)) return -1;
+  if (allow_smem(allowed, moe_route_kernel<X, VPL>, (size_t)kRouteWarps * 20 * 32 * VPL, "moe_route", err)) return -1;
   const unsigned grid = (unsigned)((p.a.T + kRouteWarps - 1) / kRouteWarps);
-  return launch_pdl(moe_route_kernel<VPL>, dim3(grid), dim3(kRouteWarps * 32), (size_t)kRouteWarps * p.row_bytes, s, p, "moe_route", err);
+  return launch_pdl(moe_route_kernel<X, VPL>, dim3(grid), dim3(kRouteWarps * 32), (size_t)kRouteWarps * p.row_bytes, s, p, "moe_route", err);
+}
+template <typename X>
+int launch_route_of(const RouteParams& p, cudaStream_t s, std::string* err) {
+  const int n = (p.a.E + 31) / 32;
+  if (n <= 1) return launch_route<X, 1>(p, s, err);
+  if (n <= 2) return launch_route<X, 2>(p, s, err);
+  if (n <= 4) return launch_route<X, 4>(p, s, err);
+  if (n <= 8) return launch_route<X, 8>(p, s, err);
+  if (n <= 16) return launch_route<X, 16>(p, s, err);
+  return launch_route<X, 32>(p, s, err);
 }
 
 }  // namespace
@@ -362,14 +528,9 @@ int launch_moe_route(const MoeRouteArgs& a, cudaStream_t s, std::string* err) {
   RouteParams p;
   p.a = a;
   p.per_group = a.E / a.n_group;
-  p.row_bytes = 12 * ((a.E + 1) / 2 * 2);
-  const int vpl = (a.E + 31) / 32;
-  if (vpl <= 1) return launch_route<1>(p, s, err);
-  if (vpl <= 2) return launch_route<2>(p, s, err);
-  if (vpl <= 4) return launch_route<4>(p, s, err);
-  if (vpl <= 8) return launch_route<8>(p, s, err);
-  if (vpl <= 16) return launch_route<16>(p, s, err);
-  return launch_route<32>(p, s, err);
+  p.row_bytes = 20 * ((a.E + 1) / 2 * 2);
+  p.magic = (1 << 20) / p.per_group + 1;  // off by less than e / 2^20 < 1 / per_group
+  return a.x_dtype == KQ_F32 ? launch_route_of<float>(p, s, err) : launch_route_of<uint16_t>(p, s, err);
 }
 
 int launch_moe_plan(const int* ids, long long n, int E, int* offsets, int* order, cudaStream_t s, std::string* err) {
@@ -377,6 +538,7 @@ int launch_moe_plan(const int* ids, long long n, int E, int* offsets, int* order
   p.ids = ids;
   p.n = (int)n;
   p.E = E;
+  p.bits = 32 - __builtin_clz(E);
   p.offsets = offsets;
   p.order = order;
   // one CTA up to what its warps take in a few turns; a cluster's two barriers cost about a microsecond

@@ -69,7 +69,7 @@ __device__ __forceinline__ void store_part(uint16_t* row, const float (&v)[kPart
   if constexpr (VEC) {
     uint32_t w[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) w[i] = (uint32_t)f32_to_bf16_rn(v[2 * i]) | (uint32_t)f32_to_bf16_rn(v[2 * i + 1]) << 16;
+    for (int i = 0; i < 4; ++i) asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w[i]) : "f"(v[2 * i + 1]), "f"(v[2 * i]));
     *reinterpret_cast<uint4*>(row + 8 * c) = make_uint4(w[0], w[1], w[2], w[3]);
   } else {
 #pragma unroll
@@ -126,31 +126,35 @@ __global__ void __launch_bounds__(PARTS > 2 ? 1024 : 512) residual_norm_kernel(c
     }
   }
   auto norm = [&](float (&u)[PARTS][kPart], const void* w, float (*part)[32]) {
-    float s = 0.f, by = 1.f;
+    float s = 0.f, eps = a.eps;
 #pragma unroll
     for (int i = 0; i < PARTS; ++i)
 #pragma unroll
       for (int j = 0; j < kPart; ++j) s = __fmaf_rn(u[i][j], u[i][j], s);
     s = group_sum(s, part[0], p.group);
     if (s == INFINITY) {  // squares past fp32: the row again at 2^-96, next to which eps is nothing
-      s = 0.f, by = 0x1p-96f;
+      s = eps = 0.f;
 #pragma unroll
       for (int i = 0; i < PARTS; ++i)
 #pragma unroll
-        for (int j = 0; j < kPart; ++j) s = __fmaf_rn(u[i][j] * by, u[i][j] * by, s);
+        for (int j = 0; j < kPart; ++j) {
+          u[i][j] *= 0x1p-96f;
+          s = __fmaf_rn(u[i][j], u[i][j], s);
+        }
       s = group_sum(s, part[1], p.group);
     }
-    const float f = rsqrtf(s / (float)H + (by == 1.f ? a.eps : 0.f));
+    const float f = rsqrtf(s / (float)H + eps);
 #pragma unroll
     for (int i = 0; i < PARTS; ++i) {
       const int c = tid + i * p.group;
       if (c < parts) {
-        float g[kPart];
-        if (w) load_any<VEC>(g, w, a.w_dtype, c, H);
 #pragma unroll
-        for (int j = 0; j < kPart; ++j) {
-          const float k = !w ? 1.f : a.offset ? g[j] + 1.f : g[j];
-          u[i][j] = u[i][j] * by * f * k;
+        for (int j = 0; j < kPart; ++j) u[i][j] *= f;
+        if (w) {
+          float g[kPart];
+          load_any<VEC>(g, w, a.w_dtype, c, H);
+#pragma unroll
+          for (int j = 0; j < kPart; ++j) u[i][j] *= g[j] + a.offset;
         }
       }
     }
