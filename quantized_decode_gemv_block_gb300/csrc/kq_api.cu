@@ -151,9 +151,9 @@ int kq_device_errors(void) {
   if (vt == 0xFFFFFFFFu) return fail(KQ_ERR_CUDA, "reading the prefill error word");
   const unsigned int vk = kq::take_kv8_errors(), va = kq::take_kv8_append_errors();
   if (vk == 0xFFFFFFFFu || va == 0xFFFFFFFFu) return fail(KQ_ERR_CUDA, "reading the paged cache's error words");
-  const unsigned int vm = kq::take_moe_errors();
-  if (vm == 0xFFFFFFFFu) return fail(KQ_ERR_CUDA, "reading the experts' error word");
-  v |= vt | vk | va | vm;
+  const unsigned int vm = kq::take_moe_errors(), vx = kq::take_moe_tc_errors();
+  if (vm == 0xFFFFFFFFu || vx == 0xFFFFFFFFu) return fail(KQ_ERR_CUDA, "reading the experts' error word");
+  v |= vt | vk | va | vm | vx;
   ok();
   return static_cast<int>(v & 0x7FFFFFFFu);
 }

@@ -230,6 +230,10 @@ size_t moe_down_workspace(int fmt, int T, int k, int E, int H, int K);
 int launch_moe_gate_up(const MoeGemmArgs& a, int num_sms, cudaStream_t s, std::string* err);
 int launch_moe_down(const MoeGemmArgs& a, int num_sms, cudaStream_t s, std::string* err);
 unsigned int take_moe_errors();
+// The same products for many rows per expert, Q4_K (moe_gemm_tc.cu).
+size_t moe_tc_workspace(int P, int K);
+int launch_moe_tc(const MoeGemmArgs& a, bool gate_up, float* parts, void* ws, int num_sms, cudaStream_t s, std::string* err);
+unsigned int take_moe_tc_errors();
 
 // GPU quantizers (fp64 arithmetic).
 int launch_quantize(int fmt, const float* w, void* blocks, int N, int K, cudaStream_t stream,

@@ -592,7 +592,13 @@ int launch_stream(const CUtensorMap& tm, StreamParams& p, size_t smem, int num_s
   return 0;
 }
 
-int launch_products(const MoeGemmArgs& a, bool gate_up, float* parts, int num_sms, cudaStream_t s, std::string* err) {
+// Rows per expert on average from which the tensor-core product is faster (Q4_K).
+constexpr int kTcMean = 44;
+bool by_tensor_cores(int fmt, int T, int k, int E) { return fmt == FMT_Q4_K && (long long)T * k >= (long long)kTcMean * E; }
+
+// ws: of the tensor-core product
+int launch_products(const MoeGemmArgs& a, bool gate_up, float* parts, void* ws, int num_sms, cudaStream_t s, std::string* err) {
+  if (by_tensor_cores(a.fmt, a.T, a.k, a.E)) return launch_moe_tc(a, gate_up, parts, ws, num_sms, s, err);
   StreamParams p = {};
   p.w = static_cast<const uint8_t*>(a.w);
   p.x = static_cast<const uint16_t*>(a.x);
@@ -648,21 +654,23 @@ int launch_products(const MoeGemmArgs& a, bool gate_up, float* parts, int num_sm
 }  // namespace
 
 size_t moe_gate_up_workspace(int fmt, int T, int k, int E, int F, int K) {
-  (void)fmt, (void)T, (void)k, (void)E, (void)F, (void)K;
-  return 0;
+  (void)F;
+  return by_tensor_cores(fmt, T, k, E) ? moe_tc_workspace(T * k, K) : 0;
 }
+// The pairs' products, then the tensor-core product's own.
+static size_t down_parts(int T, int k, int H) { return ((size_t)T * k * H * 4 + 255) / 256 * 256; }
 size_t moe_down_workspace(int fmt, int T, int k, int E, int H, int K) {
-  (void)fmt, (void)E, (void)K;
-  return ((size_t)T * k * H * 4 + 255) / 256 * 256;
+  return down_parts(T, k, H) + (by_tensor_cores(fmt, T, k, E) ? moe_tc_workspace(T * k, K) : 0);
 }
 
 int launch_moe_gate_up(const MoeGemmArgs& a, int num_sms, cudaStream_t s, std::string* err) {
-  return launch_products(a, true, nullptr, num_sms, s, err);
+  return launch_products(a, true, nullptr, a.ws, num_sms, s, err);
 }
 
 int launch_moe_down(const MoeGemmArgs& a, int num_sms, cudaStream_t s, std::string* err) {
-  if (launch_products(a, false, static_cast<float*>(a.ws), num_sms, s, err)) return -1;
-  JoinParams p = {static_cast<const float*>(a.ws), a.weights, a.add, a.ids, a.y, a.add_stride, a.y_stride, a.T, a.k, a.N, a.E, a.y_dtype};
+  float* parts = static_cast<float*>(a.ws);
+  if (launch_products(a, false, parts, static_cast<uint8_t*>(a.ws) + down_parts(a.T, a.k, a.N), num_sms, s, err)) return -1;
+  JoinParams p = {parts, a.weights, a.add, a.ids, a.y, a.add_stride, a.y_stride, a.T, a.k, a.N, a.E, a.y_dtype};
   const int V = a.N % 4 == 0 ? 4 : 1;
   const long long n = (long long)a.T * (a.N / V);
   const dim3 grid((unsigned)std::min<long long>((n + 255) / 256, (long long)num_sms * 16));

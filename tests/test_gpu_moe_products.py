@@ -162,6 +162,102 @@ def test_a_pair_has_the_bits_it_has_alone(fmt):
     assert torch.equal(gate_up(fmt, w1, p1, x, one, F)[8:10], act[8:10])
 
 
+def many_ids(counts, seed=0):
+    """Ids of one choice per token: counts[e] tokens for expert e, in a random order."""
+    ids = np.concatenate([np.full(n, e, np.int32) for e, n in enumerate(counts)])
+    return np.random.default_rng(seed).permutation(ids)[:, None].copy()
+
+
+@pytest.mark.parametrize("counts", [(33,), (64,), (65,), (255,), (256,), (257,), (513, 1), (40, 0, 31, 300, 32, 33, 0), (100, 150, 200, 250),
+                                    (700, 3, 3, 3), (48,) * 16])
+@pytest.mark.parametrize("K", [256, 768, 1280])
+def test_many_rows_of_an_expert(counts, K):
+    """Q4_K experts of more than 32 rows go to the tensor-core product where a call has many rows; the others beside them do not."""
+    E, F, H = len(counts), 128, 256
+    ids = many_ids(counts)
+    w, p = experts("q4_k", E, 2 * F, K)
+    gate_up("q4_k", w, p, bf16(len(ids), K), ids, F)
+    w, p = experts("q4_k", E, H, K)
+    down("q4_k", w, p, bf16(len(ids), K), ids, some_weights(len(ids), 1), H)
+
+
+@pytest.mark.parametrize("N", [1, 8, 40, 63, 64, 65, 127, 128, 129, 200, 320])
+def test_many_rows_of_odd_matrices(N):
+    E, K = 3, 512
+    ids = many_ids((70, 90, 130))
+    w, p = experts("q4_k", E, 2 * N, K)
+    gate_up("q4_k", w, p, bf16(len(ids), K), ids, N)
+    w, p = experts("q4_k", E, N, K)
+    down("q4_k", w, p, bf16(len(ids), K), ids, some_weights(len(ids), 1), N)
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+def test_many_rows_several_choices_and_empty_slots(fmt):
+    ids = both(fmt, 150, 3, 8, 512, 256, none=0.1)
+    assert (ids < 0).any()
+
+
+def test_many_rows_of_long_k():
+    E, F = 2, 64
+    ids = many_ids((60, 45))
+    w, p = experts("q4_k", E, 2 * F, 5376)
+    gate_up("q4_k", w, p, bf16(len(ids), 5376), ids, F)
+
+
+def test_many_rows_with_special_values():
+    """Rows of zeros, of tiny and of huge values, and of NaN and infinity beside plain ones."""
+    E, F, K = 2, 128, 512
+    ids = many_ids((80, 60))
+    w, p = experts("q4_k", E, 2 * F, K)
+    x = bf16(len(ids), K)
+    x[3] = 0
+    x[5] *= 1e-30
+    x[9] *= 1e15
+    x[11, 200:] *= 1e-6
+    clean = gate_up("q4_k", w, p, x, ids, F)
+    x[20, 7], x[21, 300] = float("nan"), float("inf")
+    out = kq.moe_gate_up("q4_k", w, x, kq.moe_plan(dev(ids), E), F, K)
+    keep = [t for t in range(len(ids)) if t not in (20, 21)]
+    assert torch.equal(out[keep], clean[keep]) and out[20].isnan().all() and not out[21].isfinite().all()
+
+
+def test_many_rows_in_a_plan_out_of_bounds():
+    E, F, K = 4, 64, 256
+    ids = many_ids((50, 60, 70, 40))
+    w, p = experts("q4_k", E, 2 * F, K)
+    x = bf16(len(ids), K)
+    good = kq.moe_plan(dev(ids), E)
+    want = gate_up("q4_k", w, p, x, ids, F)
+    assert kq.device_errors() == 0
+    for change in ("order", "offsets", "negative"):
+        order, off = good.order.clone(), good.offsets.clone()
+        if change == "order":
+            order[0], order[77] = len(ids), -5
+        elif change == "offsets":
+            off[E] = len(ids) + 1
+        else:
+            off[0] = -1
+        act = torch.full((len(ids), F), 3.0, dtype=torch.bfloat16, device="cuda")
+        kq.moe_gate_up("q4_k", w, x, kq.MoePlan(off, order), F, K, act=act)
+        assert kq.device_errors() == 2, change
+        same = (act == want).all(1)
+        assert (same | (act == 3.0).all(1)).all() and not same.all() and same.any()
+
+
+def test_many_rows_twice_give_the_same_bits_on_two_streams():
+    E, F, K = 6, 256, 512
+    ids = many_ids((90, 33, 500, 10, 64, 200))
+    w, p = experts("q4_k", E, 2 * F, K)
+    x, plan = bf16(len(ids), K), kq.moe_plan(dev(ids), E)
+    want = gate_up("q4_k", w, p, x, ids, F)
+    torch.cuda.synchronize()
+    streams, got = [torch.cuda.Stream() for _ in range(2)], []
+    for _ in range(4):
+        got += [kq.moe_gate_up("q4_k", w, x, plan, F, K, stream=s) for s in streams]
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, want) for a in got)
+
+
 def test_products_agree_with_gemv():
     E, H, K, T = 3, 520, 2560, 4
     ids = np.array([[0], [2], [1], [2]], np.int32)
