@@ -582,11 +582,12 @@ _SCORES = {"softmax": 0, "sigmoid": KQ_ROUTE_SIGMOID}
 _GROUP_SCORES = {"max": 0, "top2": KQ_ROUTE_GROUP_TOP2}
 
 
-def _device() -> int:
-    """The current device's index, -1 where there is none: what get_device() says of a tensor that a kernel may take."""
+def _where(stream):
+    """The current device's index (-1 where there is none: what get_device() says of a tensor in host memory) and the raw stream."""
     if torch.cuda.is_initialized():
-        return torch._C._cuda_getDevice()
-    return torch.cuda.current_device() if torch.cuda.is_available() else -1
+        dev = torch._C._cuda_getDevice()
+        return dev, torch._C._cuda_getCurrentRawStream(dev) if stream is None else _stream(stream)
+    return torch.cuda.current_device() if torch.cuda.is_available() else -1, _stream(stream)
 
 
 def _here(name: str, t: torch.Tensor, dev: int) -> int:
@@ -644,7 +645,7 @@ def residual_norm(h: torch.Tensor | None, y: torch.Tensor | None, post=None, gat
     if len(shape) != 2:
         raise ValueError("h and y must be (tokens, H)")
     T, H = shape
-    dev = _device()
+    dev, raw = _where(stream)
     h_dtype = (ref if h is None else h).dtype
     flags = KQ_NORM_UNIT_OFFSET if unit_offset else 0
     yp = ys = hp = hs = gp = gs = xp = xs = post_p = pre_p = 0
@@ -690,7 +691,7 @@ def residual_norm(h: torch.Tensor | None, y: torch.Tensor | None, post=None, gat
     elif x_out is not None:
         raise ValueError("x_out without pre")
     _check(lib().kq_residual_norm(_dtype(ref.dtype), yp, ys, _dtype(h_dtype), hp, hs, hop, hos, gp, gs, scale, _dtype(w_dtype), post_p,
-                                  pre_p, eps, x_code, xp, xs, T, H, flags, _stream(stream)))
+                                  pre_p, eps, x_code, xp, xs, T, H, flags, raw))
     return h_out, x_out
 
 
@@ -706,7 +707,7 @@ def moe_route(logits: torch.Tensor, k: int, score: str = "softmax", bias: torch.
     T, E = shape
     if score not in _SCORES or group_score not in _GROUP_SCORES:
         raise ValueError("score must be softmax or sigmoid, group_score max or top2")
-    dev = _device()
+    dev, raw = _where(stream)
     xp, xs = _here("logits", logits, dev), _rows("logits", logits, shape)
     bp = 0 if bias is None else _flat("bias", bias, torch.float32, (E,), dev)
     out = (T, max(k, 0))
@@ -721,7 +722,7 @@ def moe_route(logits: torch.Tensor, k: int, score: str = "softmax", bias: torch.
     else:
         wp = _flat("weights", weights, torch.float32, out, dev)
     flags = _SCORES[score] | _GROUP_SCORES[group_score] | (KQ_ROUTE_RENORM if renorm else 0)
-    _check(lib().kq_moe_route(_dtype(logits.dtype), xp, xs, T, E, k, bp, n_group, top_group, scale, flags, ip, wp, _stream(stream)))
+    _check(lib().kq_moe_route(_dtype(logits.dtype), xp, xs, T, E, k, bp, n_group, top_group, scale, flags, ip, wp, raw))
     return ids, weights
 
 
@@ -743,7 +744,7 @@ def moe_plan(ids: torch.Tensor, n_experts: int, out: MoePlan | None = None, stre
     if ids.dim() != 2:
         raise ValueError("ids must be (tokens, choices)")
     T, k = ids.shape
-    dev = _device()
+    dev, raw = _where(stream)
     ip = _flat("ids", ids, _I32, (T, k), dev)
     if out is None:
         out = MoePlan.__new__(MoePlan)
@@ -753,7 +754,7 @@ def moe_plan(ids: torch.Tensor, n_experts: int, out: MoePlan | None = None, stre
     else:
         fp = _flat("out.offsets", out.offsets, _I32, (n_experts + 1,), dev)
         op = _flat("out.order", out.order, _I32, (T * k,), dev)
-    _check(lib().kq_moe_plan(ip, T, k, n_experts, fp, op, _stream(stream)))
+    _check(lib().kq_moe_plan(ip, T, k, n_experts, fp, op, raw))
     return out
 
 
@@ -793,7 +794,7 @@ def moe_gate_up(fmt, w: torch.Tensor, x: torch.Tensor, plan: MoePlan, F: int, K:
     if x.dim() != 2 or x.dtype is not torch.bfloat16:
         raise ValueError("x must be (tokens, K) bf16")
     T = x.shape[0]
-    dev = _device()
+    dev, raw = _where(stream)
     wp, E, fp, op = _experts(w, plan, 2 * F, fmt, K, dev)
     xp, xs = _here("x", x, dev), _rows("x", x, (T, K))
     n = plan.order.shape[0]
@@ -809,7 +810,7 @@ def moe_gate_up(fmt, w: torch.Tensor, x: torch.Tensor, plan: MoePlan, F: int, K:
         size = moe_gate_up_workspace_size(fmt, T, k, E, F, K)
         workspace = _empty(max(size, 256), torch.uint8, x.device, stream)
     wsp, wsn = _workspace(workspace, dev)
-    _check(lib().kq_moe_gate_up(fmt, wp, xp, xs, fp, op, T, k, E, F, K, ap, wsp, wsn, _stream(stream)))
+    _check(lib().kq_moe_gate_up(fmt, wp, xp, xs, fp, op, T, k, E, F, K, ap, wsp, wsn, raw))
     return act
 
 
@@ -823,7 +824,7 @@ def moe_down(fmt, w: torch.Tensor, act: torch.Tensor, plan: MoePlan, ids: torch.
     if ids.dim() != 2:
         raise ValueError("ids must be (tokens, choices)")
     shape = T, k = ids.shape
-    dev = _device()
+    dev, raw = _where(stream)
     wp, E, fp, op = _experts(w, plan, H, fmt, K, dev)
     if plan.order.shape[0] != T * k:
         raise ValueError("the plan must be that of the ids")
@@ -845,7 +846,7 @@ def moe_down(fmt, w: torch.Tensor, act: torch.Tensor, plan: MoePlan, ids: torch.
         size = moe_down_workspace_size(fmt, T, k, E, H, K)
         workspace = _empty(max(size, 256), torch.uint8, act.device, stream)
     wsp, wsn = _workspace(workspace, dev)
-    _check(lib().kq_moe_down(fmt, wp, ap, fp, op, ip, tp, T, k, E, H, K, dp, ds, _dtype(y.dtype), yp, ys, wsp, wsn, _stream(stream)))
+    _check(lib().kq_moe_down(fmt, wp, ap, fp, op, ip, tp, T, k, E, H, K, dp, ds, _dtype(y.dtype), yp, ys, wsp, wsn, raw))
     return y
 
 

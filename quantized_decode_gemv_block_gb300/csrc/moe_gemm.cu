@@ -22,6 +22,7 @@
 #include "kq_device.cuh"
 #include "kq_internal.h"
 #include "kq_launch.cuh"
+#include "moe.cuh"
 
 namespace cg = cooperative_groups;
 
@@ -298,7 +299,7 @@ struct Stream {
     if (pair < 0) return;
     if (p.half) {
       const int i = tile * 8 + g;
-      if (i < p.half) p.act[(long long)pair * p.half + i] = silu_mul_bf16(a, b);
+      if (i < p.half) p.act[(long long)pair * p.half + i] = silu_mul(a, b);
     } else {
       const int n = tile * 16 + g;
       float* o = p.y + (long long)pair * p.N + n;
@@ -326,7 +327,7 @@ __global__ void __launch_bounds__(kThreads, 1) moe_stream_kernel(const __grid_co
   grid_dependency_wait();
 
   // Chunks of the experts before each one. A plan out of bounds leaves its experts without any.
-  constexpr int kPer = KQ_MOE_MAX_EXPERTS / kThreads;
+  constexpr int kPer = (KQ_MOE_MAX_EXPERTS + kThreads - 1) / kThreads;
   int n[kPer], mine = 0;
 #pragma unroll
   for (int i = 0; i < kPer; ++i) {
@@ -517,7 +518,7 @@ bool stream_layout(int fmt, StreamParams* p, size_t* smem) {
     if (fmt != FMT_Q6_K && stride / 4 > 256) continue;  // a tensor copy's box
     const size_t stage = (size_t)kWarps * 16 * stride;
     const int depth = off >= (size_t)kStreamSmem ? 0 : (int)std::min<size_t>(8, ((size_t)kStreamSmem - off) / stage);
-    if (depth < (su > 1 ? 3 : 2)) continue;
+    if (depth < 2) continue;
     p->su = su;
     p->depth = depth;
     p->row_stride = stride;
@@ -620,7 +621,16 @@ int launch_products(const MoeGemmArgs& a, bool gate_up, float* parts, void* ws, 
   while ((p.units + p.C - 1) / p.C > kMaxSliceUnits) p.C *= 2;
   p.chunk = std::min(kMaxChunk, a.T);  // a token chooses an expert once; where it does twice there are more chunks
   size_t smem = 0;
-  if (p.C > kMaxCluster || !stream_layout(a.fmt, &p, &smem)) {
+  bool fits = p.C <= kMaxCluster && stream_layout(a.fmt, &p, &smem);
+  if (fits && p.chunk > 8 && p.P <= 4 * a.E) {
+    // few rows per expert: chunks of eight where that leaves room for longer stages (37 tokens, 4 of 60 experts in Q8_0, 2560 x
+    // 1280: stages of one unit 82 us, of two 69)
+    StreamParams q = p;
+    q.chunk = 8;
+    size_t n = 0;
+    if (stream_layout(a.fmt, &q, &n) && q.su > p.su) p = q, smem = n;
+  }
+  if (!fits) {
     *err = "internal: the product does not fit shared memory";
     return -1;
   }

@@ -26,6 +26,7 @@
 #include "kq_device.cuh"
 #include "kq_internal.h"
 #include "kq_launch.cuh"
+#include "moe.cuh"
 
 namespace cg = cooperative_groups;
 
@@ -534,8 +535,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTcThreads, 1)
               const float o = __shfl_xor_sync(0xFFFFFFFFu, low ? v1 : v0, 16);
               const float g = low ? v0 : o, u = low ? o : v1;
               const uint32_t q = low ? t0 : t1;
-              // silu by the fast exponential and division: within 2^-20 of itself, next to the rounding to bf16
-              if (nok && q != kNoPair) act[(size_t)(q & 0x7FFFFFu) * p.half] = f32_to_bf16_rn(__fdividef(g, 1.f + __expf(-g)) * u);
+              if (nok && q != kNoPair) act[(size_t)(q & 0x7FFFFFu) * p.half] = silu_mul(g, u);
             } else if (nok) {
               if (t0 != kNoPair) __stcs(y + (size_t)(t0 & 0x7FFFFFu) * p.N, v0);
               if (t1 != kNoPair) __stcs(y + (size_t)(t1 & 0x7FFFFFu) * p.N, v1);
