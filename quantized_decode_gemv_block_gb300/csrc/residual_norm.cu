@@ -213,7 +213,7 @@ int launch_residual_norm(const ResidualNormArgs& a, cudaStream_t s, std::string*
   const int parts = (a.H + kPart - 1) / kPart;
   // Parts of a thread. What counts is how many rows are in flight: at 4096 four parts in 64 registers (8192 rows with a gate 81 us) beat
   // two with everything asked for at once (90), at 2560 two (54) beat four (57), at 2048 two (39) one (45)
-  const int n = parts <= 64 ? 1 : parts <= 384 ? 2 : 4;
+  const int n = parts <= 64 ? 1 : parts <= 400 ? 2 : 4;
   p.group = ((parts + n - 1) / n + 31) / 32 * 32;
   p.rows = p.group >= 256 ? 1 : 256 / p.group;
   // wide loads: every row of every array that is there starts on a part's boundary
