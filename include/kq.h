@@ -529,11 +529,15 @@ int kq_moe_plan(const int* ids, int T, int k, int E, int* offsets, int* order, v
  *   offsets, order  from kq_moe_plan
  *   act      T * k rows of F bf16, 16-byte aligned (output); rows of pairs outside the plan stay as they are
  *   workspace  kq_moe_gate_up_workspace_size() bytes, 256-byte aligned (NULL where that is 0)
- * Products and sums as kq_gemv's (fp32, exact products), g and u are not rounded before silu.
- * A pair's bits depend on its row and expert alone. K is a multiple of 256 up to 20480. Q6_K needs
- * E * 2F * row bytes to be a multiple of 16. A plan outside its bounds (offsets that fall or pass T * k, pairs outside
- * 0..T*k-1) sets bit 1 of kq_device_errors(), and the experts or pairs concerned are not computed.
+ * Products are exact and sums fp32, as kq_gemv's; g and u are not rounded before silu, which is formed within 2^-20 of
+ * itself. A pair's bits depend on its row and expert alone, whatever else the call holds, with one exception: Q4_K
+ * calls of KQ_MOE_TC_ROWS or more pairs per expert on average (T * k >= KQ_MOE_TC_ROWS * E) run on the tensor cores as
+ * kq_gemm's long prompts do, where a pair's bits depend on its row and expert alone too but are not those of smaller
+ * calls; 64 * dmin * m has to be below 65504 there. K is a multiple of 256 up to 20480. Q6_K needs E * 2F * row bytes to be
+ * a multiple of 16. A plan outside its bounds (offsets that fall or pass T * k, pairs outside 0..T*k-1) sets bit 1 of
+ * kq_device_errors(), and the experts or pairs concerned are not computed. One launch, or two on the tensor cores.
  * Errors: KQ_ERR_ARG, KQ_ERR_UNSUPPORTED, KQ_ERR_WORKSPACE, KQ_ERR_CUDA. */
+enum { KQ_MOE_TC_ROWS = 44 };
 size_t kq_moe_gate_up_workspace_size(int fmt, int T, int k, int E, int F, int K);
 int kq_moe_gate_up(int fmt, const void* w, const void* x, long long x_stride, const int* offsets, const int* order, int T,
                    int k, int E, int F, int K, void* act, void* workspace, size_t ws_bytes, void* stream);
@@ -544,7 +548,7 @@ int kq_moe_gate_up(int fmt, const void* w, const void* x, long long x_stride, co
  *   add      T rows of H fp32, add_stride elements apart (a shared expert's output, the residual), or NULL
  *   y        T rows of H (y_dtype), y_stride elements apart; may be add (same stride, fp32)
  *   workspace  kq_moe_down_workspace_size() bytes, 256-byte aligned
- * The sum over choices is fp32, in order. Otherwise as kq_moe_gate_up. */
+ * The sum over choices is fp32, in order. One launch more than kq_moe_gate_up, and otherwise as that. */
 size_t kq_moe_down_workspace_size(int fmt, int T, int k, int E, int H, int K);
 int kq_moe_down(int fmt, const void* w, const void* act, const int* offsets, const int* order, const int* ids,
                 const float* weights, int T, int k, int E, int H, int K, const float* add, long long add_stride, int y_dtype,

@@ -593,9 +593,9 @@ int launch_stream(const CUtensorMap& tm, StreamParams& p, size_t smem, int num_s
   return 0;
 }
 
-// Rows per expert on average from which the tensor-core product is faster (Q4_K).
-constexpr int kTcMean = 44;
-bool by_tensor_cores(int fmt, int T, int k, int E) { return fmt == FMT_Q4_K && (long long)T * k >= (long long)kTcMean * E; }
+// From KQ_MOE_TC_ROWS rows per expert on average the tensor-core product is faster: 128 experts of 2 x 768 x 2048, rows per expert
+// (streaming, tensor cores) 32: 186, 227 us; 48: 255, 238; 128: 597, 292; 8 experts of 2 x 2048 x 4096, 24: 68, 85; 40: 94, 87.
+bool by_tensor_cores(int fmt, int T, int k, int E) { return fmt == FMT_Q4_K && (long long)T * k >= (long long)KQ_MOE_TC_ROWS * E; }
 
 // ws: of the tensor-core product
 int launch_products(const MoeGemmArgs& a, bool gate_up, float* parts, void* ws, int num_sms, cudaStream_t s, std::string* err) {

@@ -233,7 +233,7 @@ __device__ __noinline__ int largest_keys(long long* keys, int E, int k) {
 }
 
 template <typename X, int VPL>
-__global__ void __launch_bounds__(kRouteWarps * 32, VPL <= 8 ? 10 : 1) moe_route_kernel(const __grid_constant__ RouteParams p) {
+__global__ void __launch_bounds__(kRouteWarps * 32, VPL <= 8 ? 8 : 1) moe_route_kernel(const __grid_constant__ RouteParams p) {
   extern __shared__ __align__(16) uint8_t smem[];
   const MoeRouteArgs& a = p.a;
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
@@ -282,19 +282,20 @@ __global__ void __launch_bounds__(kRouteWarps * 32, VPL <= 8 ? 10 : 1) moe_route
     const float rest = a.softmax ? __fdividef(1.f, sum) : 1.f;
 #pragma unroll
     for (int i = 0; i < VPL; ++i) {
+      const int e = 32 * i + lane;
       const float s = a.softmax ? __expf(x[i] - top) * rest : __fdividef(1.f, 1.f + __expf(-x[i]));
-      const float b = 32 * i + lane < a.E ? s + bias(32 * i + lane) : -INFINITY;
-      c.key[i] = x[i] > -INFINITY && b > -INFINITY ? key_of(b) : kNone;
+      float f = -INFINITY;
+      if (e < a.E) {
+        f = x[i] > -INFINITY ? s + bias(e) : -INFINITY;
+        f = f > -INFINITY ? f : -INFINITY;  // NaN
+        cs[e] = f;
+      }
+      c.key[i] = key_of(f);
     }
+    __syncwarp();
   } else {
 #pragma unroll
     for (int i = 0; i < VPL; ++i) c.key[i] = key_of(x[i]);
-  }
-  if (by_score) {
-#pragma unroll
-    for (int i = 0; i < VPL; ++i)
-      if (32 * i + lane < a.E) cs[32 * i + lane] = of_key(c.key[i]);
-    __syncwarp();
   }
   if (a.n_group > 1) {
     bool sure = true;
@@ -316,12 +317,11 @@ __global__ void __launch_bounds__(kRouteWarps * 32, VPL <= 8 ? 10 : 1) moe_route
     }
   }
 
-  int id = -1;  // lane j holds choice j
-  bool sure = true;
+  int id = -1;  // lane j holds choice j and its key; with a bias one more is taken, for the last gap
+  uint32_t mine = kNone, next = kNone;
+  int next_e = 0;
   c.ready();
-  uint32_t last = 0;
-  int last_e = 0;
-  const int rounds = a.bias ? min(a.k + 1, a.E) : a.k;  // one more, for the last gap
+  const int rounds = a.bias ? min(a.k + 1, a.E) : a.k;
   for (int j = 0; j < rounds; ++j) {
     uint32_t k;
     int i;
@@ -329,16 +329,21 @@ __global__ void __launch_bounds__(kRouteWarps * 32, VPL <= 8 ? 10 : 1) moe_route
     const uint32_t key = __reduce_max_sync(kAll, k);
     if (key == kNone) break;
     const int e = (int)__reduce_min_sync(kAll, k == key ? (unsigned)(32 * i + lane) : kAll);
-    if (a.bias && j > 0) {
-      const float before = of_key(last);
-      if (before - of_key(key) <= 2.f * off_by(before) && !(xs[last_e] == xs[e] && a.bias[last_e] == a.bias[e])) sure = false;
-    }
-    if (j < a.k) {
-      if (lane == j) id = e;
-      last = key;
-      last_e = e;
-    }
+    if (j == a.k) next = key, next_e = e;
+    else if (lane == j) id = e, mine = key;
     if (lane == (e & 31)) c.pop(i);
+  }
+  bool sure = true;
+  uint32_t last = kNone;  // the last choice's key
+  if (a.bias) {
+    const uint32_t k = __shfl_down_sync(kAll, mine, 1);
+    const int e = __shfl_down_sync(kAll, id, 1);
+    last = __reduce_min_sync(kAll, id >= 0 ? mine : kAll);
+    if (lane < a.k - 1) next = k, next_e = e;
+    const float f = of_key(mine), g = of_key(next);
+    const bool close = id >= 0 && lane < a.k && next != kNone && f - g <= 2.f * off_by(f) &&
+                       !(xs[id] == xs[next_e] && a.bias[id] == a.bias[next_e]);
+    sure = !__any_sync(kAll, close);
   }
   if (!sure) {  // a.bias: again from the exact choices down to the last one's reach
     __syncwarp();

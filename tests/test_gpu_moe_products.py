@@ -172,7 +172,7 @@ def many_ids(counts, seed=0):
                                     (700, 3, 3, 3), (48,) * 16])
 @pytest.mark.parametrize("K", [256, 768, 1280])
 def test_many_rows_of_an_expert(counts, K):
-    """Q4_K experts of more than 32 rows go to the tensor-core product where a call has many rows; the others beside them do not."""
+    """Q4_K calls of many rows per expert (44 on average) run on the tensor cores, experts of few rows or none among them."""
     E, F, H = len(counts), 128, 256
     ids = many_ids(counts)
     w, p = experts("q4_k", E, 2 * F, K)
@@ -195,6 +195,25 @@ def test_many_rows_of_odd_matrices(N):
 def test_many_rows_several_choices_and_empty_slots(fmt):
     ids = both(fmt, 150, 3, 8, 512, 256, none=0.1)
     assert (ids < 0).any()
+
+
+def test_many_rows_keep_a_pairs_bits():
+    """A row's bits on the tensor cores, whatever rows stand before, behind and beside it in its expert's tiles."""
+    E, F, H, K = 3, 128, 256, 768
+    w1, p1 = experts("q4_k", E, 2 * F, K)
+    w2, p2 = experts("q4_k", E, H, K, 1)
+    x = bf16(700, K)
+    outs = []
+    for order in (np.arange(700), np.random.default_rng(2).permutation(700), np.arange(150)):
+        ids = (np.arange(700) * 7 % 13 % E).astype(np.int32)[order][:, None].copy()
+        rows = x[torch.tensor(order, device="cuda")].contiguous()
+        a = gate_up("q4_k", w1, p1, rows, ids, F)
+        y = down("q4_k", w2, p2, rows, ids, torch.ones((len(order), 1), device="cuda"), H)
+        back = torch.tensor(np.argsort(order), device="cuda")
+        outs.append((a[back], y[back]))
+    for a, y in outs[1:]:
+        n = len(a)
+        assert torch.equal(a, outs[0][0][:n]) and torch.equal(y, outs[0][1][:n])
 
 
 def test_many_rows_of_long_k():
