@@ -631,6 +631,11 @@ def _weights(name: str, t: torch.Tensor, H: int, dev: int) -> int:
     return _here(name, t, dev)
 
 
+def _empty_rows(like: torch.Tensor, dtype, stream) -> torch.Tensor:
+    """An output of the shape of `like`, whose rows are contiguous (see _empty; empty_like takes a microsecond less)."""
+    return torch.empty_like(like, dtype=dtype) if stream is None else _empty(like.shape, dtype, like.device, stream)
+
+
 def residual_norm(h: torch.Tensor | None, y: torch.Tensor | None, post=None, gate: torch.Tensor | None = None, scale: float = 1.0,
                   pre=None, eps: float = 1e-6, unit_offset: bool = False, x_dtype=None, h_out: torch.Tensor | None = None,
                   x_out: torch.Tensor | None = None, stream=None):
@@ -668,7 +673,7 @@ def residual_norm(h: torch.Tensor | None, y: torch.Tensor | None, post=None, gat
         if post is not True:
             post_p, w_dtype = _weights("post", post, H, dev), post.dtype
     if h_out is None:
-        h_out, hos = _empty(shape, h_dtype, ref.device, stream), H
+        h_out, hos = _empty_rows(ref, h_dtype, stream), H
         hop = h_out.data_ptr()
     else:
         if h_out.dtype is not h_dtype and h is not None:
@@ -681,7 +686,7 @@ def residual_norm(h: torch.Tensor | None, y: torch.Tensor | None, post=None, gat
                 raise ValueError("post and pre must agree in type")
             pre_p, w_dtype = _weights("pre", pre, H, dev), pre.dtype
         if x_out is None:
-            x_out, xs = _empty(shape, x_dtype or torch.bfloat16, ref.device, stream), H
+            x_out, xs = _empty_rows(ref, x_dtype or torch.bfloat16, stream), H
             xp = x_out.data_ptr()
         else:
             if x_dtype is not None and x_out.dtype is not x_dtype:
