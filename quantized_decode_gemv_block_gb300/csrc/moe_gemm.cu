@@ -454,21 +454,31 @@ __global__ void __launch_bounds__(256) moe_join_kernel(const JoinParams p) {
     float s[V];
 #pragma unroll
     for (int v = 0; v < V; ++v) s[v] = p.add ? p.add[t * p.add_stride + h + v] : 0.f;
-    for (int j = 0; j < p.k; ++j) {
-      const int id = p.ids[t * p.k + j];
-      if (id < 0 || id >= p.E) continue;
-      const float w = p.weights[t * p.k + j];
-      const float* src = p.part + (t * p.k + j) * p.H + h;
-      if constexpr (V == 4) {
-        const float4 a = __ldcs(reinterpret_cast<const float4*>(src));
-        s[0] = __fmaf_rn(w, a.x, s[0]);
-        s[1] = __fmaf_rn(w, a.y, s[1]);
-        s[2] = __fmaf_rn(w, a.z, s[2]);
-        s[3] = __fmaf_rn(w, a.w, s[3]);
-      } else {
+    // eight choices at a time, all read without a condition so that the reads are in flight together (the rows are in the
+    // workspace whatever they hold); a choice without an expert adds nothing
+    for (int j0 = 0; j0 < p.k; j0 += 8) {
+      float w[8], r[8][V];
+      int id[8];
 #pragma unroll
-        for (int v = 0; v < V; ++v) s[v] = __fmaf_rn(w, src[v], s[v]);
+      for (int j = 0; j < 8; ++j) {
+        const long long pair = t * p.k + min(j0 + j, p.k - 1);
+        id[j] = p.ids[pair];
+        w[j] = p.weights[pair];
+        const float* src = p.part + pair * p.H + h;
+        if constexpr (V == 4) {
+          const float4 a = __ldcs(reinterpret_cast<const float4*>(src));
+          r[j][0] = a.x, r[j][1] = a.y, r[j][2] = a.z, r[j][3] = a.w;
+        } else {
+#pragma unroll
+          for (int v = 0; v < V; ++v) r[j][v] = src[v];
+        }
       }
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        if (j0 + j < p.k && id[j] >= 0 && id[j] < p.E) {
+#pragma unroll
+          for (int v = 0; v < V; ++v) s[v] = __fmaf_rn(w[j], r[j][v], s[v]);
+        }
     }
 #pragma unroll
     for (int v = 0; v < V; ++v) {

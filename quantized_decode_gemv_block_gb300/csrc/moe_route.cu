@@ -245,7 +245,7 @@ __global__ void __launch_bounds__(kRouteWarps * 32, VPL <= 8 ? 8 : 1) moe_route_
   grid_dependency_wait();
   if (t >= a.T) return;
 
-  float x[VPL];  // expert 32 i + lane
+  float x[VPL], b[VPL];  // of expert 32 i + lane: logit, and bias, asked for together
   const X* row = static_cast<const X*>(a.x) + t * a.xs + lane;
   uint32_t most = kNone;
 #pragma unroll
@@ -256,6 +256,7 @@ __global__ void __launch_bounds__(kRouteWarps * 32, VPL <= 8 ? 8 : 1) moe_route_
       else v = __uint_as_float((uint32_t)row[32 * i] << 16);
     }
     x[i] = v;
+    b[i] = a.bias && 32 * i + lane < a.E ? a.bias[32 * i + lane] : 0.f;
   }
 #pragma unroll
   for (int i = 0; i < VPL; ++i) {
@@ -274,7 +275,6 @@ __global__ void __launch_bounds__(kRouteWarps * 32, VPL <= 8 ? 8 : 1) moe_route_
 #pragma unroll
     for (int d = 16; d > 0; d /= 2) sum += __shfl_xor_sync(kAll, sum, d);
   }
-  auto bias = [&](int e) { return a.bias ? a.bias[e] : 0.f; };
 
   // c: what is compared; an expert that can be chosen has a logit, and a bias that is not -inf or NaN
   Lane<VPL> c;
@@ -286,7 +286,7 @@ __global__ void __launch_bounds__(kRouteWarps * 32, VPL <= 8 ? 8 : 1) moe_route_
       const float s = a.softmax ? __expf(x[i] - top) * rest : __fdividef(1.f, 1.f + __expf(-x[i]));
       float f = -INFINITY;
       if (e < a.E) {
-        f = x[i] > -INFINITY ? s + bias(e) : -INFINITY;
+        f = x[i] > -INFINITY ? s + b[i] : -INFINITY;
         f = f > -INFINITY ? f : -INFINITY;  // NaN
         cs[e] = f;
       }

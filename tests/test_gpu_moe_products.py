@@ -47,7 +47,8 @@ def gate_up(fmt, w, wp, x, ids, F, **kw):
     e = ids.reshape(-1)
     y, b = product(wp, x.repeat_interleave(k, 0), e)
     g, u, dg, du = y[:, :F], y[:, F:], TOL * b[:, :F], TOL * b[:, F:]
-    silu = g / (1 + np.exp(-g))
+    with np.errstate(over="ignore"):
+        silu = g / (1 + np.exp(-g))
     ref = silu * u
     tol = 1.1 * dg * np.abs(u) + (np.abs(silu) + 1.1 * dg) * du + 8 * U * np.abs(ref)
     tol += (np.abs(ref) + tol) * 2.0 ** -8 + 2.0 ** -126
