@@ -110,6 +110,22 @@ def test_lengths(fmt, K):
     down(fmt, w, p, bf16(T * k, K), ids, some_weights(T, k), N)
 
 
+@pytest.mark.parametrize("fmt", FORMATS)
+def test_the_longest_rows(fmt):
+    E, T, k, N, K = 1, 17, 1, 24, 20480
+    ids = some_ids(T, k, E)
+    w, p = experts(fmt, E, 2 * N, K)
+    gate_up(fmt, w, p, bf16(T, K), ids, N)
+
+
+@pytest.mark.parametrize("T,k", [(1, 32), (40, 3)])
+def test_the_most_experts(T, k):
+    E, N, K = 1024, 8, 256
+    ids = some_ids(T, k, E)
+    w, p = experts("q4_k", E, 2 * N, K)
+    gate_up("q4_k", w, p, bf16(T, K), ids, N)
+
+
 @pytest.mark.parametrize("fmt", ["q4_k", "q6_k", "affine4"])
 @pytest.mark.parametrize("N", [8, 24, 56, 136])
 def test_rows_that_end_inside_a_tile(fmt, N):
@@ -215,6 +231,14 @@ def test_many_rows_keep_a_pairs_bits():
     for a, y in outs[1:]:
         n = len(a)
         assert torch.equal(a, outs[0][0][:n]) and torch.equal(y, outs[0][1][:n])
+
+
+def test_many_rows_of_the_most_experts():
+    E, N, K, T, k = 1024, 8, 256, 5700, 8
+    ids = some_ids(T, k, E)
+    assert T * k >= 44 * E
+    w, p = experts("q4_k", E, 2 * N, K)
+    gate_up("q4_k", w, p, bf16(T, K), ids, N)
 
 
 def test_many_rows_of_long_k():
