@@ -49,7 +49,7 @@ constexpr int kRawBytes = TM * 144;  // one super-block of the CTA's weight rows
 // Four warpgroups: 0-1 epilogue, 2 unpacking, 3 copies / MMA. The epilogue's 128 sums per thread need more registers than
 // the 128 a 512-thread CTA starts with; the others hand theirs over.
 constexpr int kEpiWarps = 8, kDqWarps = 4;
-constexpr int kTmaWarp = kEpiWarps + kDqWarps, kMmaWarp = kTmaWarp + 1;
+constexpr int kTmaWarp = kEpiWarps + kDqWarps, kMmaWarp = kTmaWarp + 1, kRawWarp = kTmaWarp + 2;
 constexpr int kTcThreads = 16 * 32;
 constexpr int kLaunchRegs = 128, kEpiRegs = 184, kDqRegs = 96, kCtlRegs = 48;
 static_assert(2 * 128 * kEpiRegs + 128 * kDqRegs + 128 * kCtlRegs == kTcThreads * kLaunchRegs, "register split");
@@ -132,6 +132,13 @@ __device__ __forceinline__ void tma_load_2d_pair(void* dst, const void* tmap, in
       "l"(tmap), "r"(x), "r"(y), "r"(bar)
       : "memory");
 }
+// Stores without a branch.
+__device__ __forceinline__ void store_if(bool on, uint16_t* to, uint16_t v) {
+  asm volatile("{\n.reg .pred p;\nsetp.ne.u32 p, %2, 0;\n@p st.global.u16 [%0], %1;\n}" ::"l"(to), "h"(v), "r"((uint32_t)on) : "memory");
+}
+__device__ __forceinline__ void store_if(bool on, float* to, float v) {
+  asm volatile("{\n.reg .pred p;\nsetp.ne.u32 p, %2, 0;\n@p st.global.cs.f32 [%0], %1;\n}" ::"l"(to), "f"(v), "r"((uint32_t)on) : "memory");
+}
 // 16-byte chunk `c` of row r in a K-major 64-wide fp16 tile with the 128-byte swizzle.
 __device__ __forceinline__ int sw128_off(int r, int c) { return (r >> 3) * 1024 + (r & 7) * 128 + ((c ^ (r & 7)) << 4); }
 
@@ -164,23 +171,16 @@ __device__ __forceinline__ void unpack_row(const uint8_t* b, int kc, uint8_t* ti
 }
 
 // -64 dmin m of a super-block's eight sub-blocks (header h) as fp16 hi + lo, chunks 4 j .. 4 j + 3 of row r: hi, hi, lo, zeros.
+// lo = -64 dmin m - hi is exact: what rounding 11 bits times 6 to 11 leaves has six bits, none below the last of dmin.
 __device__ __forceinline__ void min_row(const uint4& h, int j, uint8_t* tile, int r) {
-  const float f = -64.f * half_bits_to_float(h.x >> 16);
+  const uint32_t dmin = prmt(h.x, 0u, 0x3232u);
+  const uint32_t m[2] = {h.z & 0x3F3F3F3Fu, ((h.w >> 4) & 0x0F0F0F0Fu) | ((h.z >> 2) & 0x30303030u)};  // six bits a byte
   uint32_t hv[4], lv[4];
 #pragma unroll
-  for (int b = 0; b < 8; b += 2) {
-    float v[2], l[2];
-    uint16_t hb[2];
-#pragma unroll
-    for (int t = 0; t < 2; ++t) {
-      const int s = b + t;
-      const int m = s < 4 ? (h.z >> (8 * s)) & 63 : ((h.w >> (8 * (s - 4) + 4)) & 15) | (((h.z >> (8 * (s - 4) + 6)) & 3) << 4);
-      v[t] = f * (float)m;  // exact: 11 bits times 6
-      hb[t] = __half_as_ushort(__float2half_rn(v[t]));
-      l[t] = v[t] - half_bits_to_float(hb[t]);
-    }
-    hv[b / 2] = hb[0] | (uint32_t)hb[1] << 16;
-    lv[b / 2] = f2_to_h2(l[0], l[1]);
+  for (int b = 0; b < 4; ++b) {
+    const uint32_t f = h2_mul(h2_sub(prmt(m[b / 2], 0x64646464u, b & 1 ? 0x4342u : 0x4140u), 0x64006400u), 0xD400D400u);  // -64 m
+    hv[b] = h2_mul(dmin, f);
+    lv[b] = h2_fma(dmin, f, hv[b] ^ 0x80008000u);
   }
   *reinterpret_cast<uint4*>(tile + sw128_off(r, 4 * j)) = make_uint4(hv[0], hv[1], hv[2], hv[3]);
   *reinterpret_cast<uint4*>(tile + sw128_off(r, 4 * j + 1)) = make_uint4(hv[0], hv[1], hv[2], hv[3]);
@@ -327,6 +327,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTcThreads, 1)
     }
   };
 
+  // This CTA's first weight row of a tile (of the gate rows and, half further on, of the up rows).
+  auto row0_of = [&](const Tile& t) {
+    return t.e * (long long)p.N + (p.half ? t.row_tile * TM + static_cast<int>(rank) * (TM / 2) : (2 * t.row_tile + static_cast<int>(rank)) * TM);
+  };
+
   const int wg = warp >> 2;  // each role's register budget is set at the top of its branch
   if (wg == 3) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kCtlRegs));
@@ -381,6 +386,25 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTcThreads, 1)
         if (!mbar_wait_bounded(mma_done, 0u, kTcWaitNs)) fail();  // whether or not another role gave up
       }
     }
+    if (warp == kRawWarp && lane == 0) {
+      // raw super-blocks, in the order they are unpacked
+      int slot = 0, turn = 0, e = 0;
+      bool ok = true;
+      for (int i = 0; i < my_tiles && ok; ++i) {
+        const Tile t = tile_of(i, e);
+        e = t.e;
+        const int r0 = static_cast<int>(row0_of(t)), r1 = r0 + (p.half ? p.half : TM / 2);
+        for (int g = 0; g < nsb; ++g) {
+          if (turn > 0 && !wait(&raw_empty[slot], static_cast<uint32_t>(turn - 1) & 1u)) { ok = false; break; }
+          fence_proxy_async_smem();  // the unpacking warps' reads of the slot before the copy's writes
+          uint8_t* dst = raw + slot * kRawBytes;
+          mbar_arrive_expect_tx(&raw_full[slot], kRawBytes);
+          tma_load_2d(dst, &wmap, g * 36, r0, &raw_full[slot]);  // 36 words = 144 bytes; 64 rows a copy
+          tma_load_2d(dst + kRawBytes / 2, &wmap, g * 36, r1, &raw_full[slot]);
+          if (++slot == RAW_STAGES) slot = 0, ++turn;
+        }
+      }
+    }
     if (!leader && warp == kMmaWarp && lane == 0) {
       // forwarder of rank 1: passes each group's "read out" on to rank 0, one arrival for eight warps
       for (int i = 0; i < my_tiles * (nsb + 1); ++i) {
@@ -391,32 +415,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTcThreads, 1)
   } else if (wg == 2) {  // warps 8..11: unpack whole k-tiles (all 128 rows) in turn
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kDqRegs));
     const int dw = warp - kEpiWarps;
-    // This CTA's first weight row of a tile (of the gate rows and, half further on, of the up rows).
-    auto row0_of = [&](const Tile& t) {
-      return t.e * (long long)p.N + (p.half ? t.row_tile * TM + static_cast<int>(rank) * (TM / 2) : (2 * t.row_tile + static_cast<int>(rank)) * TM);
-    };
-    // raw super-blocks in the order they are unpacked: item = super-block item % nsb of the (item / nsb)-th tile
-    auto raw_issue = [&](int item, int e) {
-      const int i = item / nsb, g = item - i * nsb;
-      if (i >= my_tiles) return;
-      const Tile t = tile_of(i, e);
-      const int r0 = static_cast<int>(row0_of(t));
-      uint64_t* b = &raw_full[item % RAW_STAGES];
-      uint8_t* dst = raw + (item % RAW_STAGES) * kRawBytes;
-      mbar_arrive_expect_tx(b, kRawBytes);
-      tma_load_2d(dst, &wmap, g * 36, r0, b);  // 36 words = 144 bytes; 64 rows a copy
-      tma_load_2d(dst + kRawBytes / 2, &wmap, g * 36, r0 + (p.half ? p.half : TM / 2), b);
-    };
-    if (dw == 0 && lane == 0)
-      for (int i = 0; i < RAW_STAGES; ++i) raw_issue(i, 0);
+    int e = 0;
     // Row r of a CTA's tile: with gate | up, 16 gate rows and 16 up rows of every 32.
     auto raw_row = [&](int r) { return p.half ? ((r & 16) ? TM / 2 : 0) + (r >> 5) * 16 + (r & 15) : r; };
     // k-tiles dw, dw + 4, ... of the pair's tiles: stage s in its round-th turn; a main one is chunk km % 4 of the raw super-block in
     // `slot` in that one's `turn`-th turn (a warp has one k-tile of each)
     static_assert(kDqWarps < STAGES, "a step passes one turn of the ring at most");
-    int s = dw, round = 0, slot = 0, turn = 0, q = 0, kt = dw;
+    int s = dw, round = 0, slot = 0, turn = 0, kt = dw;
     for (int tk = 0; tk < my_tiles; ++tk, kt -= kt_tile) {
-      const Tile t = tile_of(tk, 0);
+      const Tile t = tile_of(tk, e);
+      e = t.e;
       // headers of the two super-blocks of min-term tile m, four rows of this lane: asked for long before they are needed (at the
       // start of a tile they cost 2.5 us)
       uint4 head[2][TM / 32];
@@ -461,13 +469,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTcThreads, 1)
           if (leader) mbar_arrive_local(&full_w[s]);
           else mbar_arrive_remote(cluster_addr(&full_w[s], 0));
           if (main) mbar_arrive_local(&raw_empty[slot]);
-          if (main && (kt & 3) == 3 && wait(&raw_empty[slot], static_cast<uint32_t>(turn) & 1u)) {
-            fence_proxy_async_smem();  // the super-block's four k-tiles are read: its slot takes the next one
-            raw_issue(q + RAW_STAGES, t.e);
-          }
         }
         if (main) {
-          ++q;
           if (++slot == RAW_STAGES) slot = 0, ++turn;
         }
         s += kDqWarps;
@@ -495,6 +498,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTcThreads, 1)
         nok = n < p.N;
       }
       const int c0 = part * t.h;
+      uint32_t tags[TN / 64];  // of the columns, asked for here: the last sums are not to wait for them
+#pragma unroll
+      for (int b = 0; b < TN / 64; ++b) {
+        const int c = 32 * b + lane;
+        tags[b] = c0 + c < t.n && c < t.h ? p.tags[t.first + c0 + c] : kNoPair;
+      }
       uint16_t* act = p.act + n;
       float* y = p.y + n;
       float acc[TN / 2];
@@ -521,24 +530,28 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTcThreads, 1)
         if (lane == 0) mbar_arrive_local(&acc_empty[buf]);
       }
       if (stop) break;
-      // results: acc * 2^-e of the column's row, to the row's pair
+      // results: acc * 2^-e of the column's row, to the row's pair. Nothing branches, so that the columns' chains of shuffles and
+      // exponentials run beside each other
 #pragma unroll
       for (int b = 0; b < TN / 2; b += 32) {
         if (b < t.h) {
-          const int mine = c0 + b + lane;
-          const uint32_t tag = mine < t.n && b + lane < t.h ? p.tags[t.first + mine] : kNoPair;
+          const uint32_t tag = tags[b / 32];
 #pragma unroll
           for (int c = 0; c < 32; c += 2) {
             const uint32_t t0 = __shfl_sync(0xFFFFFFFFu, tag, c), t1 = __shfl_sync(0xFFFFFFFFu, tag, c + 1);
-            const float v0 = acc[b + c] * __uint_as_float(t0 & 0x7F800000u), v1 = acc[b + c + 1] * __uint_as_float(t1 & 0x7F800000u);
-            if (p.half) {  // lanes 0..15 hold gate rows and take column c, lanes 16..31 up rows and column c + 1
-              const float o = __shfl_xor_sync(0xFFFFFFFFu, low ? v1 : v0, 16);
-              const float g = low ? v0 : o, u = low ? o : v1;
-              const uint32_t q = low ? t0 : t1;
-              if (nok && q != kNoPair) act[(size_t)(q & 0x7FFFFFu) * p.half] = silu_mul(g, u);
-            } else if (nok) {
-              if (t0 != kNoPair) __stcs(y + (size_t)(t0 & 0x7FFFFFu) * p.N, v0);
-              if (t1 != kNoPair) __stcs(y + (size_t)(t1 & 0x7FFFFFu) * p.N, v1);
+            acc[b + c] *= __uint_as_float(t0 & 0x7F800000u), acc[b + c + 1] *= __uint_as_float(t1 & 0x7F800000u);
+            if (!p.half) {
+              store_if(nok && t0 != kNoPair, y + (size_t)(t0 & 0x7FFFFFu) * p.N, acc[b + c]);
+              store_if(nok && t1 != kNoPair, y + (size_t)(t1 & 0x7FFFFFu) * p.N, acc[b + c + 1]);
+            }
+          }
+          if (p.half) {  // lanes 0..15 hold gate rows and take column c, lanes 16..31 up rows and column c + 1
+#pragma unroll
+            for (int c = 0; c < 32; c += 2) {
+              const uint32_t q = __shfl_sync(0xFFFFFFFFu, tag, c + (low ? 0 : 1));
+              const float o = __shfl_xor_sync(0xFFFFFFFFu, low ? acc[b + c + 1] : acc[b + c], 16);
+              const uint16_t v = silu_mul(low ? acc[b + c] : o, low ? o : acc[b + c + 1]);
+              store_if(nok && q != kNoPair, act + (size_t)(q & 0x7FFFFFu) * p.half, v);
             }
           }
         }
