@@ -144,8 +144,9 @@ __device__ __forceinline__ int sw128_off(int r, int c) { return (r >> 3) * 1024 
 
 // The 64 values t = sc q of k-chunk kc (0..3) of a super-block into row r of the tile. b: the block; sub-blocks 2 kc (low
 // nibbles, k = 0..31) and 2 kc + 1 (high nibbles): a pair of codes becomes 1024 + q or 1024 + 16 q in fp16, and one fma takes the
-// offset off and multiplies by sc. The scales become fp16 by exponent bytes too: conversions run at a quarter of the rate.
-__device__ __forceinline__ void unpack_row(const uint8_t* b, int kc, uint8_t* tile, int r) {
+// offset off and multiplies by sc. The scales become fp16 by exponent bytes too: conversions run at a quarter of the rate. Returns
+// the header's first word: d and dmin.
+__device__ __forceinline__ uint32_t unpack_row(const uint8_t* b, int kc, uint8_t* tile, int r) {
   const uint4 h = lds128(b), qa = lds128(b + 16 + 32 * kc), qb = lds128(b + 32 + 32 * kc);
   // sc of the two sub-blocks in bytes 0 and 1: six bits of scales[2 kc], or four of scales[2 kc + 4] and two of scales[2 kc - 4]
   const int at = 16 * (kc & 1);
@@ -168,6 +169,7 @@ __device__ __forceinline__ void unpack_row(const uint8_t* b, int kc, uint8_t* ti
     *reinterpret_cast<uint4*>(tile + sw128_off(r, c)) = make_uint4(lo[4 * c], lo[4 * c + 1], lo[4 * c + 2], lo[4 * c + 3]);
     *reinterpret_cast<uint4*>(tile + sw128_off(r, c + 4)) = make_uint4(hi[4 * c], hi[4 * c + 1], hi[4 * c + 2], hi[4 * c + 3]);
   }
+  return h.x;
 }
 
 // -64 dmin m of a super-block's eight sub-blocks (header h) as fp16 hi + lo, chunks 4 j .. 4 j + 3 of row r: hi, hi, lo, zeros.
@@ -200,9 +202,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTcThreads, 1)
   __shared__ int scan_sums[16];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(tc_smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* raw = smem + STAGES * kStageBytes;     // stage s: t tile, then this CTA's rows
-  uint64_t* full_x = reinterpret_cast<uint64_t*>(raw + RAW_STAGES * kRawBytes);  // rank 0: copies landed
-  uint64_t* full_w = full_x + STAGES;             // rank 0: both CTAs' t tiles written
-  uint64_t* empty = full_w + STAGES;              // each: the pair's MMAs read the stage
+  uint64_t* full = reinterpret_cast<uint64_t*>(raw + RAW_STAGES * kRawBytes);  // rank 0: copies landed, both CTAs' t tiles written
+  uint64_t* empty = full + STAGES;                // each: the pair's MMAs read the stage
   uint64_t* acc_full = empty + STAGES;            // each [2]: group finished
   uint64_t* acc_empty = acc_full + 2;             // each [2]: the CTA's epilogue read the group (rank 0: and rank 1's)
   uint64_t* raw_full = acc_empty + 2;             // each [RAW_STAGES]: raw super-block landed
@@ -212,7 +213,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTcThreads, 1)
   unsigned int* abort_flag = tmem_slot + 1;
   // d of the last four groups' super-blocks, by row: written by the unpacking warps, read by the epilogue. Unpacking group G starts
   // after the MMAs of group G - 2, which began when the epilogue had read group G - 4
-  float* dscale = reinterpret_cast<float*>(reinterpret_cast<uint8_t*>(full_x) + kBarBytes);
+  float* dscale = reinterpret_cast<float*>(reinterpret_cast<uint8_t*>(full) + kBarBytes);
   int* start = reinterpret_cast<int*>(reinterpret_cast<uint8_t*>(dscale) + kScaleBytes);  // E + 1: tiles before each expert
   int* place = start + KQ_MOE_MAX_EXPERTS + 1;                                          // E + 1: offsets
 
@@ -226,8 +227,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTcThreads, 1)
   if (threadIdx.x == 0) {
     // rank 1's unpacking warps arrive at rank 0's barriers, its epilogue warps at their own, which one thread forwards
     for (int s = 0; s < STAGES; ++s) {
-      mbar_init(&full_x[s], 1);
-      mbar_init(&full_w[s], 2);
+      mbar_init(&full[s], 3);
       mbar_init(&empty[s], 1);
     }
     for (int b = 0; b < 2; ++b) {
@@ -346,8 +346,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTcThreads, 1)
           for (int kt = 0; kt < kt_tile; ++kt) {
             if (round > 0 && !wait(&empty[s], static_cast<uint32_t>(round - 1) & 1u)) { ok = false; break; }
             uint8_t* dst = smem + s * kStageBytes + kWTileBytes;
-            const uint32_t fb = cluster_addr(&full_x[s], 0);
-            if (leader) mbar_arrive_expect_tx(&full_x[s], 2u * boxes * kBoxRows * BK * 2);
+            const uint32_t fb = cluster_addr(&full[s], 0);
+            if (leader) mbar_arrive_expect_tx(&full[s], 2u * boxes * kBoxRows * BK * 2);
             const int col = kt * BK;  // the min-term columns stand behind the K values
             for (int b = 0; b < boxes; ++b) tma_load_2d_pair(dst + b * kBoxRows * BK * 2, &xmap, col, r0 + b * kBoxRows, fb);
             if (++s == STAGES) s = 0, ++round;
@@ -370,7 +370,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTcThreads, 1)
             tc_fence_after();
             const int n = g == nsb ? p.n_ext : 4;
             for (int kt = 0; kt < n; ++kt) {
-              if (!wait(&full_x[s], par) || !wait(&full_w[s], par)) { ok = false; break; }
+              if (!wait(&full[s], par)) { ok = false; break; }
               tc_fence_after();
               const uint64_t wa = desc0 + static_cast<uint32_t>(s * (kStageBytes >> 4)), xa = wa + (kWTileBytes >> 4);
 #pragma unroll
@@ -449,12 +449,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTcThreads, 1)
         if (!__all_sync(0xFFFFFFFFu, ok)) break;
         if (main) {
           const uint8_t* rs = raw + slot * kRawBytes;
+          float* d = dscale + ((tk * (nsb + 1) + (kt >> 2)) % kScaleGroups) * TM + lane;
 #pragma unroll 1
-          for (int i = 0; i < TM / 32; ++i) unpack_row(rs + raw_row(32 * i + lane) * 144, kt & 3, wt, 32 * i + lane);
-          if ((kt & 3) == 0) {
-            float* d = dscale + ((tk * (nsb + 1) + (kt >> 2)) % kScaleGroups) * TM + lane;
-#pragma unroll
-            for (int i = 0; i < TM / 32; ++i) d[32 * i] = half_bits_to_float(*reinterpret_cast<const uint16_t*>(rs + raw_row(32 * i + lane) * 144));
+          for (int i = 0; i < TM / 32; ++i, d += 32) {
+            const uint32_t head0 = unpack_row(rs + raw_row(32 * i + lane) * 144, kt & 3, wt, 32 * i + lane);
+            if ((kt & 3) == 0) *d = half_bits_to_float(head0 & 0xFFFFu);
           }
         } else {
 #pragma unroll
@@ -466,8 +465,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTcThreads, 1)
         fence_proxy_async_smem();  // generic-proxy writes -> visible to the tensor core
         __syncwarp();
         if (lane == 0) {
-          if (leader) mbar_arrive_local(&full_w[s]);
-          else mbar_arrive_remote(cluster_addr(&full_w[s], 0));
+          if (leader) mbar_arrive_local(&full[s]);
+          else mbar_arrive_remote(cluster_addr(&full[s], 0));
           if (main) mbar_arrive_local(&raw_empty[slot]);
         }
         if (main) {
