@@ -9,11 +9,15 @@
 //  * a cluster of two CTAs owns a tile of 256 weight rows x up to 256 rows of one expert (cta_group::2, M = 256,
 //    N = 32 .. 256 by the expert's rows; rank r holds weight rows 128 r.. and half of the N rows); for gate | up
 //    a CTA's 128 rows are 64 of each, 16 and 16 of a warp's 32 lanes, so that the epilogue forms silu(g) u by a shuffle;
-//  * roles as in the prefill product: copies, MMA, four unpacking warps, eight epilogue warps that add d_s times each
-//    finished super-block into registers.
+//  * roles as in the prefill product: copies of rows, copies of raw blocks, MMA, four unpacking warps, eight epilogue warps that
+//    add d_s times each finished super-block into registers.
 // Tiles follow from the plan's offsets on the device: expert by expert, an expert's rows in equal parts of up to 256. The
 // min-term tiles (two super-blocks each, [M_hi M_hi M_lo 0] per super-block) are formed by the unpacking warps from the
-// blocks' headers at a tile's start.
+// blocks' headers and come last.
+// 2048 tokens, 8 of 128 experts: gate | up (2 x 768 x 2048) 239 us, 430 TFLOP/s, pre-pass and all; down (2048 x 768) 169 us, 305. What
+// bounds it is the ring of five stages: free -> unpacked (0.9 of a k-tile's 1.1 thousand cycles, four at a time) -> both CTAs' arrival ->
+// MMA (0.3) -> commit; raw blocks through a warp of their own and one barrier per stage took 5 % off, results stored
+// without branches 8 %.
 // Every wait is bounded: a timeout records the error word and raises the abort flag of both CTAs; all roles then drain
 // and return.
 #include <cooperative_groups.h>
@@ -57,9 +61,12 @@ static_assert(kDqWarps <= STAGES, "an unpacking warp's previous wait was kDqWarp
 constexpr int kTmemCols = 2 * TN;  // two accumulator groups in flight
 constexpr int kBarBytes = 512;
 constexpr int kListBytes = 2 * (KQ_MOE_MAX_EXPERTS + 1) * 4 + 8;  // tiles before each expert, and its first row
+// A pair's first tiles are worked out before the roles part, for those that feed the tensor cores (2 us a tile in the MMAs' own
+// thread; 65536 pairs of 1024 experts, 2 x 512 x 1024: 572 -> 557 us); further ones, of calls beyond about 600,000 rows of 512, as they come
+constexpr int kTable = 64;
 constexpr int kScaleGroups = 4;               // super-blocks whose d the epilogue may still need
 constexpr int kScaleBytes = kScaleGroups * TM * 4;
-constexpr int kTcSmem = STAGES * kStageBytes + RAW_STAGES * kRawBytes + kBarBytes + kScaleBytes + kListBytes + 1024 /*alignment*/;
+constexpr int kTcSmem = STAGES * kStageBytes + RAW_STAGES * kRawBytes + kBarBytes + kScaleBytes + kListBytes + kTable * 16 + 1024 /*alignment*/;
 constexpr uint32_t kNoPair = 0x80000000u;  // a tag of none
 constexpr uint64_t kTcWaitNs = 2000000000ull;
 static_assert(kTcSmem <= 232448 - 256, "shared memory per CTA");
@@ -216,6 +223,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTcThreads, 1)
   float* dscale = reinterpret_cast<float*>(reinterpret_cast<uint8_t*>(full) + kBarBytes);
   int* start = reinterpret_cast<int*>(reinterpret_cast<uint8_t*>(dscale) + kScaleBytes);  // E + 1: tiles before each expert
   int* place = start + KQ_MOE_MAX_EXPERTS + 1;                                          // E + 1: offsets
+  int4* table = reinterpret_cast<int4*>(reinterpret_cast<uint8_t*>(start) + kListBytes);  // e, first, n and h, row_tile
 
   cg::cluster_group cluster = cg::this_cluster();
   const uint32_t rank = cluster.block_rank();
@@ -284,16 +292,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTcThreads, 1)
     if (2 * static_cast<int>(threadIdx.x) + 1 <= p.E) start[2 * threadIdx.x + 1] = before + n[0];
     if (threadIdx.x == kTcThreads - 1 && p.E == 2 * kTcThreads) start[p.E] = before + mine;
   }
-  tc_fence_before();
   __syncthreads();
-  cluster.sync();  // both CTAs' barriers initialised, tensor memory allocated, lists written
-  tc_fence_after();
-  const uint32_t tmem = *tmem_slot;
   const int tiles = start[p.E];
   const int my_tiles = pair < tiles ? (tiles - 1 - pair) / npairs + 1 : 0;
 
   // Tile i of this pair; e: the expert of an earlier one, or 0.
-  auto tile_of = [&](int i, int e) {
+  auto find_tile = [&](int i, int e) {
     const int t = pair + i * npairs;
     while (start[e + 1] <= t) ++e;
     Tile r;
@@ -306,6 +310,29 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTcThreads, 1)
     r.h = (r.n + 31) / 32 * 16;
     return r;
   };
+  if (static_cast<int>(threadIdx.x) < min(my_tiles, kTable)) {
+    const int i = static_cast<int>(threadIdx.x), at = pair + i * npairs;
+    int e = 0;
+    for (int end = p.E; end - e > 1;) {  // the last expert whose tiles begin at or before this one
+      const int mid = (e + end) / 2;
+      if (start[mid] <= at) e = mid;
+      else end = mid;
+    }
+    const Tile t = find_tile(i, e);
+    table[i] = make_int4(t.e, t.first, t.n | t.h << 16, t.row_tile);
+  }
+  auto tile_of = [&](int i, int e) {
+    if (i >= kTable) return find_tile(i, e);
+    const int4 v = table[i];
+    Tile r;
+    r.e = v.x, r.first = v.y, r.n = v.z & 0xFFFF, r.h = v.z >> 16, r.row_tile = v.w;
+    return r;
+  };
+  tc_fence_before();
+  __syncthreads();
+  cluster.sync();  // both CTAs' barriers initialised, tensor memory allocated, lists written
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
 
   auto aborted = [&]() { return *(volatile unsigned int*)abort_flag != 0u; };
   auto fail = [&]() {
@@ -423,7 +450,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTcThreads, 1)
     static_assert(kDqWarps < STAGES, "a step passes one turn of the ring at most");
     int s = dw, round = 0, slot = 0, turn = 0, kt = dw;
     for (int tk = 0; tk < my_tiles; ++tk, kt -= kt_tile) {
-      const Tile t = tile_of(tk, e);
+      const Tile t = find_tile(tk, e);
       e = t.e;
       // headers of the two super-blocks of min-term tile m, four rows of this lane: asked for long before they are needed (at the
       // start of a tile they cost 2.5 us)
@@ -484,7 +511,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTcThreads, 1)
     int grp = 0, e = 0;
     bool stop = false;
     for (int i = 0; i < my_tiles && !stop; ++i) {
-      const Tile t = tile_of(i, e);
+      const Tile t = find_tile(i, e);
       e = t.e;
       // this thread's weight row of the expert, and the warp's columns: rows c0 .. c0 + t.h - 1 of the tile
       int n;

@@ -189,7 +189,7 @@ def many_ids(counts, seed=0):
                                     (700, 3, 3, 3), (48,) * 16])
 @pytest.mark.parametrize("K", [256, 768, 1280])
 def test_many_rows_of_an_expert(counts, K):
-    """Q4_K calls of many rows per expert (44 on average) run on the tensor cores, experts of few rows or none among them."""
+    """Q4_K calls of many rows per expert (KQ_MOE_TC_ROWS on average) run on the tensor cores, experts of few rows or none among them."""
     E, F, H = len(counts), 128, 256
     ids = many_ids(counts)
     w, p = experts("q4_k", E, 2 * F, K)
@@ -239,6 +239,17 @@ def test_many_rows_of_the_most_experts():
     assert T * k >= 44 * E
     w, p = experts("q4_k", E, 2 * N, K)
     gate_up("q4_k", w, p, bf16(T, K), ids, N)
+
+
+def test_a_long_run_of_tiles():
+    """More tiles than the tensor-core product works out ahead (64 per pair of SMs): the same rows again and again, against few of them."""
+    F, K, n, T = 256, 256, 97, 700_000
+    w, p = experts("q4_k", 1, 2 * F, K)
+    x = bf16(n, K)
+    few = gate_up("q4_k", w, p, x, np.zeros((n, 1), np.int32), F)
+    rows = torch.arange(T, device="cuda") % n
+    out = kq.moe_gate_up("q4_k", w, x[rows], kq.moe_plan(torch.zeros((T, 1), dtype=torch.int32, device="cuda"), 1), F, K)
+    assert torch.equal(out, few[rows])
 
 
 def test_many_rows_of_long_k():
