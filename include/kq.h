@@ -537,7 +537,7 @@ int kq_moe_plan(const int* ids, int T, int k, int E, int* offsets, int* order, v
  * a multiple of 16. A plan outside its bounds (offsets that fall or pass T * k, pairs outside 0..T*k-1) sets bit 1 of
  * kq_device_errors(), and the experts or pairs concerned are not computed. One launch, or two on the tensor cores.
  * Errors: KQ_ERR_ARG, KQ_ERR_UNSUPPORTED, KQ_ERR_WORKSPACE, KQ_ERR_CUDA. */
-enum { KQ_MOE_TC_ROWS = 40 };
+enum { KQ_MOE_TC_ROWS = 34 };
 size_t kq_moe_gate_up_workspace_size(int fmt, int T, int k, int E, int F, int K);
 int kq_moe_gate_up(int fmt, const void* w, const void* x, long long x_stride, const int* offsets, const int* order, int T,
                    int k, int E, int F, int K, void* act, void* workspace, size_t ws_bytes, void* stream);

@@ -604,8 +604,8 @@ int launch_stream(const CUtensorMap& tm, StreamParams& p, size_t smem, int num_s
 }
 
 // From KQ_MOE_TC_ROWS rows per expert on average the tensor-core product is faster: 128 experts of 2 x 768 x 2048, rows per expert
-// (streaming, tensor cores) 32: 168, 192 us; 40: 199, 194; 48: 229, 198; 128: 535, 239; 60 of 2 x 1408 x 2048, 32: 138, 157;
-// 40: 171, 158; 8 of 2 x 2048 x 4096, 24: 67, 78; 40: 93, 79; down, 128 of 2048 x 768, 32: 106, 114; 40: 126, 118.
+// (streaming, tensor cores) 28: 151, 172 us; 32: 168, 174; 36: 185, 175; 128: 535, 218; 60 of 2 x 1408 x 2048, 32: 138, 142; 40:
+// 171, 143; 8 of 2 x 2048 x 4096, 24: 67, 70; 32: 78, 70; down, 128 of 2048 x 768, 32: 106, 103.
 bool by_tensor_cores(int fmt, int T, int k, int E) { return fmt == FMT_Q4_K && (long long)T * k >= (long long)KQ_MOE_TC_ROWS * E; }
 
 // ws: of the tensor-core product
