@@ -67,7 +67,8 @@ constexpr int kTable = 64;
 constexpr int kScaleGroups = 4;               // super-blocks whose d the epilogue may still need
 constexpr int kScaleBytes = kScaleGroups * TM * 4;
 constexpr int kTcSmem = STAGES * kStageBytes + RAW_STAGES * kRawBytes + kBarBytes + kScaleBytes + kListBytes + kTable * 16 + 1024 /*alignment*/;
-constexpr uint32_t kNoPair = 0x80000000u;  // a tag of none
+constexpr uint32_t kNoPair = 0x80000000u;   // a tag of none: a column behind a tile's rows
+constexpr uint32_t kBadPair = 0x80000001u;  // and of a place whose pair is out of bounds; nothing is stored from kNoPair on
 constexpr uint64_t kTcWaitNs = 2000000000ull;
 static_assert(kTcSmem <= 232448 - 256, "shared memory per CTA");
 
@@ -563,6 +564,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTcThreads, 1)
         if (lane == 0) mbar_arrive_local(&acc_empty[buf]);
       }
       if (stop) break;
+      bool bad = false;  // a place of this expert without a pair of this call. Asked here: with the tags it would wait for them (158 -> 161 us)
+#pragma unroll
+      for (int b = 0; b < TN / 64; ++b) {
+        if ((tags[b] & 0x7FFFFFu) >= static_cast<uint32_t>(p.P)) tags[b] = kBadPair;
+        bad |= tags[b] > kNoPair;
+      }
+      if (bad) atomicOr(&g_moe_tc_errors, 2u);
       // results: acc * 2^-e of the column's row, to the row's pair. Nothing branches, so that the columns' chains of shuffles and
       // exponentials run beside each other
 #pragma unroll
@@ -574,8 +582,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTcThreads, 1)
             const uint32_t t0 = __shfl_sync(0xFFFFFFFFu, tag, c), t1 = __shfl_sync(0xFFFFFFFFu, tag, c + 1);
             acc[b + c] *= __uint_as_float(t0 & 0x7F800000u), acc[b + c + 1] *= __uint_as_float(t1 & 0x7F800000u);
             if (!p.half) {
-              store_if(nok && t0 != kNoPair, y + (size_t)(t0 & 0x7FFFFFu) * p.N, acc[b + c]);
-              store_if(nok && t1 != kNoPair, y + (size_t)(t1 & 0x7FFFFFu) * p.N, acc[b + c + 1]);
+              store_if(nok && t0 < kNoPair, y + (size_t)(t0 & 0x7FFFFFu) * p.N, acc[b + c]);
+              store_if(nok && t1 < kNoPair, y + (size_t)(t1 & 0x7FFFFFu) * p.N, acc[b + c + 1]);
             }
           }
           if (p.half) {  // lanes 0..15 hold gate rows and take column c, lanes 16..31 up rows and column c + 1
@@ -584,7 +592,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTcThreads, 1)
               const uint32_t q = __shfl_sync(0xFFFFFFFFu, tag, c + (low ? 0 : 1));
               const float o = __shfl_xor_sync(0xFFFFFFFFu, low ? acc[b + c + 1] : acc[b + c], 16);
               const uint16_t v = silu_mul(low ? acc[b + c] : o, low ? o : acc[b + c + 1]);
-              store_if(nok && q != kNoPair, act + (size_t)(q & 0x7FFFFFu) * p.half, v);
+              store_if(nok && q < kNoPair, act + (size_t)(q & 0x7FFFFFu) * p.half, v);
             }
           }
         }
@@ -608,13 +616,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTcThreads, 1)
 
 // The pre-pass: a warp per row, in the plan's order. x' = fp16(x 2^e), exact for values
 // within 2^28 of the row's largest (which lands in [2^14, 2^15)); behind the K values, per super-block, S_hi x 8, S_lo x 8, S_hi x 8,
-// zeros x 8, S / 64 = hi + lo of the 32 x' of each sub-block. tags: the bits of 2^-e and the row's pair, below 2^23, in one word.
+// zeros x 8, S / 64 = hi + lo of the 32 x' of each sub-block. tags: the bits of 2^-e and the row's pair, below 2^23, in one word, or
+// kBadPair: of every place, as the product goes by each expert's own offsets, whatever the last one says.
 struct PrepParams {
   const uint16_t* x;
   long long xs;
   int div;  // pairs per row of x
-  const int *offsets, *order;
-  int E, P, K, cols;
+  const int* order;
+  int P, K, cols;
   __half* xc;
   uint32_t* tags;
 };
@@ -624,14 +633,10 @@ __global__ void __launch_bounds__(kPrepWarps * 32) moe_prep_kernel(const PrepPar
   grid_launch_dependents();
   grid_dependency_wait();
   const int lane = threadIdx.x & 31, nch = p.K / 8;  // 16-byte parts of a row
-  const int live = min(p.offsets[p.E], p.P);
-  for (int r = blockIdx.x * kPrepWarps + (threadIdx.x >> 5); r < live; r += gridDim.x * kPrepWarps) {
+  for (int r = blockIdx.x * kPrepWarps + (threadIdx.x >> 5); r < p.P; r += gridDim.x * kPrepWarps) {
     const int pair = p.order[r];
-    if (pair < 0 || pair >= p.P) {
-      if (lane == 0) {
-        atomicOr(&g_moe_tc_errors, 2u);
-        p.tags[r] = kNoPair;
-      }
+    if (pair < 0 || pair >= p.P) {  // behind the last expert's rows, or a plan out of bounds, which the product tells apart
+      if (lane == 0) p.tags[r] = kBadPair;
       continue;
     }
     const uint16_t* src = p.x + (long long)(pair / p.div) * p.xs;
@@ -705,7 +710,7 @@ int launch_moe_tc(const MoeGemmArgs& a, bool gate_up, float* parts, void* ws, in
   const int P = a.T * a.k, cols = columns(a.K), N = gate_up ? 2 * a.N : a.N;
   __half* xc = static_cast<__half*>(ws);
   uint32_t* tags = reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(ws) + al((size_t)P * cols * 2));
-  const PrepParams pp = {static_cast<const uint16_t*>(a.x), a.xs, gate_up ? a.k : 1, a.offsets, a.order, a.E, P, a.K, cols, xc, tags};
+  const PrepParams pp = {static_cast<const uint16_t*>(a.x), a.xs, gate_up ? a.k : 1, a.order, P, a.K, cols, xc, tags};
   if (launch_pdl(moe_prep_kernel, dim3(std::min((P + kPrepWarps - 1) / kPrepWarps, 64 * num_sms)), dim3(kPrepWarps * 32), 0, s, pp, "moe pre-pass", err))
     return -1;
 

@@ -299,6 +299,46 @@ def test_many_rows_in_a_plan_out_of_bounds():
         assert (same | (act == 3.0).all(1)).all() and not same.all() and same.any()
 
 
+@pytest.mark.parametrize("last", [10, 179, 0, -1])
+def test_many_rows_in_a_plan_whose_last_offset_falls(last):
+    """Only the last expert is left out: the others' rows are computed, also those behind the last offset. The workspace holds zeros
+    beforehand, which read as rows' tags name pair 0: a place that nobody has written to changes row 0."""
+    E, F, H, K = 4, 64, 200, 256
+    ids = many_ids((50, 60, 70, 40))
+    T = len(ids)
+    w1, p1 = experts("q4_k", E, 2 * F, K)
+    w2, p2 = experts("q4_k", E, H, K, 1)
+    x, ones = bf16(T, K), torch.ones((T, 1), device="cuda")
+    good = kq.moe_plan(dev(ids), E)
+    act = gate_up("q4_k", w1, p1, x, ids, F)
+    y = down("q4_k", w2, p2, x, ids, ones, H)
+    assert kq.device_errors() == 0
+    off = good.offsets.clone()
+    off[E] = last
+    plan = kq.MoePlan(off, good.order)
+    rest = torch.from_numpy(ids[:, 0] < 3).cuda()
+    for mark in (3.0, 5.0):
+        ws = torch.zeros(kq.moe_gate_up_workspace_size("q4_k", T, 1, E, F, K), dtype=torch.uint8, device="cuda")
+        out = torch.full((T, F), mark, dtype=torch.bfloat16, device="cuda")
+        kq.moe_gate_up("q4_k", w1, x, plan, F, K, act=out, workspace=ws)
+        assert kq.device_errors() == 2
+        assert torch.equal(out[rest], act[rest]) and (out[~rest] == mark).all()
+    ws = torch.zeros(kq.moe_down_workspace_size("q4_k", T, 1, E, H, K), dtype=torch.uint8, device="cuda")
+    out = kq.moe_down("q4_k", w2, x, plan, dev(ids), ones, H, K, workspace=ws)
+    assert kq.device_errors() == 2
+    assert torch.equal(out[rest], y[rest]) and not out[~rest].any()
+
+
+def test_many_rows_in_twice_as_many_places_as_the_order_fills():
+    """Places behind the last expert's rows have no pair, and are no error."""
+    E, F, K = 2, 64, 256
+    ids = many_ids((70, 60))
+    both = np.concatenate((ids, np.full_like(ids, -1)))
+    w, p = experts("q4_k", E, 2 * F, K)
+    gate_up("q4_k", w, p, bf16(len(both), K), both, F)
+    assert kq.device_errors() == 0
+
+
 def test_many_rows_twice_give_the_same_bits_on_two_streams():
     E, F, K = 6, 256, 512
     ids = many_ids((90, 33, 500, 10, 64, 200))
