@@ -8,7 +8,8 @@
 // as they are. With one, a warp orders fp32 choices and looks at the gaps that decide: where one is within what fp32 can be
 // off, it forms the choices that can be concerned in 64 bits, a lane for each (one token in a hundred needs that, but with
 // all 256 experts in 64 bits that token alone took 13 us of the call's 28: this GPU has little 64-bit arithmetic). Two
-// experts of the same logit and bias are equal in either, so that bf16 logits' ties stay in fp32.
+// experts of the same logit and bias are equal in either, so that bf16 logits' ties stay in fp32; where they stand on both sides of the
+// last gap, the one behind all of them is what it is measured to.
 //
 // One warp per token, logits and choices in registers. Bound by the instructions: up to 256 experts a lane sorts its own (a
 // network of 19 exchanges for eight) and a choice takes the largest of the lanes' heads by the warp's integer reduction, on
@@ -210,6 +211,18 @@ __device__ __noinline__ void exact_choices(const RouteParams& p, long long* keys
   __syncwarp();
 }
 
+// The largest fp32 choice up to expert id's that is not its equal by logit and bias. All lanes take part; out of line, as few tokens
+// have equals at the border.
+__device__ __noinline__ float next_other(const float* xs, const float* cs, const float* bias, int E, int id) {
+  const float x = xs[id], b = bias[id], c = cs[id];
+  float most = -INFINITY;
+  for (int e = threadIdx.x % 32; e < E; e += 32) {
+    const float f = cs[e];
+    if (f <= c && !(xs[e] == x && bias[e] == b)) most = fmaxf(most, f);
+  }
+  return of_key(__reduce_max_sync(kAll, key_of(most)));
+}
+
 // Lane j gets the expert of the j-th largest key, -1 where there is none; the keys are used up.
 __device__ __noinline__ int largest_keys(long long* keys, int E, int k) {
   const int lane = threadIdx.x % 32;
@@ -340,10 +353,17 @@ __global__ void __launch_bounds__(kRouteWarps * 32, VPL <= 8 ? 8 : 1) moe_route_
     const int e = __shfl_down_sync(kAll, id, 1);
     last = __reduce_min_sync(kAll, id >= 0 ? mine : kAll);
     if (lane < a.k - 1) next = k, next_e = e;
-    const float f = of_key(mine), g = of_key(next);
-    const bool close = id >= 0 && lane < a.k && next != kNone && f - g <= 2.f * off_by(f) &&
-                       !(xs[id] == xs[next_e] && a.bias[id] == a.bias[next_e]);
-    sure = !__any_sync(kAll, close);
+    const float f = of_key(mine);
+    float g = of_key(next);
+    const bool gap = id >= 0 && lane < a.k && next != kNone;
+    bool equal = gap && xs[id] == xs[next_e] && a.bias[id] == a.bias[next_e];
+    // equals on both sides of the border: what decides is whether one behind them can be larger than they are
+    if (__shfl_sync(kAll, equal, a.k - 1)) {
+      __syncwarp();
+      const float o = next_other(xs, cs, a.bias, a.E, __shfl_sync(kAll, id, a.k - 1));
+      if (lane == a.k - 1) g = o, equal = o == -INFINITY;
+    }
+    sure = !__any_sync(kAll, gap && !equal && f - g <= 2.f * off_by(f));
   }
   if (!sure) {  // a.bias: again from the exact choices down to the last one's reach
     __syncwarp();

@@ -132,6 +132,32 @@ def test_choices_that_fp32_cannot_order(score):
     run(x, 8, score, bias, 8, 3, "max")
 
 
+@pytest.mark.parametrize("x", ["f32", "bf16"])
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("E", [32, 64, 256, 1000])
+def test_equals_at_the_border_and_a_larger_one_behind_them(E, score, x):
+    """The k-th choice and the next ones have the same logit and bias; one behind them is their equal in fp32 and larger in 64 bits: sigmoids of
+    17 and 18 are both 1 in fp32, and so are softmax scores of about 2^-30 beside a bias of 1."""
+    rows = torch.zeros((6, E), device="cuda")
+    low, high = (17.0, 18.0) if score == "sigmoid" else (1.0, 2.0)
+    for t, at in enumerate(([0, 1], [0, 1, 2], [3, 4, 9, 10], [0, 30], [1, 2, 3, 4, 5, 6, 7], [0, 1])):
+        rows[t, at] = low
+        rows[t, E - 1 - t] = high
+    rows[5, E - 2] = high  # two equals behind
+    if score == "softmax":
+        rows[:, 20] = 22.0
+    bias = torch.zeros(E, device="cuda")
+    if score == "softmax":
+        bias += 1.0
+        bias[20] = -1.0
+    for k in (1, 2, 3, 5, 8):
+        run(rows.to(DT[x]), k, score, bias)
+        for G, g in ((4, 2), (8, 3)):
+            if k <= E // G * g and E % G == 0:
+                run(rows.to(DT[x]), k, score, bias, G, g, "top2")
+                run(rows.to(DT[x]), k, score, bias, G, g, "max")
+
+
 def test_experts_that_cannot_be_chosen():
     """-inf and NaN logits, whole rows of them, +inf, and biases that exclude."""
     x = logits(9, 40)
