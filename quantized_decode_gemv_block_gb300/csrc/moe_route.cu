@@ -157,12 +157,16 @@ __device__ unsigned keep_groups(const V* choice, int G, int keep, int per_group,
     before += o > s || (o == s && g < lane);
   }
   const unsigned kept = __ballot_sync(kAll, lane < G && before < keep);
-  if (sure) {
-    const bool in = lane < G && (kept >> lane & 1);
-    const float f = (float)s;
-    const float low = of_key(__reduce_min_sync(kAll, key_of(in ? f : INFINITY)));
-    const float high = of_key(__reduce_max_sync(kAll, key_of(lane < G && !in ? f : -INFINITY)));
-    if (low - high <= 4.f * off_by(low)) *sure = false;  // sums of two
+  if constexpr (sizeof(V) == 4) {
+    if (sure) {
+      // a sum is off by what its two choices are, which can be far larger than it is
+      const float o = __shfl_sync(kAll, off_by(a) + (two && b != none ? off_by(b) : 0.f), (lane < G ? lane : 0) * lanes);
+      const bool in = lane < G && (kept >> lane & 1);
+      const float off = fabsf(s) < INFINITY ? o : 0.f;
+      const float low = of_key(__reduce_min_sync(kAll, key_of(in ? s - off : INFINITY)));
+      const float high = of_key(__reduce_max_sync(kAll, key_of(lane < G && !in ? s + off : -INFINITY)));
+      if (low <= high && high > -INFINITY) *sure = false;
+    }
   }
   return kept;
 }

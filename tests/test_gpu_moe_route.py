@@ -158,6 +158,19 @@ def test_equals_at_the_border_and_a_larger_one_behind_them(E, score, x):
                 run(rows.to(DT[x]), k, score, bias, G, g, "max")
 
 
+def test_groups_whose_two_best_cancel():
+    """A sum of 1000 + s and -1000 + s' is off by units of 2^-14 in fp32, whatever it comes to; beside it a group whose sum is nearer than that."""
+    T = 96
+    g = torch.Generator(device="cuda").manual_seed(11)
+    s = 0.3 + 0.3 * torch.rand((T, 8), generator=g, device="cuda", dtype=torch.float64)
+    apart = (10 ** (-6 + 1.6 * torch.rand(T, generator=g, device="cuda", dtype=torch.float64))) * (torch.arange(T, device="cuda") % 2 * 2 - 1)
+    s[:, 5] = s[:, 0] + s[:, 1] - s[:, 4] + apart
+    x = torch.log(s / (1 - s)).float()
+    bias = torch.tensor([1000.0, -1000.0, -float("inf"), -float("inf"), 0.0, 0.0, -float("inf"), -float("inf")], device="cuda")
+    run(x, 2, "sigmoid", bias, 2, 1, "top2")
+    run(x[:, [4, 5, 6, 7, 0, 1, 2, 3]].contiguous(), 2, "sigmoid", bias[[4, 5, 6, 7, 0, 1, 2, 3]].contiguous(), 2, 1, "top2")
+
+
 def test_experts_that_cannot_be_chosen():
     """-inf and NaN logits, whole rows of them, +inf, and biases that exclude."""
     x = logits(9, 40)
