@@ -111,7 +111,7 @@ __device__ __forceinline__ double of_key64(long long k) { return __longlong_as_d
 
 __device__ __forceinline__ float least(float) { return -INFINITY; }
 __device__ __forceinline__ long long least(long long) { return kLeast; }
-__device__ __forceinline__ float plus(float a, float b) { return a + b; }
+__device__ __forceinline__ float plus(float a, float b) { return fmaxf(a + b, -FLT_MAX); }  // -inf stands for none
 __device__ __forceinline__ long long plus(long long a, long long b) { return key64_of(of_key64(a) + of_key64(b)); }
 
 // What a choice formed from fast fp32 scores can be off by: __expf is within (2 + 1.2 |d|) 2^-23 of its value e^-|d|, so

@@ -171,6 +171,26 @@ def test_groups_whose_two_best_cancel():
     run(x[:, [4, 5, 6, 7, 0, 1, 2, 3]].contiguous(), 2, "sigmoid", bias[[4, 5, 6, 7, 0, 1, 2, 3]].contiguous(), 2, 1, "top2")
 
 
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+def test_biases_of_the_lowest_value(score):
+    """A bias of fp32's lowest value puts an expert last without excluding it: the sum of two such choices is below fp32's range, and still above a
+    group without any choice and below one with a single such choice."""
+    x = logits(20, 16)
+    low = torch.finfo(torch.float32).min
+    for first, second in ((-float("inf"), low), (low, -float("inf"))):
+        bias = some_bias(16)
+        bias[:4], bias[4:8] = first, second
+        for group in ("top2", "max"):
+            run(x, 10, score, bias, 4, 3, group)
+            run(x, 8, score, bias, 4, 2, group)
+        one = bias.clone()
+        one[:8] = low
+        one[5:8] = -float("inf")
+        run(x, 9, score, one, 4, 3, "top2")
+    run(x, 16, score, torch.full((16,), low, device="cuda"), 4, 4, "top2")
+    run(x, 4, score, torch.full((16,), low, device="cuda"), 4, 2, "top2")
+
+
 def test_experts_that_cannot_be_chosen():
     """-inf and NaN logits, whole rows of them, +inf, and biases that exclude."""
     x = logits(9, 40)
