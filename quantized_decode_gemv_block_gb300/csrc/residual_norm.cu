@@ -128,24 +128,29 @@ __global__ void __launch_bounds__(PARTS > 2 ? 1024 : 512) residual_norm_kernel(c
     }
   }
   auto norm = [&](float (&u)[PARTS][kPart], const void* w, float (*part)[32]) {
-    float s = 0.f, eps = a.eps;
+    float s = 0.f;
 #pragma unroll
     for (int i = 0; i < PARTS; ++i)
 #pragma unroll
       for (int j = 0; j < kPart; ++j) s = __fmaf_rn(u[i][j], u[i][j], s);
     s = group_sum(s, part[0], p.group);
-    if (s == INFINITY) {  // squares past fp32: the row again at 2^-96, next to which eps is nothing
-      s = eps = 0.f;
+    float mean = s / (float)H + a.eps;
+    // Squares past fp32: the row again at 2^-96, next to which eps is nothing; below it, under an eps of as good as none: at 2^96
+    if (mean < 0x1p-100f || s == INFINITY) {
+      const bool large = s == INFINITY;
+      const float to = large ? 0x1p-96f : 0x1p96f;
+      s = 0.f;
 #pragma unroll
       for (int i = 0; i < PARTS; ++i)
 #pragma unroll
         for (int j = 0; j < kPart; ++j) {
-          u[i][j] *= 0x1p-96f;
+          u[i][j] *= to;
           s = __fmaf_rn(u[i][j], u[i][j], s);
         }
       s = group_sum(s, part[1], p.group);
+      mean = s / (float)H + (large ? 0.f : a.eps * to * to);
     }
-    const float f = rsqrtf(s / (float)H + eps);
+    const float f = rsqrtf(mean);
 #pragma unroll
     for (int i = 0; i < PARTS; ++i) {
       const int c = tid + i * p.group;

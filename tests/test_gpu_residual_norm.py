@@ -154,6 +154,31 @@ def test_rows_of_zeros_and_extreme_values():
     assert not ho[keep].isnan().any()
 
 
+@pytest.mark.parametrize("eps", [0.0, 1e-44, 1e-38, 1e-33])
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+@pytest.mark.parametrize("H", [40, 1001, 4096, 32768])
+def test_tiny_rows_under_hardly_any_eps(H, dt, eps):
+    """Rows whose squares leave fp32, down to values that are subnormal themselves, beside plain ones. eps is the fp32 number that the call takes:
+    1e-44 is none, the nearest, 7 2^-149, is 2 % below it, and under these rows eps counts in full."""
+    eps = float(np.float32(eps))
+    a = make(8, H, dt, dt)
+    for t, size in enumerate((1e-15, 1e-17, 1e-20, 1e-25, 1e-34, 1e-38, 1e-42)):
+        a["y"][t] = (a["y"][t].double() * size).to(DT[dt])
+    for b, k in ((dict(a, h=None), "y"), (dict(a, y=None, h=a["y"], post=None), "h")):
+        if dt == "bf16" and eps == 0.0:  # 1e-42 is none of bf16's numbers but 0, and 0 / 0 is what the formula gives
+            assert not b[k][6].any() and kq.residual_norm(**b, eps=eps)[1][6].isnan().all()
+            b[k] = b[k][[0, 1, 2, 3, 4, 5, 7]].contiguous()
+        run(b, eps=eps)
+
+
+def test_a_row_of_zeros_without_eps_is_nan():
+    a = make(3, 1001, "f32", "f32")
+    a["h"][1] = 0.0
+    h, x = kq.residual_norm(a["h"], None, pre=a["pre"], eps=0.0)
+    assert torch.equal(h, a["h"]) and x[1].isnan().all() and x[::2].isfinite().all()
+    assert not kq.residual_norm(a["h"], None, pre=a["pre"], eps=1e-40)[1][1].any()
+
+
 def test_eps_counts():
     a = make(4, 640)
     a["y"] *= 1e-4
