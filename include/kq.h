@@ -530,12 +530,13 @@ int kq_moe_plan(const int* ids, int T, int k, int E, int* offsets, int* order, v
  *   act      T * k rows of F bf16, 16-byte aligned (output); rows of pairs outside the plan stay as they are
  *   workspace  kq_moe_gate_up_workspace_size() bytes, 256-byte aligned (NULL where that is 0)
  * Products are exact and sums fp32, as kq_gemv's; g and u are not rounded before silu, which is formed within 2^-20 of
- * itself. A pair's bits depend on its row and expert alone, whatever else the call holds, with one exception: Q4_K
- * calls of KQ_MOE_TC_ROWS or more pairs per expert on average (T * k >= KQ_MOE_TC_ROWS * E) run on the tensor cores as
- * kq_gemm's long prompts do, where a pair's bits depend on its row and expert alone too but are not those of smaller
- * calls; 64 * dmin * m has to be below 65504 there. K is a multiple of 256 up to 20480. Q6_K needs E * 2F * row bytes to be
- * a multiple of 16. A plan outside its bounds (offsets that fall or pass T * k, pairs outside 0..T*k-1) sets bit 1 of
- * kq_device_errors(), and the experts or pairs concerned are not computed. One launch, or two on the tensor cores.
+ * itself for g >= 0 and (5 + 1.2 |g|) 2^-23 for g < 0, and is 0 from about -87 down. A pair's bits depend on its row and
+ * expert alone, whatever else the call holds, with one exception: Q4_K calls of KQ_MOE_TC_ROWS or more pairs per expert on
+ * average (T * k >= KQ_MOE_TC_ROWS * E) run on the tensor cores as kq_gemm's long prompts do, where a pair's bits depend on
+ * its row and expert alone too but are not those of smaller calls; 64 * dmin * m has to be below 65504 there. K is a
+ * multiple of 256 up to 20480. Q6_K needs E * 2F * row bytes to be a multiple of 16. A plan outside its bounds (offsets that
+ * fall or pass T * k, pairs outside 0..T*k-1) sets bit 1 of kq_device_errors(), and the experts or pairs concerned are not
+ * computed. One launch, or two on the tensor cores.
  * Errors: KQ_ERR_ARG, KQ_ERR_UNSUPPORTED, KQ_ERR_WORKSPACE, KQ_ERR_CUDA. */
 enum { KQ_MOE_TC_ROWS = 34 };
 size_t kq_moe_gate_up_workspace_size(int fmt, int T, int k, int E, int F, int K);
