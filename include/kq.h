@@ -511,7 +511,8 @@ enum { KQ_MOE_MAX_EXPERTS = 1024, KQ_MOE_MAX_CHOICES = 32, KQ_MOE_MAX_K = 20480,
  *   bias     E fp32 (device) or NULL; it takes part in the choice only
  *   ids      T x k ints: the experts, or -1 where no more can be chosen
  *   weights  T x k fp32: s of each choice, with KQ_ROUTE_RENORM divided by the sum over the token's choices
- *            (0 where that is 0), times `scale`; 0 for id -1
+ *            (0 where that is 0), times `scale`; 0 for id -1. s is formed in fp32: a sigmoid of a logit below about
+ *            -88 is 0, and a token whose choices all are gets weights of 0
  * Choices are those of 64-bit scores; without a bias they follow the logits. k <= top_group * (E / n_group),
  * n_group <= 32. One launch. Errors: KQ_ERR_ARG, KQ_ERR_UNSUPPORTED, KQ_ERR_CUDA. */
 enum kq_route_flags { KQ_ROUTE_SIGMOID = 1u, KQ_ROUTE_RENORM = 2u, KQ_ROUTE_GROUP_TOP2 = 4u };
