@@ -90,7 +90,8 @@ const char* kq_version(void);
  * Every wait inside a kernel is bounded: if one gives up, the kernel records bit 0 here,
  * skips the rest of its work (its output is then invalid) and returns instead of hanging.
  * Bit 1: a paged-cache kernel met lengths, slots or page ids outside the bounds it was given, or an
- * experts' product a plan outside them.
+ * experts' product a plan outside them. Bit 2: an experts' product on the tensor cores met Q4_K blocks whose mins
+ * are past its range.
  * Returns the bits (0 = nothing recorded) or KQ_ERR_CUDA if the word cannot be read. */
 int kq_device_errors(void);
 
@@ -534,10 +535,11 @@ int kq_moe_plan(const int* ids, int T, int k, int E, int* offsets, int* order, v
  * itself for g >= 0 and (5 + 1.2 |g|) 2^-23 for g < 0, and is 0 from about -87 down. A pair's bits depend on its row and
  * expert alone, whatever else the call holds, with one exception: Q4_K calls of KQ_MOE_TC_ROWS or more pairs per expert on
  * average (T * k >= KQ_MOE_TC_ROWS * E) run on the tensor cores as kq_gemm's long prompts do, where a pair's bits depend on
- * its row and expert alone too but are not those of smaller calls; 64 * dmin * m has to be below 65504 there. K is a
- * multiple of 256 up to 20480. Q6_K needs E * 2F * row bytes to be a multiple of 16. A plan outside its bounds (offsets that
- * fall or pass T * k, pairs outside 0..T*k-1) sets bit 1 of kq_device_errors(), and the experts or pairs concerned are not
- * computed. One launch, or two on the tensor cores.
+ * its row and expert alone too but are not those of smaller calls; 64 * dmin * m has to be below 65504 there: a larger one
+ * sets bit 2 of kq_device_errors(), and its row's results are not finite. K is a multiple of 256 up to 20480. Q6_K needs
+ * E * 2F * row bytes to be a multiple of 16. A plan outside its bounds (offsets that fall or pass T * k, pairs outside
+ * 0..T*k-1) sets bit 1 of kq_device_errors(), and the experts or pairs concerned are not computed. One launch, or two on the
+ * tensor cores.
  * Errors: KQ_ERR_ARG, KQ_ERR_UNSUPPORTED, KQ_ERR_WORKSPACE, KQ_ERR_CUDA. */
 enum { KQ_MOE_TC_ROWS = 34 };
 size_t kq_moe_gate_up_workspace_size(int fmt, int T, int k, int E, int F, int K);

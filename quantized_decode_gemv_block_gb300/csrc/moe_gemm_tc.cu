@@ -36,7 +36,7 @@ namespace cg = cooperative_groups;
 
 namespace kq {
 
-__device__ unsigned int g_moe_tc_errors = 0;  // bit 0: a bounded wait gave up; bit 1: a plan out of bounds
+__device__ unsigned int g_moe_tc_errors = 0;  // bit 0: a bounded wait gave up; bit 1: a plan out of bounds; bit 2: a min past fp16
 
 namespace {
 
@@ -203,6 +203,15 @@ __device__ __forceinline__ void min_row(const uint4& h, int j, uint8_t* tile, in
   *reinterpret_cast<uint4*>(tile + sw128_off(r, 4 * j + 1)) = make_uint4(hv[0], hv[1], hv[2], hv[3]);
   *reinterpret_cast<uint4*>(tile + sw128_off(r, 4 * j + 2)) = make_uint4(lv[0], lv[1], lv[2], lv[3]);
   *reinterpret_cast<uint4*>(tile + sw128_off(r, 4 * j + 3)) = make_uint4(0u, 0u, 0u, 0u);
+}
+
+// Whether -64 dmin m of one of a header's sub-blocks is past fp16. Out of line, and asked only where dmin is 16.25 or more: below, no m
+// of six bits gets there (asked of every header: 2048 tokens, gate | up 217 -> 223 us).
+__device__ __noinline__ bool min_past(const uint4 h) {
+  const float dmin = fabsf(half_bits_to_float(h.x >> 16));
+  uint32_t most = 0u;
+  for (int b = 0; b < 4; ++b) most = max(most, max(h.z >> 8 * b & 63u, (h.w >> (8 * b + 4) & 15u) | (h.z >> (8 * b + 2) & 48u)));
+  return !(64.f * dmin * (float)most < 65520.f);
 }
 
 // A tile: `n` rows of expert e from place `first` of the plan on, its weight rows from row_tile on; h of the rows (a multiple of 16)
@@ -491,6 +500,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTcThreads, 1)
             if ((kt & 3) == 0) *d = half_bits_to_float(head0 & 0xFFFFu);
           }
         } else {
+          uint32_t big = 0u;
+#pragma unroll
+          for (int i = 0; i < TM / 32; ++i)
+#pragma unroll
+            for (int j = 0; j < 2; ++j) big = max(big, head[j][i].x & 0x7FFF0000u);
+          if (big >= 0x4C100000u) {
+#pragma unroll
+            for (int i = 0; i < TM / 32; ++i)
+#pragma unroll
+              for (int j = 0; j < 2; ++j)
+                if (min_past(head[j][i])) atomicOr(&g_moe_tc_errors, 4u);
+          }
 #pragma unroll
           for (int i = 0; i < TM / 32; ++i)
 #pragma unroll

@@ -276,6 +276,31 @@ def test_many_rows_with_special_values():
     assert torch.equal(out[keep], clean[keep]) and out[20].isnan().all() and not out[21].isfinite().all()
 
 
+@pytest.mark.parametrize("dmin,m,bits", [(16.2, 63, 0), (20.0, 51, 0), (20.0, 52, 4), (16.25, 63, 4), (1000.0, 1, 0), (1000.0, 2, 4), (60000.0, 0, 0)])
+@pytest.mark.parametrize("at", [(0, 0, 0), (1, 130, 1), (0, 199, 2)])
+def test_many_rows_of_large_mins(dmin, m, bits, at):
+    """Mins of a block up to what 64 dmin m in fp16 allows are computed, larger ones reported; calls of few rows take them all."""
+    import oracle
+    E, H, K = 2, 200, 768
+    ids = many_ids((60, 45))
+    w, p = experts("q4_k", E, H, K)
+    block = w.view(E, H, K // 256, 144)[at]
+    block[2:4] = torch.tensor([dmin], dtype=torch.float16).view(torch.uint8).cuda()
+    block[8:12] = m  # of sub-blocks 0 to 3; 0 of 4 to 7
+    block[12:16] &= 0x0F
+    e = at[0]
+    p[e] = oracle.dequant(2, w.view(E, -1)[e].cpu().numpy(), H, K).reshape(H, K)
+    ones = torch.ones((len(ids), 1), device="cuda")
+    x = bf16(len(ids), K)
+    down("q4_k", w, p, x[:40], ids[:40], ones[:40], H)
+    assert kq.device_errors() == 0
+    if bits:
+        kq.moe_down("q4_k", w, x, kq.moe_plan(dev(ids), E), dev(ids), ones, H, K)
+    else:
+        down("q4_k", w, p, x, ids, ones, H)
+    assert kq.device_errors() == bits
+
+
 def test_many_rows_in_a_plan_out_of_bounds():
     E, F, K = 4, 64, 256
     ids = many_ids((50, 60, 70, 40))
