@@ -281,7 +281,8 @@ def head_argmax(w_q8: torch.Tensor, shortlist: torch.Tensor | None, x: torch.Ten
 
 def device_errors() -> int:
     """Read and clear the device error word (bit 0: a bounded in-kernel wait gave up; bit 1: a paged-cache
-    kernel met lengths, slots or page ids out of bounds)."""
+    kernel met lengths, slots or page ids out of bounds, or an experts' product a plan out of bounds; bit 2: an
+    experts' product on the tensor cores met Q4_K mins past its range)."""
     rc = lib().kq_device_errors()
     if rc < 0:
         _check(rc)

@@ -14,10 +14,11 @@
 // Tiles follow from the plan's offsets on the device: expert by expert, an expert's rows in equal parts of up to 256. The
 // min-term tiles (two super-blocks each, [M_hi M_hi M_lo 0] per super-block) are formed by the unpacking warps from the
 // blocks' headers and come last.
-// 2048 tokens, 8 of 128 experts: gate | up (2 x 768 x 2048) 218 us, 470 TFLOP/s, pre-pass and all; down (2048 x 768) 158 us, 325. What
-// bounds it is the unpacking: 2100 cycles for a warp's k-tile, four at a time, against 290 for the MMAs of 144 rows. On the way there:
-// raw blocks through a warp of their own and one barrier per stage 5 %, results stored without branches 8 %, roles of one thread
-// by elect 9 %.
+// 2048 tokens, 8 of 128 experts: gate | up (2 x 768 x 2048) 218 us, 470 TFLOP/s, pre-pass and all; down (2048 x 768) 159 us, 325. No
+// part alone bounds it: gate | up without the unpacking takes 187 us, without the results' stores 197, without the MMAs 207, without
+// unpacking and MMAs 174, the rest of which are the hand-overs between the roles (stage free, unpacked, both CTAs' arrival, MMA,
+// commit), the epilogue and the pre-pass. On the way there: raw blocks through a warp of their own and one barrier per stage 5 %,
+// results stored without branches 8 %, roles of one thread by elect 9 %.
 // Every wait is bounded: a timeout records the error word and raises the abort flag of both CTAs; all roles then drain
 // and return.
 #include <cooperative_groups.h>
