@@ -579,6 +579,8 @@ def attention_kv8(q: torch.Tensor, cache: KV8Cache, block_table: torch.Tensor, c
 
 KQ_NORM_POST, KQ_NORM_UNIT_OFFSET = 1, 2
 KQ_ROUTE_SIGMOID, KQ_ROUTE_RENORM, KQ_ROUTE_GROUP_TOP2 = 1, 2, 4
+KQ_MOE_MAX_EXPERTS, KQ_MOE_MAX_CHOICES, KQ_MOE_MAX_K, KQ_MOE_MAX_PAIRS = 1024, 32, 20480, 8388608
+KQ_MOE_TC_ROWS = 34  # pairs per expert on average from which on Q4_K products run on the tensor cores, and have other bits
 _SCORES = {"softmax": 0, "sigmoid": KQ_ROUTE_SIGMOID}
 _GROUP_SCORES = {"max": 0, "top2": KQ_ROUTE_GROUP_TOP2}
 

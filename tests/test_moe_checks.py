@@ -76,6 +76,18 @@ def test_product_refusals_and_sizes(kq):
         assert L.kq_moe_down_workspace_size(*bad) == 0 and L.kq_moe_gate_up_workspace_size(*bad) == 0
 
 
+def test_the_bindings_limits_are_the_headers(kq):
+    import os
+    import re
+
+    from conftest import ROOT
+    text = open(os.path.join(ROOT, "include", "kq.h")).read()
+    names = re.findall(r"\b(KQ_(?:MOE|NORM|ROUTE)_\w+) = (\d+)u?\b", text)
+    assert len(names) == 10
+    for name, value in names:
+        assert getattr(kq, name) == int(value), name
+
+
 def test_binding_refusals(kq):
     x = torch.zeros((4, 64))
     i32 = dict(dtype=torch.int32)
